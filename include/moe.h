@@ -540,6 +540,153 @@ moe_status moe_step_noalloc(const uint16_t* x, const float* logits, const float*
                             int32_t* route_src, int32_t* route_pos,
                             uint16_t* y, void* stream);
 
+/* Element type of a call's logits. */
+typedef enum {
+  MOE_DTYPE_F32 = 0,
+  MOE_DTYPE_BF16 = 1
+} moe_dtype;
+
+/* Router scores of a logit z: softmax over the token's experts, or 1 / (1 + e^-z). */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1
+} moe_score;
+
+/*
+ * moe_route_grouped — routing by scores, with a balance bias and groups.
+ *
+ * moe_route_topk's bias is part of the softmax and its weights always sum to
+ * one.  This call is the rule of routers that are balanced by a bias which
+ * only the selection sees, and that confine a token to a few groups of
+ * experts (the experts of one device, say).  Per token, with E / groups
+ * consecutive experts to a group:
+ *   s_e = score of logits[t,e];  c_e = s_e + bias[e] (c = s without bias);
+ *   a group's value is the sum of its group_top largest c (1 or 2);
+ *   the groups_kept groups of largest value are kept, and of their experts
+ *   the k of largest c are chosen, in that order;
+ *   topk_w[t,j] = scale * s_j, divided by the sum of the chosen s where
+ *   renormalise is not 0 (0 where that sum is 0).
+ * Equal values go to the lower id, of groups and of experts.  Scores, choice
+ * values and sums are computed in fp64 and the weights rounded once to fp32.
+ *
+ * Masks: an expert is masked where its logit or its bias is NaN or at or
+ * below -3.3e38 (so -inf and the lowest value of fp32 and of bf16).  Masked
+ * logits have score 0 and no part in a softmax; masked experts count in no
+ * group's value; a group with none left has the lowest value.  Where fewer
+ * than k experts are left in the kept groups, the remaining slots hold those
+ * groups' masked experts, lowest id first, with weight 0: every row of
+ * topk_idx holds k different ids of [0, E), fit for moe_bucket_routes and
+ * moe_expert_ffn.  Logits of +inf count as the largest float.
+ *
+ *   logits       [T, E] logits_type (a moe_dtype)  in
+ *   bias         [E] fp32 or NULL                  in
+ *   score        a moe_score
+ *   topk_idx     [T, k] int32                      out
+ *   topk_w       [T, k] fp32                       out
+ * Shapes: T >= 0 (T = 0 launches nothing), 1 <= k <= groups_kept * E / groups,
+ * groups divides E, 1 <= groups_kept <= groups, group_top 1 or 2, scale
+ * finite (else MOE_ERR_INVALID_SHAPE).  Envelope: E <= 1024, k <= 32,
+ * groups <= 64, T*k <= 2^24, and at most 16 experts for each of the lanes a
+ * group has, 64 / (groups rounded up to a power of two): always so where
+ * groups is a power of two (else MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_route_grouped(const void* logits, int logits_type, const float* bias,
+                             int T, int E, int k, int score,
+                             int groups, int groups_kept, int group_top,
+                             int renormalise, float scale,
+                             int32_t* topk_idx, float* topk_w, void* stream);
+
+/*
+ * moe_route_grouped_bucket — moe_route_grouped followed by moe_bucket_routes:
+ * the arguments, outputs, envelope and errors of the two, every check before
+ * any launch, outputs bit for bit those of the two calls.
+ */
+moe_status moe_route_grouped_bucket(const void* logits, int logits_type, const float* bias,
+                                    int T, int E, int k, int score,
+                                    int groups, int groups_kept, int group_top,
+                                    int renormalise, float scale,
+                                    int32_t* topk_idx, float* topk_w,
+                                    int32_t* expert_count, int32_t* expert_offset,
+                                    int32_t* active_experts, int32_t* n_active,
+                                    int32_t* route_src, int32_t* route_pos,
+                                    void* stream);
+
+/*
+ * Formats of a dense 4-bit matrix [N, K]: e2m1 codes packed two per byte
+ * (element 2i in the low nibble of byte i, [N, K/2]) and scales along K.
+ *   MOE_QUANT_NVFP4  an e4m3 (OCP E4M3FN) scale per 16 weights, [N, K/16],
+ *                    and one fp32 global scale: the experts' format
+ *   MOE_QUANT_MXFP4  an e8m0 scale 2^(byte - 127) per 32 weights, [N, K/32];
+ *                    the global scale may be NULL (1)
+ * Scale bytes are not NaN, and not negative (precondition); e8m0 bytes lie
+ * in 2 .. 252 (2^-125 .. 2^125), so that every weight is a finite normal
+ * bf16 value or zero.
+ */
+typedef enum {
+  MOE_QUANT_NVFP4 = 0,
+  MOE_QUANT_MXFP4 = 1
+} moe_quant_format;
+
+/*
+ * moe_quant_linear — a dense layer with 4-bit weights and bf16 activations.
+ *
+ * Defines y[t,n] = bf16( g * sum_k x[t,k] * W[n,k] + bias[n] ): the weights
+ * are used at their exact values, the sum is fp32 in a fixed order, and y is
+ * rounded once (RNE).
+ *   format    a moe_quant_format
+ *   x         [T, K] bf16 bits       in
+ *   codes     [N, K/2] uint8         in
+ *   scales    [N, K/16] or [N, K/32] in
+ *   g_scale   [1] fp32 (4-byte aligned)  in   required for NVFP4
+ *   bias      [N] bf16 bits or NULL  in
+ *   y         [T, N] bf16 bits       out  overlaps no input
+ * Shapes: T >= 0 (T = 0 launches nothing), N >= 1 (any), K a multiple of 32
+ * (else MOE_ERR_INVALID_SHAPE).  Envelope: N and T up to 2^20, K up to 2^15
+ * (else MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_quant_linear(int format, const uint16_t* x,
+                            const uint8_t* codes, const uint8_t* scales, const float* g_scale,
+                            const uint16_t* bias, int T, int N, int K,
+                            uint16_t* y, void* stream);
+
+/*
+ * Bytes of device workspace moe_quant_shared_expert needs (0 when T <= 0):
+ * h (bf16 [T, Is]) and the token gates (fp32 [T]), each rounded up to 256.
+ */
+size_t moe_quant_shared_expert_workspace_size(int T, int H, int Is);
+
+/*
+ * moe_quant_shared_expert — the shared expert of every token with 4-bit
+ * weights, gated per token and summed onto the routed output.
+ *
+ * Defines h[t] = bf16( SiLU(W_gate x_t) * (W_up x_t) ) and
+ *   y[t] = bf16( add[t] + sigmoid(x_t . token_gate) * (W_down h_t) ),
+ * without the factor where token_gate is NULL and without the term where add
+ * is NULL.  Sums are fp32 in a fixed order; h is kept as bf16 between the
+ * two products, as in moe_shared_expert and moe_expert_ffn; y is rounded
+ * once.
+ *   format       a moe_quant_format, of the three matrices
+ *   x            [T, H] bf16 bits            in
+ *   gate_*, up_* the matrices [Is, H], down_* the matrix [H, Is] (codes,
+ *                scales, global scale as in moe_quant_linear)   in
+ *   token_gate   [H] bf16 bits or NULL       in
+ *   add          [T, H] bf16 bits or NULL    in   may be y itself
+ *   workspace    >= moe_quant_shared_expert_workspace_size(T, H, Is) bytes,
+ *                owned by the caller; contents unspecified, never needs a
+ *                reset
+ *   y            [T, H] bf16 bits            out  overlaps no other input
+ * Shapes: T >= 0 (T = 0 launches nothing), H and Is multiples of 32.
+ * Envelope: H and Is up to 2^15, T up to 2^20 (else MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_quant_shared_expert(int format, const uint16_t* x,
+                                   const uint8_t* gate_codes, const uint8_t* gate_scales, const float* gate_g,
+                                   const uint8_t* up_codes, const uint8_t* up_scales, const float* up_g,
+                                   const uint8_t* down_codes, const uint8_t* down_scales, const float* down_g,
+                                   const uint16_t* token_gate, const uint16_t* add,
+                                   int T, int H, int Is,
+                                   void* workspace, size_t workspace_bytes,
+                                   uint16_t* y, void* stream);
+
 /* Static English description of a status code (never NULL). */
 const char* moe_status_string(moe_status s);
 

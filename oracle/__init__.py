@@ -13,6 +13,8 @@ What it computes (one routed-MoE step of a decode/verify batch):
   moe_output      per route: SiLU(W_gate x) * (W_up x), then W_down; weighted
                   sum over each token's k routes in slot order
   shared_expert_output  the dense BF16 shared expert for every token
+  route_grouped   routing by scores, with a balance bias and groups
+  quant_linear, quant_shared_expert  dense products with 4-bit weights
 
 Sources: the routing rule of the fused MoE routing kernel (page "How I forked
 vLLM and made Qwen3.8-Flash-Next decode 1.6x faster on one GPU", section
@@ -37,8 +39,13 @@ from .router import router_logits
 from .buckets import bucket_routes
 from .ffn import expert_route_output, moe_output, ExpertDecoder
 from .shared import shared_expert_output
+from .grouped import route_grouped
+from .quant import quant_linear, quant_shared_expert
 
 __all__ = [
+    "route_grouped",
+    "quant_linear",
+    "quant_shared_expert",
     "shared_expert_output",
     "E2M1_VALUES",
     "e4m3_table",

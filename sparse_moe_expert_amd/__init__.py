@@ -4,6 +4,10 @@ A C-ABI HIP library (include/moe.h) with three calls per routed-MoE step:
 moe_route_topk -> moe_bucket_routes -> moe_expert_ffn (or the whole step in
 one call, moe_step), bound here for torch tensors.  PyTorch provides device memory and the stream; the kernels are the
 library's own.
+
+Around the routed experts: moe_route_grouped(_bucket) routes by scores with a
+balance bias and groups, moe_quant_linear is a dense layer with 4-bit weights,
+moe_quant_shared_expert the shared expert with 4-bit weights.
 """
 
 from ._lib import (
@@ -33,6 +37,16 @@ from ._lib import (
     NOALLOC_SCRATCH_BYTES,
     pack_weights,
 )
+from .layer import (
+    QuantWeight,
+    RouteRule,
+    make_quant_shared_workspace,
+    moe_quant_linear,
+    moe_quant_shared_expert,
+    moe_quant_shared_expert_workspace_size,
+    moe_route_grouped,
+    moe_route_grouped_bucket,
+)
 from .step import MoeStep, expert_weights_from_numpy
 
 __all__ = [
@@ -61,6 +75,14 @@ __all__ = [
     "moe_step_workspace_size",
     "NOALLOC_SCRATCH_BYTES",
     "pack_weights",
+    "QuantWeight",
+    "RouteRule",
+    "make_quant_shared_workspace",
+    "moe_quant_linear",
+    "moe_quant_shared_expert",
+    "moe_quant_shared_expert_workspace_size",
+    "moe_route_grouped",
+    "moe_route_grouped_bucket",
     "MoeStep",
     "expert_weights_from_numpy",
 ]

@@ -1,6 +1,6 @@
 """Build the HIP library libsparse_moe_expert_amd.so in-tree for gfx950.
 
-Every csrc/*.hip file is compiled separately (in parallel) with hipcc and the
+Every csrc/*.hip and csrc/layer/*.hip file is compiled separately (in parallel) with hipcc and the
 objects are linked into one shared library next to this file.  Packed fp32
 VALU instructions are disabled for all device code.
 
@@ -49,7 +49,7 @@ def _run(cmd):
 def build_library(verbose: bool = False, jobs: int = 8) -> str:
     """Compile all HIP sources and link the shared library; returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    sources = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+    sources = sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "layer", "*.hip")))
     if not sources:
         raise RuntimeError(f"no HIP sources under {CSRC}")
 

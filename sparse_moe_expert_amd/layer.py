@@ -1,0 +1,205 @@
+"""Binding of the operators around the routed experts: grouped routing, dense
+products with 4-bit weights and the 4-bit shared expert (argument marshalling
+only, as in _lib).
+
+These calls are a few microseconds of GPU work each, so what does not change
+from call to call is checked once: a RouteRule and a QuantWeight check
+themselves when they are made, and a call checks its own tensors.
+"""
+
+from __future__ import annotations
+
+import contextlib
+from typing import Optional
+
+import torch
+
+from ._lib import Buckets, _check, _need, empty_buckets, load_library
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}        # moe_dtype
+_SCORES = {"softmax": 0, "sigmoid": 1}                 # moe_score
+_FORMATS = {"nvfp4": (0, 16), "mxfp4": (1, 32)}        # moe_quant_format, weights per scale
+
+_here = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """The library launches on the current device: make it the tensors' one."""
+    return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _tensor(t: torch.Tensor, name: str, dtype, shape, device):
+    """_need's checks, with the passing case in one expression."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape, device)
+
+
+class RouteRule:
+    """How moe_route_grouped selects: k experts by `score` ("softmax" or
+    "sigmoid") plus the bias, from the `groups_kept` best of `groups` groups (a
+    group's value: the sum of its `group_top` best), weights renormalised over
+    the chosen experts or not, times `scale`."""
+
+    __slots__ = ("k", "score", "groups", "groups_kept", "group_top", "renormalise", "scale", "_args")
+
+    def __init__(self, k: int, score: str = "sigmoid", groups: int = 1, groups_kept: Optional[int] = None,
+                 group_top: int = 2, renormalise: bool = True, scale: float = 1.0):
+        if score not in _SCORES:
+            raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
+        self.k, self.score, self.groups = int(k), score, int(groups)
+        self.groups_kept = self.groups if groups_kept is None else int(groups_kept)
+        self.group_top, self.renormalise, self.scale = int(group_top), bool(renormalise), float(scale)
+        self._args = (_SCORES[score], self.groups, self.groups_kept, self.group_top, int(self.renormalise), self.scale)
+
+
+def _route_args(logits, bias, rule, topk_idx, topk_w):
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise TypeError("logits must be a [T, E] tensor")
+    if logits.dtype not in _DTYPES:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    (T, E), k, dev = logits.shape, rule.k, logits.device
+    _tensor(logits, "logits", logits.dtype, (T, E), dev)
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    if bias is not None:
+        _tensor(bias, "bias", torch.float32, (E,), dev)
+    if topk_idx is None:
+        topk_idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    _tensor(topk_idx, "topk_idx", torch.int32, (T, k), dev)
+    _tensor(topk_w, "topk_w", torch.float32, (T, k), dev)
+    args = (logits.data_ptr(), _DTYPES[logits.dtype], None if bias is None else bias.data_ptr(), T, E, k, *rule._args,
+            topk_idx.data_ptr(), topk_w.data_ptr())
+    return args, T, E, k, dev, topk_idx, topk_w
+
+
+def moe_route_grouped(logits: torch.Tensor, bias: Optional[torch.Tensor], rule: RouteRule,
+                      topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None):
+    """Expert ids (int32 [T,k]) and gate weights (fp32 [T,k]) of fp32 or bf16
+    logits [T,E] by a RouteRule; `bias` (fp32 [E]) counts in the selection only."""
+    args, _, _, _, dev, topk_idx, topk_w = _route_args(logits, bias, rule, topk_idx, topk_w)
+    with _on(dev):
+        _check("moe_route_grouped", load_library().moe_route_grouped(*args, _stream(dev)))
+    return topk_idx, topk_w
+
+
+def moe_route_grouped_bucket(logits: torch.Tensor, bias: Optional[torch.Tensor], rule: RouteRule,
+                             topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                             out: Optional[Buckets] = None):
+    """moe_route_grouped and moe_bucket_routes in one call: ids, weights, buckets."""
+    args, T, E, k, dev, topk_idx, topk_w = _route_args(logits, bias, rule, topk_idx, topk_w)
+    b = out if out is not None else empty_buckets(T, E, max(k, 0), dev)
+    for name, t, n in zip(Buckets._fields, b, (E, E + 1, E, 1, T * k, T * k)):
+        _tensor(t, name, torch.int32, (n,), dev)
+    with _on(dev):
+        _check("moe_route_grouped_bucket",
+               load_library().moe_route_grouped_bucket(*args, *(t.data_ptr() for t in b), _stream(dev)))
+    return topk_idx, topk_w, b
+
+
+class QuantWeight:
+    """A dense 4-bit matrix [N, K] on the device: `codes` uint8 [N, K/2],
+    `scales` uint8 [N, K/16] ("nvfp4") or [N, K/32] ("mxfp4") and the global
+    scale, fp32 [1] (None: 1, "mxfp4" only)."""
+
+    __slots__ = ("codes", "scales", "g_scale", "format", "N", "K", "device", "_format")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, g_scale: Optional[torch.Tensor] = None,
+                 format: str = "nvfp4"):
+        if format not in _FORMATS:
+            raise ValueError(f"format must be one of {tuple(_FORMATS)}, got {format!r}")
+        self._format, group = _FORMATS[format]
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+            raise TypeError("codes must be a [N, K/2] tensor")
+        self.N, self.K, self.device = codes.shape[0], 2 * codes.shape[1], codes.device
+        if self.K % 32 != 0 or self.K == 0 or self.N == 0:
+            raise ValueError(f"a 4-bit matrix needs N >= 1 and K a multiple of 32, got N={self.N}, K={self.K}")
+        _need(codes, "codes", torch.uint8, None, self.device)
+        _need(scales, "scales", torch.uint8, (self.N, self.K // group), self.device)
+        if g_scale is not None:
+            _need(g_scale, "g_scale", torch.float32, (1,), self.device)
+        elif format == "nvfp4":
+            raise ValueError("nvfp4 weights need their global scale (g_scale)")
+        self.codes, self.scales, self.g_scale, self.format = codes, scales, g_scale, format
+
+    @property
+    def shape(self):
+        return self.N, self.K
+
+    def _ptrs(self):
+        g = self.g_scale
+        return self.codes.data_ptr(), self.scales.data_ptr(), None if g is None else g.data_ptr()
+
+
+def _check_quant_x(x, weight: QuantWeight):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a [T, K] tensor")
+    _tensor(x, "x", torch.bfloat16, (x.shape[0], weight.K), weight.device)
+    return x.shape[0]
+
+
+def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.Tensor] = None,
+                     y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """bf16 y [T,N] = x W^T + bias for bf16 x [T,K], a QuantWeight [N,K] and an
+    optional bf16 bias [N]."""
+    T, N, dev = _check_quant_x(x, weight), weight.N, weight.device
+    if bias is not None:
+        _tensor(bias, "bias", torch.bfloat16, (N,), dev)
+    if y is None:
+        y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _tensor(y, "y", torch.bfloat16, (T, N), dev)
+    with _on(dev):
+        _check("moe_quant_linear", load_library().moe_quant_linear(
+            weight._format, x.data_ptr(), *weight._ptrs(), None if bias is None else bias.data_ptr(), T, N, weight.K,
+            y.data_ptr(), _stream(dev)))
+    return y
+
+
+def moe_quant_shared_expert_workspace_size(T: int, H: int, Is: int) -> int:
+    return int(load_library().moe_quant_shared_expert_workspace_size(T, H, Is))
+
+
+def make_quant_shared_workspace(T: int, H: int, Is: int, device) -> torch.Tensor:
+    """Workspace of the size moe_quant_shared_expert needs (reusable across calls)."""
+    return torch.empty((max(moe_quant_shared_expert_workspace_size(T, H, Is), 256),), dtype=torch.uint8, device=device)
+
+
+def moe_quant_shared_expert(x: torch.Tensor, gate: QuantWeight, up: QuantWeight, down: QuantWeight,
+                            token_gate: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                            y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The 4-bit shared expert: bf16 y [T,H] = add + sigmoid(x . token_gate) *
+    W_down (SiLU(W_gate x) * (W_up x)), gate/up [Is,H] and down [H,Is] of one
+    format; `token_gate` (bf16 [H]) and `add` (bf16 [T,H], may be y) optional."""
+    T, H, Is, dev = _check_quant_x(x, gate), gate.K, gate.N, gate.device
+    if up.shape != (Is, H) or down.shape != (H, Is):
+        raise ValueError(f"gate is {gate.shape}, up {up.shape}, down {down.shape}: up must be gate's shape, down its "
+                         "transpose's")
+    if not (gate._format == up._format == down._format):
+        raise ValueError("gate, up and down must have one format")
+    if not (up.device == dev and down.device == dev):
+        raise ValueError(f"gate is on {dev}, up on {up.device}, down on {down.device}")
+    if token_gate is not None:
+        _tensor(token_gate, "token_gate", torch.bfloat16, (H,), dev)
+    if add is not None:
+        _tensor(add, "add", torch.bfloat16, (T, H), dev)
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    else:
+        _tensor(y, "y", torch.bfloat16, (T, H), dev)
+    if workspace is None:
+        workspace = make_quant_shared_workspace(T, H, Is, dev)
+    else:
+        _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    with _on(dev):
+        _check("moe_quant_shared_expert", load_library().moe_quant_shared_expert(
+            gate._format, x.data_ptr(), *gate._ptrs(), *up._ptrs(), *down._ptrs(),
+            None if token_gate is None else token_gate.data_ptr(), None if add is None else add.data_ptr(),
+            T, H, Is, workspace.data_ptr(), workspace.numel(), y.data_ptr(), _stream(dev)))
+    return y
