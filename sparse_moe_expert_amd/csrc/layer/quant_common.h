@@ -9,11 +9,6 @@
 #include "row_dot.h"
 
 namespace moe {
-namespace {
-
-// weights that share a scale
-template <int FMT>
-constexpr int kScaleGroup = FMT == MOE_QUANT_NVFP4 ? 16 : 32;
 
 // A 4-bit matrix [N, K]
 struct QuantMat {
@@ -22,17 +17,126 @@ struct QuantMat {
   const float* g;          // global scale, or null for 1
 };
 
-// One block scale as fp32 (exact)
+// y[t,n] = bf16( add[t,n] + gate[t] * (x_t . a_n + bias[n]) ), or for a
+// gate/up pair y[t,n] = bf16( SiLU(x_t . a_n) * (x_t . b_n) ); a null bias,
+// gate or add leaves its term out.  With `token_gate` the launch also fills
+// gate_out[t] = sigmoid(x_t . token_gate).
+struct DenseArgs {
+  const uint16_t* x;
+  QuantMat a, b;
+  const uint16_t* bias;
+  const float* gate;
+  const uint16_t* add;
+  uint16_t* y;
+  int T, N, K;
+  const uint16_t* token_gate;
+  float* gate_out;
+};
+
+// The products' kernels; `gate_up`: the pair a, b.  Arguments already checked.
+moe_status quant_stream(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// weights that share a scale
 template <int FMT>
-__device__ __forceinline__ float block_scale(uint32_t byte) {
-  if constexpr (FMT == MOE_QUANT_NVFP4) return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
-  // 2^-127 is subnormal in fp32
-  return byte == 0 ? 5.877471754e-39f : __uint_as_float(byte << 23);
+constexpr int kScaleGroup = FMT == MOE_QUANT_NVFP4 ? 16 : 32;
+
+// Two e2m1 codes (byte B of `word`) times `scale`, as two bf16.  Exact: e2m1
+// has 2 significant bits and e4m3 has 4, a bf16 holds 8.  The conversion's
+// own scale operand takes powers of two only, which MXFP4's scales are.
+template <int FMT, int B>
+__device__ __forceinline__ uint32_t fp4x2_scaled(uint32_t word, float scale) {
+  if constexpr (FMT == MOE_QUANT_MXFP4) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, B));
+  } else {
+    const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, B);
+    const bf16x2 r = {(__bf16)(v.x * scale), (__bf16)(v.y * scale)};
+    return __builtin_bit_cast(uint32_t, r);
+  }
+}
+
+// 32 weights (16 code bytes and their scale bytes: two e4m3, or one e8m0) ->
+// four fragments of 8 bf16.
+template <int FMT>
+__device__ __forceinline__ void dequant32(const uint4 codes, uint32_t sb, bf16x8 (&fr)[4]) {
+  float s0, s1;
+  if constexpr (FMT == MOE_QUANT_NVFP4) {
+    s0 = __builtin_amdgcn_cvt_f32_fp8((int)sb, 0);
+    s1 = __builtin_amdgcn_cvt_f32_fp8((int)sb, 1);
+  } else {
+    s0 = s1 = __uint_as_float(sb << 23);
+  }
+  const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float s = i < 2 ? s0 : s1;
+    const uint4 v = make_uint4(fp4x2_scaled<FMT, 0>(c[i], s), fp4x2_scaled<FMT, 1>(c[i], s),
+                               fp4x2_scaled<FMT, 2>(c[i], s), fp4x2_scaled<FMT, 3>(c[i], s));
+    fr[i] = __builtin_bit_cast(bf16x8, v);
+  }
 }
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t bits) { return __uint_as_float(bits << 16); }
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
+
+// sigmoid(x_t . token_gate) of token t, by one wavefront
+__device__ __forceinline__ void token_gate_row(const DenseArgs& p, int t, int lane) {
+  float acc = 0.0f;
+  const uint4* const xr = reinterpret_cast<const uint4*>(p.x + (size_t)t * p.K);
+  const uint4* const vr = reinterpret_cast<const uint4*>(p.token_gate);
+  for (int c = lane; c < p.K / 8; c += kWave) {
+    const uint4 a = xr[c], b = vr[c];
+    acc = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(a.x), as_bf16x2(b.x), acc, false);
+    acc = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(a.y), as_bf16x2(b.y), acc, false);
+    acc = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(a.z), as_bf16x2(b.z), acc, false);
+    acc = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(a.w), as_bf16x2(b.w), acc, false);
+  }
+  acc = group_sum(acc, kWave);
+  if (lane == 0) p.gate_out[t] = sigmoid(acc);
+}
+
+// y[t, n .. n+3] from four sums (and for a gate/up pair four more), rows at
+// or past N left alone.
+template <bool GU>
+__device__ __forceinline__ void write4(const DenseArgs& p, int t, int n, f32x4 a, f32x4 b, float ga, float gb) {
+  float v[4];
+  const float gate = !GU && p.gate ? p.gate[t] : 1.0f;
+  uint16_t* const out = p.y + (size_t)t * p.N + n;
+  const uint16_t* const add = !GU && p.add ? p.add + (size_t)t * p.N + n : nullptr;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = a[j] * ga;
+    if constexpr (GU) {
+      v[j] = silu(v[j]) * (b[j] * gb);
+    } else if (n + j < p.N) {
+      if (p.bias) v[j] += bf16_to_f32(p.bias[n + j]);
+      v[j] *= gate;
+      if (add) v[j] += bf16_to_f32(add[j]);
+    }
+  }
+  if (p.N % 4 == 0) {                          // 8-byte aligned, and whole fours
+    if (n < p.N)
+      *reinterpret_cast<uint2*>(out) = make_uint2(f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
+                                                  f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < p.N) out[j] = (uint16_t)f32_to_bf16_rne(v[j]);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 }  // namespace
 
