@@ -8,6 +8,8 @@
 
 #include "row_dot.h"
 
+#include <type_traits>
+
 namespace moe {
 
 // A 4-bit matrix [N, K]
@@ -34,6 +36,9 @@ struct DenseArgs {
 };
 
 // The products' kernels; `gate_up`: the pair a, b.  Arguments already checked.
+// quant_few takes what quant_few_ok says, quant_stream anything.
+bool quant_few_ok(const DenseArgs& p);
+moe_status quant_few(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
 moe_status quant_stream(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
 
 namespace {
@@ -101,40 +106,78 @@ __device__ __forceinline__ void token_gate_row(const DenseArgs& p, int t, int la
   if (lane == 0) p.gate_out[t] = sigmoid(acc);
 }
 
-// y[t, n .. n+3] from four sums (and for a gate/up pair four more), rows at
-// or past N left alone.
+// One output from its sum (and for a gate/up pair the other's)
 template <bool GU>
-__device__ __forceinline__ void write4(const DenseArgs& p, int t, int n, f32x4 a, f32x4 b, float ga, float gb) {
-  float v[4];
-  const float gate = !GU && p.gate ? p.gate[t] : 1.0f;
-  uint16_t* const out = p.y + (size_t)t * p.N + n;
-  const uint16_t* const add = !GU && p.add ? p.add + (size_t)t * p.N + n : nullptr;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[j] = a[j] * ga;
-    if constexpr (GU) {
-      v[j] = silu(v[j]) * (b[j] * gb);
-    } else if (n + j < p.N) {
-      if (p.bias) v[j] += bf16_to_f32(p.bias[n + j]);
-      v[j] *= gate;
-      if (add) v[j] += bf16_to_f32(add[j]);
-    }
+__device__ __forceinline__ float output(const DenseArgs& p, int t, int n, float a, float b) {
+  a = p.a.g ? a * *p.a.g : a;
+  if constexpr (GU) {
+    b = p.b.g ? b * *p.b.g : b;
+    return silu(a) * b;
+  } else {
+    if (p.bias) a += bf16_to_f32(p.bias[n]);
+    if (p.gate) a *= p.gate[t];
+    if (p.add) a += bf16_to_f32(p.add[(size_t)t * p.N + n]);
+    return a;
   }
+}
+
+template <bool GU>
+__device__ __forceinline__ void write1(const DenseArgs& p, int t, int n, float a, float b) {
+  p.y[(size_t)t * p.N + n] = (uint16_t)f32_to_bf16_rne(output<GU>(p, t, n, a, b));
+}
+
+// y[t, n .. n+3], rows at or past N left alone.
+template <bool GU>
+__device__ __forceinline__ void write4(const DenseArgs& p, int t, int n, f32x4 a, f32x4 b) {
   if (p.N % 4 == 0) {                          // 8-byte aligned, and whole fours
-    if (n < p.N)
-      *reinterpret_cast<uint2*>(out) = make_uint2(f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
-                                                  f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16));
+    if (n >= p.N) return;
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = f32_to_bf16_rne(output<GU>(p, t, n + j, a[j], b[j]));
+    *reinterpret_cast<uint2*>(p.y + (size_t)t * p.N + n) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (n + j < p.N) out[j] = (uint16_t)f32_to_bf16_rne(v[j]);
+      if (n + j < p.N) write1<GU>(p, t, n + j, a[j], b[j]);
   }
 }
+
+__device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+
+// s_waitcnt vmcnt(N), and as the compiler's own, which then does not wait
+// for what came before once more
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "six bits");
+  fence();
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+  fence();
+}
+
+// f(integral_constant 0 .. N-1), unrolled
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void for_each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    for_each<N, I + 1>(f);
+  }
+}
+
+// Workgroup barrier without the fence of __syncthreads(), which would wait
+// for every load in flight.
+__device__ __forceinline__ void barrier() {
+  fence();
+  __builtin_amdgcn_s_barrier();
+  fence();
+}
+
+// A buffer offset beyond every resource of these kernels
+constexpr uint32_t kOutside = 0x60000000u;
 
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 

@@ -9,6 +9,10 @@
 namespace moe {
 namespace {
 
+moe_status quant_product(int format, bool gate_up, const DenseArgs& p, hipStream_t s) {
+  return quant_few_ok(p) ? quant_few(format, gate_up, p, s) : quant_stream(format, gate_up, p, s);
+}
+
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 }  // namespace
@@ -26,7 +30,7 @@ extern "C" moe_status moe_quant_linear(int format, const uint16_t* x, const uint
       !aligned4(g_scale))
     return MOE_ERR_MISALIGNED;
   const DenseArgs p{x, {codes, scales, g_scale}, {}, bias, nullptr, nullptr, y, T, N, K, nullptr, nullptr};
-  return quant_stream(format, false, p, static_cast<hipStream_t>(stream));
+  return quant_product(format, false, p, static_cast<hipStream_t>(stream));
 }
 
 extern "C" size_t moe_quant_shared_expert_workspace_size(int T, int H, int Is) {
@@ -61,8 +65,8 @@ extern "C" moe_status moe_quant_shared_expert(int format, const uint16_t* x, con
                                                             align256((size_t)T * (size_t)Is * 2)) : nullptr;
   const DenseArgs up{x, {gate_codes, gate_scales, gate_g}, {up_codes, up_scales, up_g}, nullptr, nullptr, nullptr,
                      h, T, Is, H, token_gate, gate};
-  const moe_status st = quant_stream(format, true, up, s);
+  const moe_status st = quant_product(format, true, up, s);
   if (st != MOE_OK) return st;
   const DenseArgs down{h, {down_codes, down_scales, down_g}, {}, nullptr, gate, add, y, T, H, Is, nullptr, nullptr};
-  return quant_stream(format, false, down, s);
+  return quant_product(format, false, down, s);
 }

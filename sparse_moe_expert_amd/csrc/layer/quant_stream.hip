@@ -31,10 +31,6 @@
 namespace moe {
 namespace {
 
-__device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
-
-constexpr uint32_t kOutside = 0x60000000u;     // beyond every resource here
-
 template <int FMT, bool GU, int R, int TT, int WAVES, int NS>
 struct StreamTile {
   static constexpr int NA = (GU ? 2 : 1) * R;                // A operands: R row tiles of each matrix
@@ -141,15 +137,20 @@ __global__ __launch_bounds__(WAVES * kWave) void quant_stream_kernel(DenseArgs p
     bf16x8 af[NA][4];
 #pragma unroll
     for (int a = 0; a < NA; ++a) dequant32<FMT>(tl.wc[G][a], tl.ws[G][a], af[a]);
-    const int left = p.K - (first + s) * 128;                // K is a multiple of 32: whole lane quarters
+    uint8_t* const xs = (G == 0 ? s_x0 : G == 1 ? s_x1 : G == 2 ? s_x2 : s_x3) + wave * Tile::kWaveBytes;
+    const int left = p.K - (first + s) * 128;
+    if (left < 128) {                                        // what follows a token's row is not its
+#pragma unroll
+      for (int j = 0; j < Tile::XL; ++j)
+        if ((l16 ^ ((j * 4 + q) & 15)) * 8 >= left) *reinterpret_cast<uint4*>(xs + j * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int row = TT < 16 ? min(l16, TT - 1) : t * 16 + l16;
-      const uint8_t* const xr = (G == 0 ? s_x0 : G == 1 ? s_x1 : G == 2 ? s_x2 : s_x3) + wave * Tile::kWaveBytes + row * 256;
+      const uint8_t* const xr = xs + row * 256;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        bf16x8 b = *reinterpret_cast<const bf16x8*>(xr + (((q * 4 + i) ^ (row & 15)) << 4));
-        if (left < 128 && q * 32 >= left) b = bf16x8{};      // what follows the row is not its
+        const bf16x8 b = *reinterpret_cast<const bf16x8*>(xr + (((q * 4 + i) ^ (row & 15)) << 4));
 #pragma unroll
         for (int a = 0; a < NA; ++a) acc[a][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[a][i], b, acc[a][t], 0, 0, 0);
       }
@@ -176,7 +177,6 @@ __global__ __launch_bounds__(WAVES * kWave) void quant_stream_kernel(DenseArgs p
 #pragma unroll
     for (int t = 0; t < NT; ++t) red[((wave * NA + a) * NT + t) * kWave + lane] = acc[a][t];
   __syncthreads();
-  const float ga = p.a.g ? *p.a.g : 1.0f, gb = GU && p.b.g ? *p.b.g : 1.0f;
   for (int i = threadIdx.x; i < R * NT * kWave; i += WAVES * kWave) {
     const int r = i / (NT * kWave), rest = i % (NT * kWave);  // row tile; token tile and lane
     const int t = t0 + (rest >> 6) * 16 + (rest & 15), n = n0 + r * 16 + ((rest >> 4) & 3) * 4;
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(WAVES * kWave) void quant_stream_kernel(DenseArgs p
       va += red[(w * NA + r) * NT * kWave + rest];
       if constexpr (GU) vb += red[(w * NA + R + r) * NT * kWave + rest];
     }
-    write4<GU>(p, t, n, va, vb, ga, gb);
+    write4<GU>(p, t, n, va, vb);
   }
 }
 
@@ -202,7 +202,6 @@ moe_status launch(const DenseArgs& p, hipStream_t s) {
 
 template <int FMT, bool GU>
 moe_status dispatch(const DenseArgs& p, hipStream_t s) {
-  if (p.T <= 4) return launch<FMT, GU, 1, 4, 8, 4>(p, s);
   if (p.T <= 16) return launch<FMT, GU, 1, 16, 4, 3>(p, s);
   if (p.T <= 32) return launch<FMT, GU, 2, 32, 4, 2>(p, s);
   return launch<FMT, GU, 2, 64, 4, 2>(p, s);
