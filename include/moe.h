@@ -628,6 +628,13 @@ typedef enum {
 } moe_quant_format;
 
 /*
+ * Bytes of device workspace moe_quant_linear needs: 0 for up to four tokens
+ * and for batches whose output tiles fill the chip; else the fp32 sums of the
+ * parts that the reduction is split into.
+ */
+size_t moe_quant_linear_workspace_size(int T, int N, int K);
+
+/*
  * moe_quant_linear — a dense layer with 4-bit weights and bf16 activations.
  *
  * Defines y[t,n] = bf16( g * sum_k x[t,k] * W[n,k] + bias[n] ): the weights
@@ -639,6 +646,9 @@ typedef enum {
  *   scales    [N, K/16] or [N, K/32] in
  *   g_scale   [1] fp32 (4-byte aligned)  in   required for NVFP4
  *   bias      [N] bf16 bits or NULL  in
+ *   workspace >= moe_quant_linear_workspace_size(T, N, K) bytes, owned by the
+ *             caller (NULL where that is 0); contents unspecified, never
+ *             needs a reset
  *   y         [T, N] bf16 bits       out  overlaps no input
  * Shapes: T >= 0 (T = 0 launches nothing), N >= 1 (any), K a multiple of 32
  * (else MOE_ERR_INVALID_SHAPE).  Envelope: N and T up to 2^20, K up to 2^15
@@ -647,11 +657,14 @@ typedef enum {
 moe_status moe_quant_linear(int format, const uint16_t* x,
                             const uint8_t* codes, const uint8_t* scales, const float* g_scale,
                             const uint16_t* bias, int T, int N, int K,
+                            void* workspace, size_t workspace_bytes,
                             uint16_t* y, void* stream);
 
 /*
- * Bytes of device workspace moe_quant_shared_expert needs (0 when T <= 0):
- * h (bf16 [T, Is]) and the token gates (fp32 [T]), each rounded up to 256.
+ * Bytes of device workspace moe_quant_shared_expert needs (0 when T <= 0 or
+ * the sizes are outside the call's envelope): h (bf16 [T, Is]), the token
+ * gates (fp32 [T]) and the sums of a product whose reduction is split, each
+ * rounded up to 256.
  */
 size_t moe_quant_shared_expert_workspace_size(int T, int H, int Is);
 

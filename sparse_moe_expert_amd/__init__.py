@@ -42,6 +42,7 @@ from .layer import (
     RouteRule,
     make_quant_shared_workspace,
     moe_quant_linear,
+    moe_quant_linear_workspace_size,
     moe_quant_shared_expert,
     moe_quant_shared_expert_workspace_size,
     moe_route_grouped,
@@ -79,6 +80,7 @@ __all__ = [
     "RouteRule",
     "make_quant_shared_workspace",
     "moe_quant_linear",
+    "moe_quant_linear_workspace_size",
     "moe_quant_shared_expert",
     "moe_quant_shared_expert_workspace_size",
     "moe_route_grouped",

@@ -54,7 +54,8 @@ SIGNATURES = {
     "moe_step_noalloc": (_I, [_P, _P, _P] + [_P] * 7 + [_P] + [_I] * 5 + [_P] * 8 + [_P, _P]),
     "moe_route_grouped": (_I, [_P, _I, _P] + [_I] * 8 + [ctypes.c_float] + [_P] * 3),
     "moe_route_grouped_bucket": (_I, [_P, _I, _P] + [_I] * 8 + [ctypes.c_float] + [_P] * 9),
-    "moe_quant_linear": (_I, [_I] + [_P] * 5 + [_I] * 3 + [_P, _P]),
+    "moe_quant_linear_workspace_size": (ctypes.c_size_t, [_I, _I, _I]),
+    "moe_quant_linear": (_I, [_I] + [_P] * 5 + [_I] * 3 + [_P, ctypes.c_size_t, _P, _P]),
     "moe_quant_shared_expert_workspace_size": (ctypes.c_size_t, [_I, _I, _I]),
     "moe_quant_shared_expert": (_I, [_I] + [_P] * 12 + [_I] * 3 + [_P, ctypes.c_size_t, _P, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),

@@ -36,8 +36,13 @@ struct DenseArgs {
 };
 
 // The products' kernels; `gate_up`: the pair a, b.  Arguments already checked.
-// quant_few takes what quant_few_ok says, quant_stream anything.
-bool quant_few_ok(const DenseArgs& p);
+// quant_few and quant_tile take what their _ok says, quant_split anything
+// (with a workspace of quant_split_workspace bytes).
+size_t quant_split_workspace(bool gate_up, int T, int N, int K);
+moe_status quant_split(int format, bool gate_up, const DenseArgs& p, void* workspace, hipStream_t s);
+bool quant_tile_ok(bool gate_up, int T, int N);
+moe_status quant_tile(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
+bool quant_few_ok(int T, int K);
 moe_status quant_few(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
 moe_status quant_stream(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
 
@@ -142,6 +147,40 @@ __device__ __forceinline__ void write4(const DenseArgs& p, int t, int n, f32x4 a
   }
 }
 
+// y[t, n .. n+7] from sums (of a gate/up pair: from its outputs), n < N
+template <bool GU>
+__device__ __forceinline__ void write8(const DenseArgs& p, int t, int n, f32x4 lo, f32x4 hi) {
+  float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  const size_t at = (size_t)t * p.N + n;
+  if (p.N % 8 == 0) {                          // 16-byte aligned, and whole eights
+    if constexpr (!GU) {
+      const float g = p.a.g ? *p.a.g : 1.0f, gate = p.gate ? p.gate[t] : 1.0f;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      const uint4 bias = p.bias ? *reinterpret_cast<const uint4*>(p.bias + n) : zero;
+      const uint4 add = p.add ? *reinterpret_cast<const uint4*>(p.add + at) : zero;
+      const uint32_t b[4] = {bias.x, bias.y, bias.z, bias.w}, d[4] = {add.x, add.y, add.z, add.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int sh = i % 2 * 16;
+        if (p.bias) v[i] = v[i] * g + bf16_to_f32(b[i / 2] >> sh & 0xFFFFu);
+        else v[i] *= g;
+        v[i] *= gate;
+        if (p.add) v[i] += bf16_to_f32(d[i / 2] >> sh & 0xFFFFu);
+      }
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_rne(v[2 * i]) | (f32_to_bf16_rne(v[2 * i + 1]) << 16);
+    *reinterpret_cast<uint4*>(p.y + at) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (n + i >= p.N) return;
+      p.y[at + i] = (uint16_t)f32_to_bf16_rne(GU ? v[i] : output<false>(p, t, n + i, v[i], 0.0f));
+    }
+  }
+}
+
 __device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
 
 template <int N>
@@ -186,7 +225,8 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 // Argument checks shared by the 4-bit products
 inline bool quant_format_ok(int f) { return f == MOE_QUANT_NVFP4 || f == MOE_QUANT_MXFP4; }
 inline bool quant_dims_ok(int n, int k) { return n >= 1 && k >= 32 && k % 32 == 0; }
-inline bool quant_dims_fit(int n, int k) { return n <= (1 << 20) && k <= (1 << 15); }
+constexpr int kQuantMaxK = 1 << 15;
+inline bool quant_dims_fit(int n, int k) { return n <= (1 << 20) && k <= kQuantMaxK; }
 constexpr int kQuantMaxTokens = 1 << 20;
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 

@@ -9,8 +9,16 @@
 namespace moe {
 namespace {
 
-moe_status quant_product(int format, bool gate_up, const DenseArgs& p, hipStream_t s) {
-  return quant_few_ok(p) ? quant_few(format, gate_up, p, s) : quant_stream(format, gate_up, p, s);
+size_t product_workspace(bool gate_up, int T, int N, int K) {
+  if (quant_few_ok(T, K) || quant_tile_ok(gate_up, T, N)) return 0;
+  return quant_split_workspace(gate_up, T, N, K);
+}
+
+// `workspace`: product_workspace bytes
+moe_status quant_product(int format, bool gate_up, const DenseArgs& p, void* workspace, hipStream_t s) {
+  if (quant_few_ok(p.T, p.K)) return quant_few(format, gate_up, p, s);
+  if (quant_tile_ok(gate_up, p.T, p.N)) return quant_tile(format, gate_up, p, s);
+  return quant_split(format, gate_up, p, workspace, s);
 }
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -18,9 +26,15 @@ inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 }  // namespace
 }  // namespace moe
 
+extern "C" size_t moe_quant_linear_workspace_size(int T, int N, int K) {
+  using namespace moe;
+  if (T <= 0 || T > kQuantMaxTokens || !quant_dims_ok(N, K) || !quant_dims_fit(N, K)) return 0;
+  return align256(product_workspace(false, T, N, K));
+}
+
 extern "C" moe_status moe_quant_linear(int format, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
-                                       const float* g_scale, const uint16_t* bias, int T, int N, int K, uint16_t* y,
-                                       void* stream) {
+                                       const float* g_scale, const uint16_t* bias, int T, int N, int K,
+                                       void* workspace, size_t workspace_bytes, uint16_t* y, void* stream) {
   using namespace moe;
   if (!quant_format_ok(format) || T < 0 || !quant_dims_ok(N, K)) return MOE_ERR_INVALID_SHAPE;
   if (!quant_dims_fit(N, K) || T > kQuantMaxTokens) return MOE_ERR_UNSUPPORTED;
@@ -29,14 +43,21 @@ extern "C" moe_status moe_quant_linear(int format, const uint16_t* x, const uint
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(y) || (bias && !aligned16(bias)) ||
       !aligned4(g_scale))
     return MOE_ERR_MISALIGNED;
+  const size_t need = moe_quant_linear_workspace_size(T, N, K);
+  if (need > 0 && !workspace) return MOE_ERR_NULL_POINTER;
+  if (need > 0 && !aligned16(workspace)) return MOE_ERR_MISALIGNED;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const DenseArgs p{x, {codes, scales, g_scale}, {}, bias, nullptr, nullptr, y, T, N, K, nullptr, nullptr};
-  return quant_product(format, false, p, static_cast<hipStream_t>(stream));
+  return quant_product(format, false, p, workspace, static_cast<hipStream_t>(stream));
 }
 
 extern "C" size_t moe_quant_shared_expert_workspace_size(int T, int H, int Is) {
-  (void)H;
-  if (T <= 0 || Is <= 0) return 0;
-  return moe::align256((size_t)T * (size_t)Is * 2) + moe::align256((size_t)T * 4);
+  using namespace moe;
+  if (T <= 0 || T > kQuantMaxTokens || !quant_dims_ok(H, Is) || !quant_dims_ok(Is, H) || H > kQuantMaxK || Is > kQuantMaxK)
+    return 0;
+  // h, the token gates, and the parts' sums of whichever product needs more
+  const size_t up = product_workspace(true, T, Is, H), down = product_workspace(false, T, H, Is);
+  return align256((size_t)T * (size_t)Is * 2) + align256((size_t)T * 4) + align256(up > down ? up : down);
 }
 
 extern "C" moe_status moe_quant_shared_expert(int format, const uint16_t* x, const uint8_t* gate_codes,
@@ -48,7 +69,7 @@ extern "C" moe_status moe_quant_shared_expert(int format, const uint16_t* x, con
                                               uint16_t* y, void* stream) {
   using namespace moe;
   if (!quant_format_ok(format) || T < 0 || !quant_dims_ok(H, Is) || !quant_dims_ok(Is, H)) return MOE_ERR_INVALID_SHAPE;
-  if (H > (1 << 15) || Is > (1 << 15) || T > kQuantMaxTokens) return MOE_ERR_UNSUPPORTED;
+  if (H > kQuantMaxK || Is > kQuantMaxK || T > kQuantMaxTokens) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   const void* need[] = {x, gate_codes, gate_scales, up_codes, up_scales, down_codes, down_scales, workspace, y};
   for (const void* q : need)
@@ -60,13 +81,14 @@ extern "C" moe_status moe_quant_shared_expert(int format, const uint16_t* x, con
     return MOE_ERR_MISALIGNED;
   if (workspace_bytes < moe_quant_shared_expert_workspace_size(T, H, Is)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* const at_gate = static_cast<uint8_t*>(workspace) + align256((size_t)T * (size_t)Is * 2);
+  uint8_t* const at_sums = at_gate + align256((size_t)T * 4);
   uint16_t* const h = static_cast<uint16_t*>(workspace);
-  float* const gate = token_gate ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                                            align256((size_t)T * (size_t)Is * 2)) : nullptr;
+  float* const gate = token_gate ? reinterpret_cast<float*>(at_gate) : nullptr;
   const DenseArgs up{x, {gate_codes, gate_scales, gate_g}, {up_codes, up_scales, up_g}, nullptr, nullptr, nullptr,
                      h, T, Is, H, token_gate, gate};
-  const moe_status st = quant_product(format, true, up, s);
+  const moe_status st = quant_product(format, true, up, at_sums, s);
   if (st != MOE_OK) return st;
   const DenseArgs down{h, {down_codes, down_scales, down_g}, {}, nullptr, gate, add, y, T, H, Is, nullptr, nullptr};
-  return quant_product(format, false, down, s);
+  return quant_product(format, false, down, at_sums, s);
 }

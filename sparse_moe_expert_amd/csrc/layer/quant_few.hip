@@ -209,10 +209,11 @@ __global__ __launch_bounds__(kFewWaves * kWave, 4) void quant_few_kernel(DenseAr
   }
 }
 
-template <int FMT, bool GU>
-uint32_t lds_bytes(const DenseArgs& p, int waves) {
-  const uint32_t S = (uint32_t)(p.K + kStepK - 1) / kStepK;
-  return (uint32_t)p.T * S * 1024u + (uint32_t)waves * (GU ? 2 : 1) * scale_bytes((uint32_t)(p.K / kScaleGroup<FMT>));
+// LDS bytes of a workgroup: the tokens, and its waves' scales
+uint32_t lds_bytes(int format, bool gate_up, int T, int K, int waves) {
+  const uint32_t S = (uint32_t)(K + kStepK - 1) / kStepK;
+  return (uint32_t)T * S * 1024u +
+         (uint32_t)waves * (gate_up ? 2 : 1) * scale_bytes((uint32_t)(K / (format == MOE_QUANT_NVFP4 ? 16 : 32)));
 }
 
 template <int FMT, bool GU, int TT, int P>
@@ -220,7 +221,7 @@ moe_status launch(const DenseArgs& p, hipStream_t s) {
   const int waves = 4;
   const int tiles = (p.N + 4 * waves - 1) / (4 * waves);
   const int grid = tiles + (p.token_gate ? (p.T + waves - 1) / waves : 0);
-  quant_few_kernel<FMT, GU, TT, P><<<(unsigned)grid, waves * kWave, lds_bytes<FMT, GU>(p, waves), s>>>(p, tiles);
+  quant_few_kernel<FMT, GU, TT, P><<<(unsigned)grid, waves * kWave, lds_bytes(FMT, GU, p.T, p.K, waves), s>>>(p, tiles);
   return launch_status();
 }
 
@@ -240,9 +241,7 @@ moe_status dispatch(const DenseArgs& p, hipStream_t s) {
 
 }  // namespace
 
-bool quant_few_ok(const DenseArgs& p) {
-  return p.T <= 4 && lds_bytes<MOE_QUANT_NVFP4, true>(p, 4) <= 128 * 1024;
-}
+bool quant_few_ok(int T, int K) { return T <= 4 && lds_bytes(MOE_QUANT_NVFP4, true, T, K, 4) <= 128 * 1024; }
 
 moe_status quant_few(int format, bool gate_up, const DenseArgs& p, hipStream_t s) {
   if (format == MOE_QUANT_NVFP4)

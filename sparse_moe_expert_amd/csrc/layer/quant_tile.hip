@@ -1,0 +1,233 @@
+// 4-bit products of many tokens: bound by the matrix cores.
+//
+// A workgroup of four waves owns 128 tokens and 256 weight rows (128 rows of
+// both matrices of a gate/up pair); a wave owns 64 of the rows (32 of each
+// matrix) and all of the tokens, so that every weight is decoded once a
+// workgroup and every token fragment read from LDS feeds two products.
+// v_mfma_f32_32x32x16_bf16, weights as A: lane l holds row l%32, reduction
+// indices 8*(l/32)..+8; tokens as B: column l%32, the same indices; D
+// register r is row 8*(r/4) + 4*(l/32) + r%4, column l%32.  The reduction
+// index is permuted alike in both: in a step of 64 the lane half h covers
+// 32h .. 32h+32, so that a lane's codes of a step are one 16-byte load.
+//
+// Tokens go straight to a ring of four LDS stages (16-byte chunk c of token
+// row r at c ^ ((r >> 1) & 7): the reads of 16 lanes hit all banks), codes and
+// scales to a ring of registers, all issued two steps ahead.  With two stages
+// more than steps in flight one barrier a step is enough: the stage that step
+// s fills was read in step s-2, and a wave passes step s-1's barrier only when
+// every wave's reads of s-2 have returned.
+//
+// Workgroups are dealt round robin to the 8 XCDs; each XCD takes consecutive
+// tiles, the row tiles of one token tile after another, so that its L2 holds
+// the tokens that its workgroups share.
+#include "quant_common.h"
+
+#include <type_traits>
+
+namespace moe {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kTileThreads = 256;
+constexpr int kTileTokens = 128;
+constexpr int kTileK = 64;
+constexpr int kStages = 4, kLead = 2;
+constexpr int kStageBytes = kTileTokens * kTileK * 2;        // 16 KB
+constexpr int kXcds = 8;
+
+template <int FMT, bool GU>
+struct RowTile {
+  static constexpr int kLoads = 4 + 2 * 2;                   // a step's, per thread
+  __amdgpu_buffer_rsrc_t rc[GU ? 2 : 1], rs[GU ? 2 : 1], rx;
+  uint32_t c_off[2], s_off[2], x_off[4];
+  uint4 wc[kStages][2];
+  uint16_t ws[kStages][2];                                   // 16 bits until used: a widening would wait for its load
+
+  template <int S>
+  __device__ __forceinline__ void issue(uint8_t* stage, int wave, uint32_t step) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int r = GU ? m : 0;
+      wc[S][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rc[r], c_off[m] + step * 32u, 0, 0));
+      if constexpr (FMT == MOE_QUANT_NVFP4)
+        ws[S][m] = __builtin_amdgcn_raw_buffer_load_b16(rs[r], s_off[m] + step * 4u, 0, 0);
+      else
+        ws[S][m] = __builtin_amdgcn_raw_buffer_load_b8(rs[r], s_off[m] + step * 2u, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, stage + (i * 4 + wave) * 1024, 16, x_off[i] + step * 128u, 0, 0, 0);
+  }
+};
+
+template <int FMT, bool GU>
+__global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p, int row_tiles, int tiles) {
+  using Tile = RowTile<FMT, GU>;
+  constexpr int kRows = GU ? 128 : 256;
+  // one array per stage, so that reads of one stage are seen not to alias the
+  // loads in flight to the others
+  __shared__ __align__(16) uint8_t s_0[kStageBytes];
+  __shared__ __align__(16) uint8_t s_1[kStageBytes];
+  __shared__ __align__(16) uint8_t s_2[kStageBytes];
+  __shared__ __align__(16) uint8_t s_3[kStageBytes];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int per = (tiles + kXcds - 1) / kXcds;
+  if ((int)blockIdx.x >= per * kXcds) {                      // token gates, one wave a token
+    const int t = ((int)blockIdx.x - per * kXcds) * 4 + wave;
+    if (t < p.T) token_gate_row(p, t, lane);
+    return;
+  }
+  const int tile = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
+  if (tile >= tiles) return;
+  const int n0 = (tile % row_tiles) * kRows, t0 = (tile / row_tiles) * kTileTokens;
+  const int l32 = lane & 31, half = lane >> 5;
+  const int rows = min(kRows, p.N - n0), toks = min(kTileTokens, p.T - t0);
+
+  Tile tl;
+  const uint32_t code_row = (uint32_t)p.K / 2, scale_row = (uint32_t)(p.K / kScaleGroup<FMT>);
+#pragma unroll
+  for (int m = 0; m < (GU ? 2 : 1); ++m) {
+    const QuantMat& w = m ? p.b : p.a;
+    tl.rc[m] = make_rsrc(w.codes + (size_t)n0 * code_row, (uint32_t)rows * code_row);
+    tl.rs[m] = make_rsrc(w.scales + (size_t)n0 * scale_row, (uint32_t)rows * scale_row);
+  }
+  tl.rx = make_rsrc(p.x + (size_t)t0 * p.K, (uint32_t)toks * (uint32_t)p.K * 2u);
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const uint32_t row = (uint32_t)((GU ? 0 : m * 128) + wave * 32 + l32);
+    tl.c_off[m] = row * code_row + (uint32_t)half * 16u;
+    tl.s_off[m] = row * scale_row + (uint32_t)half * (FMT == MOE_QUANT_NVFP4 ? 2u : 1u);
+  }
+  // piece i of a wave: 8 token rows of 128 bytes; rows past the last token repeat it
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = (i * 4 + wave) * 8 + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+    tl.x_off[i] = (uint32_t)min(row, toks - 1) * (uint32_t)p.K * 2u + (uint32_t)c * 16u;
+  }
+  const int steps = (p.K + kTileK - 1) / kTileK;
+  f32x16 acc[2][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[m][j] = f32x16{};
+
+  // a step past the last one is issued out of range: it reads nothing
+  auto at = [&](int s) { return s < steps ? (uint32_t)s : kOutside / 128u; };
+  tl.template issue<0>(s_0, wave, at(0));
+  fence();
+  tl.template issue<1>(s_1, wave, at(1));
+  fence();
+  auto body = [&](auto stage_c, int s) {
+    constexpr int S = decltype(stage_c)::value, F = (S + kLead) % kStages;
+    tl.template issue<F>(F == 0 ? s_0 : F == 1 ? s_1 : F == 2 ? s_2 : s_3, wave, at(s + kLead));
+    wait_vm<kLead * Tile::kLoads>();                         // this wave's part of step s is here
+    uint8_t* const stage = S == 0 ? s_0 : S == 1 ? s_1 : S == 2 ? s_2 : s_3;
+    if (p.K - s * kTileK < kTileK) {                         // half a step: what follows a token's row is not its
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = (i * 4 + wave) * 8 + (lane >> 3);
+        if (((lane & 7) ^ ((row >> 1) & 7)) >= 4)
+          *reinterpret_cast<uint4*>(stage + (i * 4 + wave) * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    wait_lds();                                              // and its reads of step s-1 have returned
+    barrier();
+    bf16x8 af[2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) dequant32<FMT>(tl.wc[S][m], tl.ws[S][m], af[m]);
+    // all four token tiles, also where the last ones are past T: branches
+    // around them would keep the products of a tile apart
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = j * 32 + l32;
+        const bf16x8 b = *reinterpret_cast<const bf16x8*>(stage + row * 128 + (((half * 4 + i) ^ ((row >> 1) & 7)) << 4));
+#pragma unroll
+        for (int m = 0; m < 2; ++m) acc[m][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[m][i], b, acc[m][j], 0, 0, 0);
+      }
+    }
+  };
+  int s0 = 0;
+  for (; s0 + kStages <= steps; s0 += kStages) {
+    body(std::integral_constant<int, 0>{}, s0);
+    body(std::integral_constant<int, 1>{}, s0 + 1);
+    body(std::integral_constant<int, 2>{}, s0 + 2);
+    body(std::integral_constant<int, 3>{}, s0 + 3);
+  }
+  if (s0 < steps) body(std::integral_constant<int, 0>{}, s0);
+  if (s0 + 1 < steps) body(std::integral_constant<int, 1>{}, s0 + 1);
+  if (s0 + 2 < steps) body(std::integral_constant<int, 2>{}, s0 + 2);
+  wait_vm<0>();                                              // the loads past the last step have landed
+
+  // Sums to LDS as fp32, then whole 16-byte pieces of output rows.  One array
+  // takes 32 tokens x 128 rows, chunk c of four rows of token t at c ^ (t & 15).
+  constexpr int kRound = GU ? 4 : 2;                         // token tiles a round
+#pragma unroll
+  for (int j0 = 0; j0 < 4; j0 += kRound) {
+    if (j0 * 32 >= toks) break;
+    __syncthreads();
+#pragma unroll
+    for (int jj = 0; jj < kRound; ++jj) {
+      const int j = j0 + jj;
+#pragma unroll
+      for (int m = 0; m < (GU ? 1 : 2); ++m) {
+        const int a = GU ? jj : jj * 2 + m;
+        uint8_t* const out = (a == 0 ? s_0 : a == 1 ? s_1 : a == 2 ? s_2 : s_3) + l32 * 512;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          f32x4 v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = acc[m][j][r * 4 + i];
+            if constexpr (GU) {
+              const float ga = p.a.g ? *p.a.g : 1.0f, gb = p.b.g ? *p.b.g : 1.0f;
+              v[i] = silu(v[i] * ga) * (acc[1][j][r * 4 + i] * gb);
+            }
+          }
+          const int c = wave * 8 + r * 2 + half;
+          *reinterpret_cast<f32x4*>(out + ((c ^ (l32 & 15)) << 4)) = v;
+        }
+      }
+    }
+    __syncthreads();
+    const int pieces = min(toks - j0 * 32, kRound * 32) * (kRows / 8);
+    for (int i = tid; i < pieces; i += kTileThreads) {
+      const int tok = i / (kRows / 8), piece = i % (kRows / 8);        // a token's eight rows
+      const int n = n0 + piece * 8, t = t0 + j0 * 32 + tok;
+      if (n >= p.N) continue;
+      const int a = GU ? tok >> 5 : (tok >> 5) * 2 + (piece >> 4), c = (piece & 15) * 2;
+      const uint8_t* const in = (a == 0 ? s_0 : a == 1 ? s_1 : a == 2 ? s_2 : s_3) + (tok & 31) * 512;
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(in + ((c ^ (tok & 15)) << 4));
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(in + (((c + 1) ^ (tok & 15)) << 4));
+      write8<GU>(p, t, n, lo, hi);
+    }
+  }
+}
+
+template <int FMT, bool GU>
+moe_status launch(const DenseArgs& p, hipStream_t s) {
+  constexpr int kRows = GU ? 128 : 256;
+  const int row_tiles = (p.N + kRows - 1) / kRows;
+  const int tiles = row_tiles * ((p.T + kTileTokens - 1) / kTileTokens);      // at most 2^26 (N and T up to 2^20)
+  const int grid = (tiles + kXcds - 1) / kXcds * kXcds + (p.token_gate ? (p.T + 3) / 4 : 0);
+  quant_tile_kernel<FMT, GU><<<(unsigned)grid, kTileThreads, 0, s>>>(p, row_tiles, tiles);
+  return launch_status();
+}
+
+}  // namespace
+
+bool quant_tile_ok(bool gate_up, int T, int N) {
+  const int rows = gate_up ? 128 : 256;
+  return T > 64 && (long long)((N + rows - 1) / rows) * ((T + kTileTokens - 1) / kTileTokens) >= 128;
+}
+
+moe_status quant_tile(int format, bool gate_up, const DenseArgs& p, hipStream_t s) {
+  if (format == MOE_QUANT_NVFP4)
+    return gate_up ? launch<MOE_QUANT_NVFP4, true>(p, s) : launch<MOE_QUANT_NVFP4, false>(p, s);
+  return gate_up ? launch<MOE_QUANT_MXFP4, true>(p, s) : launch<MOE_QUANT_MXFP4, false>(p, s);
+}
+
+}  // namespace moe

@@ -144,10 +144,15 @@ def _check_quant_x(x, weight: QuantWeight):
     return x.shape[0]
 
 
+def moe_quant_linear_workspace_size(T: int, N: int, K: int) -> int:
+    return int(load_library().moe_quant_linear_workspace_size(T, N, K))
+
+
 def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.Tensor] = None,
-                     y: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """bf16 y [T,N] = x W^T + bias for bf16 x [T,K], a QuantWeight [N,K] and an
-    optional bf16 bias [N]."""
+    optional bf16 bias [N].  The workspace (uint8, for batches that need one) is
+    allocated where none is given."""
     T, N, dev = _check_quant_x(x, weight), weight.N, weight.device
     if bias is not None:
         _tensor(bias, "bias", torch.bfloat16, (N,), dev)
@@ -155,9 +160,16 @@ def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.
         y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
     else:
         _tensor(y, "y", torch.bfloat16, (T, N), dev)
+    lib = load_library()
+    if workspace is not None:
+        _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    elif T > 4 or weight.K > 4096:                   # no workspace below that
+        need = lib.moe_quant_linear_workspace_size(T, N, weight.K)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     with _on(dev):
-        _check("moe_quant_linear", load_library().moe_quant_linear(
+        _check("moe_quant_linear", lib.moe_quant_linear(
             weight._format, x.data_ptr(), *weight._ptrs(), None if bias is None else bias.data_ptr(), T, N, weight.K,
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
             y.data_ptr(), _stream(dev)))
     return y
 

@@ -57,8 +57,8 @@ def test_route_grouped_host_checks(lib, fused):
 
 
 def test_quant_linear_host_checks(lib):
-    def call(fmt=0, x=A, codes=A, scales=A, g=A, bias=None, T=0, N=7, K=64, y=A):
-        return lib.moe_quant_linear(fmt, x, codes, scales, g, bias, T, N, K, y, None)
+    def call(fmt=0, x=A, codes=A, scales=A, g=A, bias=None, T=0, N=7, K=64, y=A, ws=A, ws_bytes=1 << 30):
+        return lib.moe_quant_linear(fmt, x, codes, scales, g, bias, T, N, K, ws, ctypes.c_size_t(ws_bytes), y, None)
     assert call() == OK
     assert call(x=None, y=None) == OK               # T = 0: nothing launched
     for bad in (dict(fmt=2), dict(fmt=-1), dict(T=-1), dict(N=0), dict(K=0), dict(K=48), dict(K=-32)):
@@ -70,6 +70,14 @@ def test_quant_linear_host_checks(lib):
     for name in ("x", "codes", "scales", "bias", "y"):
         assert call(T=1, **{name: P(264)}) == MISALIGNED, name
     assert call(T=1, g=P(258)) == MISALIGNED
+    size = lib.moe_quant_linear_workspace_size
+    assert size(1, 4096, 4096) == size(4, 100, 4096) == size(4096, 4096, 4096) == 0
+    assert size(0, 64, 64) == size(8, 0, 64) == size(8, 64, 48) == size((1 << 20) + 1, 64, 64) == 0
+    need = size(32, 200, 4096)                      # parts of fp32 [32, 256]
+    assert need > 0 and need % (32 * 256 * 4) == 0
+    assert call(T=32, N=200, K=4096, ws_bytes=need - 1) == WORKSPACE
+    assert call(T=32, N=200, K=4096, ws=None) == NULL
+    assert call(T=32, N=200, K=4096, ws=P(264)) == MISALIGNED
 
 
 def test_quant_shared_host_checks(lib):
@@ -93,7 +101,7 @@ def test_quant_shared_host_checks(lib):
     assert call(T=1, v=P(264)) == MISALIGNED
     assert call(T=1, add=P(264)) == MISALIGNED
     need = lib.moe_quant_shared_expert_workspace_size(5, 64, 96)
-    assert need == 1024 + 256                       # 5 * 96 * 2 and 5 * 4, each rounded up to 256
+    assert need == 1024 + 256                       # 5 * 96 * 2 and 5 * 4, each rounded up to 256; nothing split
     assert call(T=5, Is=96, ws=need - 1) == WORKSPACE
     assert lib.moe_quant_shared_expert_workspace_size(0, 64, 96) == 0
 

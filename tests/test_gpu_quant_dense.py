@@ -19,6 +19,7 @@ LINEAR = [
     (8, 64, 1056), (9, 129, 288), (15, 65, 4096), (16, 256, 512), (17, 31, 224), (31, 127, 640), (32, 999, 1024),
     (33, 128, 2080), (63, 72, 96), (64, 512, 256), (65, 257, 128), (100, 640, 320), (127, 1, 64), (128, 128, 64),
     (129, 385, 1088), (255, 200, 32), (257, 512, 512), (1, 20, 32768), (40, 20, 16416), (600, 300, 2048),
+    (4, 40, 12288), (4, 30, 32768), (600, 6500, 96), (513, 8200, 160), (300, 16390, 64),
 ]
 
 
@@ -31,8 +32,9 @@ def test_linear(T, N, K, fmt):
     bias = bits(rng.standard_normal(N)) if (T + N) % 2 else None
     hw, hx, hb = handle(w, fmt), dev_bf16(x), None if bias is None else dev_bf16(bias)
     out = torch.full((T + 2, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = torch.full((max(sme.moe_quant_linear_workspace_size(T, N, K), 16),), 0xFF, dtype=torch.uint8, device=DEV)
     head = T * N * 2 % 16 == 0
-    y = sme.moe_quant_linear(hx, hw, hb, out[:T] if head else None)
+    y = sme.moe_quant_linear(hx, hw, hb, out[:T] if head else None, ws)
     y2 = sme.moe_quant_linear(hx, hw, hb)
     torch.cuda.synchronize()
     assert torch.equal(y.view(torch.int16), y2.view(torch.int16))      # bitwise reproducible
@@ -76,7 +78,7 @@ SHARED = [
     (1, 32, 32, True, True), (1, 2048, 512, False, False), (2, 96, 160, True, False), (4, 2048, 512, True, True),
     (5, 640, 96, False, True), (8, 288, 1056, True, True), (13, 512, 224, True, True), (16, 2560, 640, False, False),
     (32, 64, 2048, True, False), (33, 416, 352, True, True), (64, 256, 256, False, True), (100, 2560, 640, True, True),
-    (130, 512, 128, True, True), (257, 160, 416, True, True),
+    (130, 512, 128, True, True), (257, 160, 416, True, True), (1029, 2080, 2080, True, True),
 ]
 
 
