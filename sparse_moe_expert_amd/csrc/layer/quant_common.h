@@ -42,7 +42,7 @@ size_t quant_split_workspace(bool gate_up, int T, int N, int K);
 moe_status quant_split(int format, bool gate_up, const DenseArgs& p, void* workspace, hipStream_t s);
 bool quant_tile_ok(bool gate_up, int T, int N);
 moe_status quant_tile(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
-bool quant_few_ok(int T, int K);
+bool quant_few_ok(bool gate_up, int T, int N, int K);
 moe_status quant_few(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
 moe_status quant_stream(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
 

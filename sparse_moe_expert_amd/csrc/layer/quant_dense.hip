@@ -10,13 +10,13 @@ namespace moe {
 namespace {
 
 size_t product_workspace(bool gate_up, int T, int N, int K) {
-  if (quant_few_ok(T, K) || quant_tile_ok(gate_up, T, N)) return 0;
+  if (quant_few_ok(gate_up, T, N, K) || quant_tile_ok(gate_up, T, N)) return 0;
   return quant_split_workspace(gate_up, T, N, K);
 }
 
 // `workspace`: product_workspace bytes
 moe_status quant_product(int format, bool gate_up, const DenseArgs& p, void* workspace, hipStream_t s) {
-  if (quant_few_ok(p.T, p.K)) return quant_few(format, gate_up, p, s);
+  if (quant_few_ok(gate_up, p.T, p.N, p.K)) return quant_few(format, gate_up, p, s);
   if (quant_tile_ok(gate_up, p.T, p.N)) return quant_tile(format, gate_up, p, s);
   return quant_split(format, gate_up, p, workspace, s);
 }

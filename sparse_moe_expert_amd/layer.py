@@ -163,7 +163,7 @@ def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.
     lib = load_library()
     if workspace is not None:
         _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    elif T > 4 or weight.K > 4096:                   # no workspace below that
+    elif T > 4 or weight.K > 8192:                   # no workspace below that
         need = lib.moe_quant_linear_workspace_size(T, N, weight.K)
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     with _on(dev):

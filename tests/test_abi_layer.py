@@ -73,11 +73,11 @@ def test_quant_linear_host_checks(lib):
     size = lib.moe_quant_linear_workspace_size
     assert size(1, 4096, 4096) == size(4, 100, 4096) == size(4096, 4096, 4096) == 0
     assert size(0, 64, 64) == size(8, 0, 64) == size(8, 64, 48) == size((1 << 20) + 1, 64, 64) == 0
-    need = size(32, 200, 4096)                      # parts of fp32 [32, 256]
-    assert need > 0 and need % (32 * 256 * 4) == 0
-    assert call(T=32, N=200, K=4096, ws_bytes=need - 1) == WORKSPACE
-    assert call(T=32, N=200, K=4096, ws=None) == NULL
-    assert call(T=32, N=200, K=4096, ws=P(264)) == MISALIGNED
+    need = size(64, 4100, 8192)                     # parts of fp32 [64, 4224]
+    assert need > 0 and need % (64 * 4224 * 4) == 0
+    assert call(T=64, N=4100, K=8192, ws_bytes=need - 1) == WORKSPACE
+    assert call(T=64, N=4100, K=8192, ws=None) == NULL
+    assert call(T=64, N=4100, K=8192, ws=P(264)) == MISALIGNED
 
 
 def test_quant_shared_host_checks(lib):

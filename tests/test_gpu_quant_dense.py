@@ -20,6 +20,8 @@ LINEAR = [
     (33, 128, 2080), (63, 72, 96), (64, 512, 256), (65, 257, 128), (100, 640, 320), (127, 1, 64), (128, 128, 64),
     (129, 385, 1088), (255, 200, 32), (257, 512, 512), (1, 20, 32768), (40, 20, 16416), (600, 300, 2048),
     (4, 40, 12288), (4, 30, 32768), (600, 6500, 96), (513, 8200, 160), (300, 16390, 64),
+    # split reductions: aligned scale rows or not, one to three token tiles, whole and partial steps
+    (20, 33, 16384), (17, 1000, 4128), (33, 900, 8224), (60, 700, 8192), (130, 2600, 4160), (24, 130, 32736),
 ]
 
 
@@ -79,6 +81,7 @@ SHARED = [
     (5, 640, 96, False, True), (8, 288, 1056, True, True), (13, 512, 224, True, True), (16, 2560, 640, False, False),
     (32, 64, 2048, True, False), (33, 416, 352, True, True), (64, 256, 256, False, True), (100, 2560, 640, True, True),
     (130, 512, 128, True, True), (257, 160, 416, True, True), (1029, 2080, 2080, True, True),
+    (20, 8224, 1056, True, True), (70, 4160, 2112, False, True), (150, 1056, 4192, True, False),
 ]
 
 
