@@ -10,101 +10,333 @@
 // choice values are held in 64 bits: sums s + b of different experts often
 // agree to 32 bits, and which expert is taken would hang on the last bit of an
 // exponential.
+//
+// Up to 16 tokens one workgroup selects (a wavefront a token) and buckets; a
+// larger batch selects over the chip, then buckets in a workgroup for each
+// 1024 routes, which counts all routes' experts itself (all of them, and those
+// before its own: no hand-off between workgroups).  From 2^18 routes that
+// counting would take longer than counting once, in the place of an output
+// that is not written yet.
 #include "moe_common.h"
-#include "bucket_block.h"
 #include "route_rule.h"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
 
-// One token per wavefront: scores in LDS, k rounds of arg-max over them.
-__global__ __launch_bounds__(kWave) void route_grouped_kernel(RouteRule r, const void* __restrict__ logits,
-                                                              const float* __restrict__ bias,
-                                                              int32_t* __restrict__ topk_idx,
-                                                              float* __restrict__ topk_w) {
-  __shared__ double s_score[1024];
-  __shared__ double s_choice[1024];
-  __shared__ double s_group[64];
-  __shared__ int s_kept[64];
-  const int lane = threadIdx.x, t = blockIdx.x;
-  const double kMasked = -__builtin_huge_val();
-  double top = kMasked;
-  for (int e = lane; e < r.E; e += kWave) {
-    const double z = load_logit(logits, r.bf16, (size_t)t * r.E + e);
-    s_score[e] = z;
-    top = fmax(top, z);
-  }
-  for (int o = 32; o > 0; o >>= 1) top = fmax(top, __shfl_xor(top, o, kWave));
-  double sum = 0.0;
-  if (r.softmax) {
-    for (int e = lane; e < r.E; e += kWave) {
-      const double z = s_score[e];
-      if (z > kMasked) sum += exp(z - top);
-    }
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
-  }
-  for (int e = lane; e < r.E; e += kWave) {
-    const double z = s_score[e];
-    double s = 0.0;
-    if (z > kMasked) s = r.softmax ? exp(z - top) / sum : 1.0 / (1.0 + exp(-z));
-    const float b = bias ? bias[e] : 0.0f;
-    s_score[e] = s;
-    s_choice[e] = z > kMasked && b > kLowest ? s + (double)b : kMasked;
-  }
-  __syncthreads();
-  const int size = r.E / r.groups;
-  if (lane < r.groups) {
-    double a = kMasked, c = kMasked;
-    for (int i = 0; i < size; ++i) {
-      const double v = s_choice[lane * size + i];
-      if (v > a) { c = a; a = v; } else if (v > c) { c = v; }
-    }
-    s_group[lane] = r.group_top == 2 && c > kMasked ? a + c : a;
-  }
-  __syncthreads();
-  if (lane < r.groups) {
-    int before = 0;
-    for (int g = 0; g < r.groups; ++g)
-      before += s_group[g] > s_group[lane] || (s_group[g] == s_group[lane] && g < lane);
-    s_kept[lane] = before < r.kept;
-  }
-  __syncthreads();
-  // the masked experts of the kept groups follow its others, lowest id first
-  constexpr double kLast = -1e300, kTaken = -1e306;
-  for (int e = lane; e < r.E; e += kWave)
-    s_choice[e] = s_kept[e / size] ? fmax(s_choice[e], kLast) : kTaken;
-  double total = 0.0, my_s = 0.0;
-  int my_e = 0;
-  for (int j = 0; j < r.k; ++j) {
-    double best = -__builtin_huge_val();
-    int be = 1 << 20;
-    for (int e = lane; e < r.E; e += kWave)
-      if (s_choice[e] > best) { best = s_choice[e]; be = e; }
-    for (int o = 32; o > 0; o >>= 1) {
-      const double v = __shfl_xor(best, o, kWave);
-      const int ve = __shfl_xor(be, o, kWave);
-      if (v > best || (v == best && ve < be)) { best = v; be = ve; }
-    }
-    const double s = best > kLast ? s_score[be] : 0.0;
-    total += s;
-    if (lane == j) { my_s = s; my_e = be; }
-    if (lane == (be & (kWave - 1))) s_choice[be] = kTaken;
-  }
+constexpr int kRouteWaves = 4;                 // tokens of a selecting workgroup
+constexpr int kSmallTokens = 16;
+constexpr int kBkThreads = 1024, kBkWaves = kBkThreads / kWave;
+constexpr int kMaxExperts = 1024;
+
+struct BucketOut {
+  int32_t* count;
+  int32_t* offset;
+  int32_t* active;
+  int32_t* n_active;
+  int32_t* src;
+  int32_t* pos;
+};
+
+template <int V>
+__global__ __launch_bounds__(kRouteWaves* kWave) void route_grouped_kernel(RouteRule r, const void* __restrict__ logits,
+                                                                           const float* __restrict__ bias,
+                                                                           int32_t* __restrict__ topk_idx,
+                                                                           float* __restrict__ topk_w) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int t = (int)blockIdx.x * kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= r.T) return;
+  int e;
+  float w;
+  select_grouped<V>(r, logits, bias, t, lane, e, w);
   if (lane < r.k) {
-    double w = my_s;
-    if (r.renormalise) w = total > 0.0 ? w / total : 0.0;
-    topk_idx[(size_t)t * r.k + lane] = my_e;
-    topk_w[(size_t)t * r.k + lane] = (float)(w * (double)r.scale);
+    topk_idx[(size_t)t * r.k + lane] = e;
+    topk_w[(size_t)t * r.k + lane] = w;
   }
 }
 
-__global__ __launch_bounds__(kBucketThreads) void bucket_grouped_kernel(
-    const int32_t* __restrict__ topk_idx, int R, int E, int32_t* __restrict__ expert_count,
-    int32_t* __restrict__ expert_offset, int32_t* __restrict__ active_experts, int32_t* __restrict__ n_active,
-    int32_t* __restrict__ route_src, int32_t* __restrict__ route_pos) {
-  __shared__ BucketShared sh;
-  bucket_block(topk_idx, R, E, sh, expert_count, expert_offset, active_experts, n_active, route_src, route_pos,
-               WorkLists{});
+// Exclusive scan of one value a thread over the workgroup's `waves` waves, and
+// the total.  s_wave: 16 ints.
+__device__ __forceinline__ int scan_block(int v, int* s_wave, int waves, int& total) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int inc = wave_inclusive_scan(v);
+  if (lane == kWave - 1) s_wave[wave] = inc;
+  __syncthreads();
+  int base = 0;
+  total = 0;
+  for (int w = 0; w < waves; ++w) {
+    const int x = s_wave[w];
+    base += w < wave ? x : 0;
+    total += x;
+  }
+  __syncthreads();
+  return base + inc - v;
+}
+
+// Offsets and the active list from the counts s_cnt[E] in LDS, which become the
+// offsets; `write`: to global memory too.
+__device__ __forceinline__ void offsets_block(int* s_cnt, int* s_wave, int E, int threads, bool write, const BucketOut& o) {
+  const int per = (E + threads - 1) / threads, e0 = (int)threadIdx.x * per;
+  int routes = 0, actives = 0;
+  for (int e = e0; e < min(e0 + per, E); ++e) {
+    routes += s_cnt[e];
+    actives += s_cnt[e] > 0;
+  }
+  int all, all_active;
+  int off = scan_block(routes, s_wave, threads / kWave, all);
+  int apos = scan_block(actives, s_wave, threads / kWave, all_active);
+  for (int e = e0; e < min(e0 + per, E); ++e) {
+    const int c = s_cnt[e];
+    s_cnt[e] = off;
+    if (write) {
+      o.count[e] = c;
+      o.offset[e] = off;
+      if (c > 0) o.active[apos] = e;
+      if (e >= all_active) o.active[e] = -1;
+    }
+    off += c;
+    apos += c > 0;
+  }
+  if (write && threadIdx.x == 0) {
+    o.offset[E] = all;
+    *o.n_active = all_active;
+  }
+  __syncthreads();
+}
+
+// Lanes of the wave with the same expert as this one
+__device__ __forceinline__ uint64_t same_expert(int e, bool valid) {
+  uint64_t same = __ballot(valid);
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {                             // ids are below 1024
+    const bool bit = (e >> b) & 1;
+    const uint64_t have = __ballot(bit);
+    same &= bit ? have : ~have;
+  }
+  return same;
+}
+
+// Positions of the routes r0 .. r0 + threads: the base of the expert (its
+// offset, and its routes before r0), and its routes before this one in the
+// workgroup.  s_wcnt: a row of E bytes a wave, zero.
+__device__ __forceinline__ void place_block(const int* s_base, uint8_t (*s_wcnt)[kMaxExperts], int r, bool valid, int e,
+                                            const BucketOut& o) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const uint64_t same = same_expert(e, valid);
+  int rank = __popcll(same & ((1ull << lane) - 1ull));
+  if (valid && rank == 0) s_wcnt[wave][e] = (uint8_t)__popcll(same);
+  __syncthreads();
+  if (valid) {
+    for (int w = 0; w < wave; ++w) rank += s_wcnt[w][e];
+    const int pos = s_base[e] + rank;
+    o.src[pos] = r;
+    o.pos[r] = pos;
+  }
+}
+
+__device__ __forceinline__ void clear(void* p, int bytes, int threads) {
+  for (int i = threadIdx.x; i < bytes / 4; i += threads) static_cast<int*>(p)[i] = 0;
+}
+
+// Selection and buckets of up to 16 tokens; a workgroup of max(T, T*k/64) waves
+template <int V>
+__global__ __launch_bounds__(kBkThreads) void route_bucket_grouped_kernel(RouteRule r, const void* __restrict__ logits,
+                                                                          const float* __restrict__ bias,
+                                                                          int32_t* __restrict__ topk_idx,
+                                                                          float* __restrict__ topk_w, BucketOut o) {
+  __shared__ int s_cnt[kMaxExperts];
+  __shared__ int s_ids[kSmallTokens * 32];
+  __shared__ int s_wave[kBkWaves];
+  __shared__ __align__(4) uint8_t s_wcnt[kSmallTokens * 32 / kWave][kMaxExperts];      // of the waves that have routes
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), threads = (int)blockDim.x;
+  const int t = __builtin_amdgcn_readfirstlane(tid >> 6), R = r.T * r.k;
+  clear(s_cnt, sizeof(s_cnt), threads);
+  clear(s_wcnt, sizeof(s_wcnt), threads);
+  if (t < r.T) {
+    int e;
+    float w;
+    select_grouped<V>(r, logits, bias, t, lane, e, w);
+    if (lane < r.k) {
+      topk_idx[t * r.k + lane] = e;
+      topk_w[t * r.k + lane] = w;
+      s_ids[t * r.k + lane] = e;
+    }
+  }
+  __syncthreads();
+  const bool valid = tid < R;
+  const int e = valid ? s_ids[tid] : 0;
+  if (valid) atomicAdd(&s_cnt[e], 1);                        // integer counts: order-free
+  __syncthreads();
+  offsets_block(s_cnt, s_wave, r.E, threads, true, o);
+  place_block(s_cnt, s_wcnt, tid, valid, e, o);
+}
+
+struct ChunkShared {
+  int all[kMaxExperts];
+  int before[kMaxExperts];
+  int wave[kBkWaves];
+  uint8_t wcnt[kBkWaves][kMaxExperts];
+};
+
+// Workgroup c: routes 1024c .. 1024c + 1024.  The routes before those are
+// counted first, and what is there by then is what earlier workgroups place.
+__global__ __launch_bounds__(kBkThreads) void bucket_chunk_kernel(const int32_t* __restrict__ ids, int R, int E, BucketOut o) {
+  __shared__ ChunkShared sh;
+  const int tid = threadIdx.x, mine = (int)blockIdx.x * kBkThreads;
+  clear(sh.all, sizeof(sh.all), kBkThreads);
+  clear(sh.wcnt, sizeof(sh.wcnt), kBkThreads);
+  __syncthreads();
+  // routes [from, to), from a multiple of 1024: four a thread at a time, eight such loads in flight
+  auto count = [&](int from, int to) {
+    constexpr int kLoads = 8;
+    for (int r0 = from; r0 < to; r0 += kLoads * 4 * kBkThreads) {
+      int4 v[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int r = r0 + (u * kBkThreads + tid) * 4;
+        v[u] = r + 4 <= to ? *reinterpret_cast<const int4*>(ids + r)
+                           : make_int4(r < to ? ids[r] : -1, r + 1 < to ? ids[r + 1] : -1, r + 2 < to ? ids[r + 2] : -1, -1);
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        if (v[u].x >= 0) atomicAdd(&sh.all[v[u].x], 1);
+        if (v[u].y >= 0) atomicAdd(&sh.all[v[u].y], 1);
+        if (v[u].z >= 0) atomicAdd(&sh.all[v[u].z], 1);
+        if (v[u].w >= 0) atomicAdd(&sh.all[v[u].w], 1);
+      }
+    }
+  };
+  count(0, mine);
+  __syncthreads();
+  if (tid < E) sh.before[tid] = sh.all[tid];
+  __syncthreads();
+  count(mine, R);
+  __syncthreads();
+  offsets_block(sh.all, sh.wave, E, kBkThreads, blockIdx.x == 0, o);
+  if (tid < E) sh.before[tid] += sh.all[tid];
+  const int r = mine + tid;
+  const bool valid = r < R;
+  __syncthreads();
+  place_block(sh.before, sh.wcnt, r, valid, valid ? ids[r] : 0, o);
+}
+
+// Many routes, in chunks of 2048: counts[c][e] of every chunk, their prefixes
+// over the chunks, route_src, and its inverse.  The counts lie where route_pos
+// goes (R >= C * E from 2048 routes on), which only the last kernel writes.
+constexpr int kChunk = 2 * kBkThreads;
+
+__global__ __launch_bounds__(kBkThreads) void count_kernel(const int32_t* __restrict__ ids, int R, int E,
+                                                           int32_t* __restrict__ counts) {
+  __shared__ int s_cnt[kMaxExperts];
+  const int tid = threadIdx.x;
+  s_cnt[tid] = 0;
+  __syncthreads();
+  for (int u = 0; u < 2; ++u) {
+    const int r = (int)blockIdx.x * kChunk + u * kBkThreads + tid;
+    if (r < R) atomicAdd(&s_cnt[ids[r]], 1);
+  }
+  __syncthreads();
+  if (tid < E) counts[(size_t)blockIdx.x * E + tid] = s_cnt[tid];
+}
+
+__global__ __launch_bounds__(kBkThreads) void prefix_kernel(int32_t* __restrict__ counts, int C, int E, BucketOut o) {
+  __shared__ int s_cnt[kMaxExperts];
+  __shared__ int s_wave[kBkWaves];
+  const int e = threadIdx.x;
+  constexpr int kTogether = 16;                              // counts in flight
+  int run = 0;
+  if (e < E) {
+    for (int c0 = 0; c0 < C; c0 += kTogether) {
+      int v[kTogether];
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) v[j] = c0 + j < C ? counts[(size_t)(c0 + j) * E + e] : 0;
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        if (c0 + j < C) counts[(size_t)(c0 + j) * E + e] = run;
+        run += v[j];
+      }
+    }
+    s_cnt[e] = run;
+  }
+  __syncthreads();
+  offsets_block(s_cnt, s_wave, E, kBkThreads, true, o);
+}
+
+__global__ __launch_bounds__(kBkThreads) void scatter_kernel(const int32_t* __restrict__ ids, int R, int E,
+                                                             const int32_t* __restrict__ counts, BucketOut o) {
+  __shared__ int s_base[kMaxExperts];
+  __shared__ uint8_t s_wcnt[kBkWaves][kMaxExperts];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+  if (tid < E) s_base[tid] = o.offset[tid] + counts[(size_t)blockIdx.x * E + tid];
+  for (int u = 0; u < 2; ++u) {
+    clear(s_wcnt, sizeof(s_wcnt), kBkThreads);
+    const int r = (int)blockIdx.x * kChunk + u * kBkThreads + tid;
+    const bool valid = r < R;
+    const int e = valid ? ids[r] : 0;
+    const uint64_t same = same_expert(e, valid);
+    const int rank = __popcll(same & ((1ull << lane) - 1ull));
+    __syncthreads();
+    if (valid && rank == 0) s_wcnt[wave][e] = (uint8_t)__popcll(same);
+    __syncthreads();
+    int pos = 0;
+    if (valid) {
+      pos = s_base[e] + rank;
+      for (int w = 0; w < wave; ++w) pos += s_wcnt[w][e];
+      o.src[pos] = r;
+    }
+    __syncthreads();
+    if (valid && rank == 0) atomicAdd(&s_base[e], __popcll(same));
+    __syncthreads();
+  }
+}
+
+__global__ __launch_bounds__(256) void invert_kernel(const int32_t* __restrict__ src, int R, int32_t* __restrict__ pos) {
+  const int p = (int)blockIdx.x * 256 + threadIdx.x;
+  if (p < R) pos[src[p]] = p;
+}
+
+// 2^18 routes: 19 us counted by every workgroup, and longer by its square;
+// once: four launches
+constexpr int kChunkRoutes = 1 << 18;
+
+moe_status bucket(const int32_t* ids, int R, int E, const BucketOut& o, hipStream_t s) {
+  if (R <= kChunkRoutes) {
+    bucket_chunk_kernel<<<(unsigned)((R + kBkThreads - 1) / kBkThreads), kBkThreads, 0, s>>>(ids, R, E, o);
+    return launch_status();
+  }
+  const int C = (R + kChunk - 1) / kChunk;
+  int32_t* const counts = o.pos;
+  count_kernel<<<(unsigned)C, kBkThreads, 0, s>>>(ids, R, E, counts);
+  prefix_kernel<<<1, kBkThreads, 0, s>>>(counts, C, E, o);
+  scatter_kernel<<<(unsigned)C, kBkThreads, 0, s>>>(ids, R, E, counts, o);
+  invert_kernel<<<(unsigned)((R + 255) / 256), 256, 0, s>>>(o.src, R, o.pos);
+  return launch_status();
+}
+
+RouteRule make_rule(int logits_type, int T, int E, int k, int score, int groups, int groups_kept, int group_top,
+                    int renormalise, float scale) {
+  const int lanes = group_lanes(groups), size = E / groups;
+  return RouteRule{T, E, k, groups, groups_kept, group_top, renormalise != 0, score == MOE_SCORE_SOFTMAX,
+                   logits_type == MOE_DTYPE_BF16, scale, lanes, (size + lanes - 1) / lanes};
+}
+
+// f(integral_constant): experts of a lane, rounded up to a power of two
+template <class F>
+void with_experts(const RouteRule& r, F&& f) {
+  if (r.per_lane <= 1) f(std::integral_constant<int, 1>{});
+  else if (r.per_lane <= 2) f(std::integral_constant<int, 2>{});
+  else if (r.per_lane <= 4) f(std::integral_constant<int, 4>{});
+  else if (r.per_lane <= 8) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 16>{});
+}
+
+moe_status select(const RouteRule& r, const void* logits, const float* bias, int32_t* topk_idx, float* topk_w, hipStream_t s) {
+  with_experts(r, [&](auto v) {
+    route_grouped_kernel<decltype(v)::value><<<(unsigned)((r.T + kRouteWaves - 1) / kRouteWaves), kRouteWaves * kWave, 0, s>>>(
+        r, logits, bias, topk_idx, topk_w);
+  });
+  return launch_status();
 }
 
 moe_status check_grouped(const void* logits, int logits_type, const float* bias, int T, int E, int k, int score,
@@ -134,10 +366,8 @@ extern "C" moe_status moe_route_grouped(const void* logits, int logits_type, con
   const moe_status st = check_grouped(logits, logits_type, bias, T, E, k, score, groups, groups_kept, group_top, scale,
                                       topk_idx, topk_w);
   if (st != MOE_OK || T == 0) return st;
-  const RouteRule r{T, E, k, groups, groups_kept, group_top, renormalise != 0, score == MOE_SCORE_SOFTMAX,
-                    logits_type == MOE_DTYPE_BF16, scale};
-  route_grouped_kernel<<<T, kWave, 0, static_cast<hipStream_t>(stream)>>>(r, logits, bias, topk_idx, topk_w);
-  return launch_status();
+  return select(make_rule(logits_type, T, E, k, score, groups, groups_kept, group_top, renormalise, scale), logits, bias,
+                topk_idx, topk_w, static_cast<hipStream_t>(stream));
 }
 
 extern "C" moe_status moe_route_grouped_bucket(const void* logits, int logits_type, const float* bias, int T, int E,
@@ -155,10 +385,17 @@ extern "C" moe_status moe_route_grouped_bucket(const void* logits, int logits_ty
     if (!o) return MOE_ERR_NULL_POINTER;
   for (const int32_t* o : outs)
     if (!aligned16(o)) return MOE_ERR_MISALIGNED;
-  st = moe_route_grouped(logits, logits_type, bias, T, E, k, score, groups, groups_kept, group_top, renormalise, scale,
-                         topk_idx, topk_w, stream);
-  if (st != MOE_OK) return st;
-  bucket_grouped_kernel<<<1, kBucketThreads, 0, static_cast<hipStream_t>(stream)>>>(
-      topk_idx, T * k, E, expert_count, expert_offset, active_experts, n_active, route_src, route_pos);
-  return launch_status();
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const RouteRule r = make_rule(logits_type, T, E, k, score, groups, groups_kept, group_top, renormalise, scale);
+  const BucketOut o{expert_count, expert_offset, active_experts, n_active, route_src, route_pos};
+  if (T <= kSmallTokens) {
+    const int routes = (T * k + kWave - 1) / kWave, waves = T > routes ? T : routes;
+    with_experts(r, [&](auto v) {
+      route_bucket_grouped_kernel<decltype(v)::value><<<1, (waves < 4 ? 4 : waves) * kWave, 0, s>>>(r, logits, bias, topk_idx,
+                                                                                                 topk_w, o);
+    });
+    return launch_status();
+  }
+  st = select(r, logits, bias, topk_idx, topk_w, s);
+  return st == MOE_OK ? bucket(topk_idx, T * k, E, o, s) : st;
 }
