@@ -39,17 +39,18 @@ struct BucketOut {
   int32_t* pos;
 };
 
-template <int V>
+template <int V, bool BF16>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_grouped_kernel(RouteRule r, const void* __restrict__ logits,
                                                                            const float* __restrict__ bias,
                                                                            int32_t* __restrict__ topk_idx,
                                                                            float* __restrict__ topk_w) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int t = (int)blockIdx.x * kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  extern __shared__ __align__(16) float s_rows[];            // 2E a wave
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (int)blockIdx.x * kRouteWaves + wave;
   if (t >= r.T) return;
   int e;
   float w;
-  select_grouped<V>(r, logits, bias, t, lane, e, w);
+  select_grouped<V, BF16>(r, logits, bias, t, lane, s_rows + wave * 2 * r.E, e, w);
   if (lane < r.k) {
     topk_idx[(size_t)t * r.k + lane] = e;
     topk_w[(size_t)t * r.k + lane] = w;
@@ -140,11 +141,12 @@ __device__ __forceinline__ void clear(void* p, int bytes, int threads) {
 }
 
 // Selection and buckets of up to 16 tokens; a workgroup of max(T, T*k/64) waves
-template <int V>
+template <int V, bool BF16>
 __global__ __launch_bounds__(kBkThreads) void route_bucket_grouped_kernel(RouteRule r, const void* __restrict__ logits,
                                                                           const float* __restrict__ bias,
                                                                           int32_t* __restrict__ topk_idx,
                                                                           float* __restrict__ topk_w, BucketOut o) {
+  extern __shared__ __align__(16) float s_rows[];            // 2E a token
   __shared__ int s_cnt[kMaxExperts];
   __shared__ int s_ids[kSmallTokens * 32];
   __shared__ int s_wave[kBkWaves];
@@ -156,7 +158,7 @@ __global__ __launch_bounds__(kBkThreads) void route_bucket_grouped_kernel(RouteR
   if (t < r.T) {
     int e;
     float w;
-    select_grouped<V>(r, logits, bias, t, lane, e, w);
+    select_grouped<V, BF16>(r, logits, bias, t, lane, s_rows + t * 2 * r.E, e, w);
     if (lane < r.k) {
       topk_idx[t * r.k + lane] = e;
       topk_w[t * r.k + lane] = w;
@@ -314,27 +316,35 @@ moe_status bucket(const int32_t* ids, int R, int E, const BucketOut& o, hipStrea
   return launch_status();
 }
 
-RouteRule make_rule(int logits_type, int T, int E, int k, int score, int groups, int groups_kept, int group_top,
+RouteRule make_rule(int T, int E, int k, int score, int groups, int groups_kept, int group_top,
                     int renormalise, float scale) {
   const int lanes = group_lanes(groups), size = E / groups;
   return RouteRule{T, E, k, groups, groups_kept, group_top, renormalise != 0, score == MOE_SCORE_SOFTMAX,
-                   logits_type == MOE_DTYPE_BF16, scale, lanes, (size + lanes - 1) / lanes};
+                   scale, lanes, (size + lanes - 1) / lanes};
 }
 
-// f(integral_constant): experts of a lane, rounded up to a power of two
-template <class F>
+// f(experts of a lane, rounded up to a power of two, and whether logits are bf16, as integral constants)
+template <bool BF16, class F>
 void with_experts(const RouteRule& r, F&& f) {
-  if (r.per_lane <= 1) f(std::integral_constant<int, 1>{});
-  else if (r.per_lane <= 2) f(std::integral_constant<int, 2>{});
-  else if (r.per_lane <= 4) f(std::integral_constant<int, 4>{});
-  else if (r.per_lane <= 8) f(std::integral_constant<int, 8>{});
-  else f(std::integral_constant<int, 16>{});
+  const std::integral_constant<bool, BF16> bf16;
+  if (r.per_lane <= 1) f(std::integral_constant<int, 1>{}, bf16);
+  else if (r.per_lane <= 2) f(std::integral_constant<int, 2>{}, bf16);
+  else if (r.per_lane <= 4) f(std::integral_constant<int, 4>{}, bf16);
+  else if (r.per_lane <= 8) f(std::integral_constant<int, 8>{}, bf16);
+  else f(std::integral_constant<int, 16>{}, bf16);
+}
+template <class F>
+void with_kernel(int logits_type, const RouteRule& r, F&& f) {
+  if (logits_type == MOE_DTYPE_BF16) with_experts<true>(r, f);
+  else with_experts<false>(r, f);
 }
 
-moe_status select(const RouteRule& r, const void* logits, const float* bias, int32_t* topk_idx, float* topk_w, hipStream_t s) {
-  with_experts(r, [&](auto v) {
-    route_grouped_kernel<decltype(v)::value><<<(unsigned)((r.T + kRouteWaves - 1) / kRouteWaves), kRouteWaves * kWave, 0, s>>>(
-        r, logits, bias, topk_idx, topk_w);
+moe_status select(int logits_type, const RouteRule& r, const void* logits, const float* bias, int32_t* topk_idx,
+                  float* topk_w, hipStream_t s) {
+  with_kernel(logits_type, r, [&](auto v, auto bf16) {
+    route_grouped_kernel<decltype(v)::value, decltype(bf16)::value>
+        <<<(unsigned)((r.T + kRouteWaves - 1) / kRouteWaves), kRouteWaves * kWave, kRouteWaves * 8u * r.E, s>>>(
+            r, logits, bias, topk_idx, topk_w);
   });
   return launch_status();
 }
@@ -366,7 +376,7 @@ extern "C" moe_status moe_route_grouped(const void* logits, int logits_type, con
   const moe_status st = check_grouped(logits, logits_type, bias, T, E, k, score, groups, groups_kept, group_top, scale,
                                       topk_idx, topk_w);
   if (st != MOE_OK || T == 0) return st;
-  return select(make_rule(logits_type, T, E, k, score, groups, groups_kept, group_top, renormalise, scale), logits, bias,
+  return select(logits_type, make_rule(T, E, k, score, groups, groups_kept, group_top, renormalise, scale), logits, bias,
                 topk_idx, topk_w, static_cast<hipStream_t>(stream));
 }
 
@@ -386,16 +396,16 @@ extern "C" moe_status moe_route_grouped_bucket(const void* logits, int logits_ty
   for (const int32_t* o : outs)
     if (!aligned16(o)) return MOE_ERR_MISALIGNED;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const RouteRule r = make_rule(logits_type, T, E, k, score, groups, groups_kept, group_top, renormalise, scale);
+  const RouteRule r = make_rule(T, E, k, score, groups, groups_kept, group_top, renormalise, scale);
   const BucketOut o{expert_count, expert_offset, active_experts, n_active, route_src, route_pos};
   if (T <= kSmallTokens) {
     const int routes = (T * k + kWave - 1) / kWave, waves = T > routes ? T : routes;
-    with_experts(r, [&](auto v) {
-      route_bucket_grouped_kernel<decltype(v)::value><<<1, (waves < 4 ? 4 : waves) * kWave, 0, s>>>(r, logits, bias, topk_idx,
-                                                                                                 topk_w, o);
+    with_kernel(logits_type, r, [&](auto v, auto bf16) {
+      route_bucket_grouped_kernel<decltype(v)::value, decltype(bf16)::value>
+          <<<1, (waves < 4 ? 4 : waves) * kWave, T * 8u * E, s>>>(r, logits, bias, topk_idx, topk_w, o);
     });
     return launch_status();
   }
-  st = select(r, logits, bias, topk_idx, topk_w, s);
+  st = select(logits_type, r, logits, bias, topk_idx, topk_w, s);
   return st == MOE_OK ? bucket(topk_idx, T * k, E, o, s) : st;
 }

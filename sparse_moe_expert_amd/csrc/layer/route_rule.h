@@ -4,9 +4,12 @@
 // experts (and groups) ordered by them; an order is taken where every gap that
 // decides it is wider than twice the bound on the fp32 error, or separates
 // experts of the same logit and bias (which tie exactly, and go by their ids).
-// Else the token is ordered again by scores in fp64, as the rule defines them:
-// a few tokens in a hundred with spread logits.  An fp32 score takes about 6
-// instructions, an fp64 one 60, and 512 experts of them would set the time.
+// Else the first k and a few more, one to a lane, are ordered by scores in
+// fp64, as the rule defines them; and where those few do not reach past the
+// doubt, or the groups are in doubt, all experts are.  A few tokens in a
+// hundred with spread logits take the second way, hardly any the third.  An
+// fp32 score takes about 6 instructions, an fp64 one 60, and 512 experts of
+// them would set the time.
 //
 // The error bound, u = 2^-24.  Sigmoid: e^-z is off by (1.5 |z| + 2) u of
 // itself (product and hardware exponential), the sum and the reciprocal by 3 u;
@@ -28,7 +31,7 @@ namespace {
 struct RouteRule {
   int T, E, k;
   int groups, kept, group_top;
-  bool renormalise, softmax, bf16;
+  bool renormalise, softmax;
   float scale;
   int lanes, per_lane;       // of a group; a lane's experts (the last lanes may have fewer)
 };
@@ -52,9 +55,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // softmax over it is defined: such experts share all of the weight).
 __device__ __forceinline__ float mask_logit(float z) { return z > kLowest ? fminf(z, 3.402823466e+38f) : -kInf; }
 
-__device__ __forceinline__ float load_logit(const void* __restrict__ p, bool bf16, size_t i) {
-  return mask_logit(bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16)
-                         : static_cast<const float*>(p)[i]);
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* __restrict__ p, size_t i) {
+  if constexpr (BF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+  else return static_cast<const float*>(p)[i];
 }
 
 template <int CTRL>
@@ -103,14 +107,37 @@ __device__ __forceinline__ void sort_keys(uint64_t (&K)[V]) {
       }
 }
 
-// Largest and second largest over a group's lanes, in every one of them
+__device__ __forceinline__ float read_lane(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane), lo = __builtin_amdgcn_readlane((uint32_t)u, lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float v) {
+  return __builtin_bit_cast(float, dpp_u32<CTRL>(__builtin_bit_cast(uint32_t, v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_move(double v) { return dpp_f64<CTRL>(v); }
+
+// Largest and second largest over a group's lanes (a power of two of them), in
+// every one of them.  Once the lanes of a half agree, a mirrored lane is as
+// good as the one opposite.
 template <class F>
 __device__ __forceinline__ void group_best(int lanes, F& a, F& b) {
-  for (int o = 1; o < lanes; o <<= 1) {
-    const F x = __shfl_xor(a, o, kWave), y = __shfl_xor(b, o, kWave);
+  auto merge = [&](F x, F y) {
     b = fmax(fmin(a, x), fmax(b, y));
     a = fmax(a, x);
-  }
+  };
+  if (lanes > 1) merge(dpp_move<0xB1>(a), dpp_move<0xB1>(b));          // quad_perm [1,0,3,2]
+  if (lanes > 2) merge(dpp_move<0x4E>(a), dpp_move<0x4E>(b));          // quad_perm [2,3,0,1]
+  if (lanes > 4) merge(dpp_move<0x141>(a), dpp_move<0x141>(b));        // row_half_mirror
+  if (lanes > 8) merge(dpp_move<0x140>(a), dpp_move<0x140>(b));        // row_mirror
+  if (lanes > 16) merge(__shfl_xor(a, 16, kWave), __shfl_xor(b, 16, kWave));
+  if (lanes > 32) merge(__shfl_xor(a, 32, kWave), __shfl_xor(b, 32, kWave));
 }
 
 // A group's value from its two best; -inf where it has none
@@ -125,7 +152,7 @@ template <class F>
 __device__ __forceinline__ bool group_kept(const RouteRule& r, int group, F v) {
   int before = 0;
   for (int g = 0; g < r.groups; ++g) {
-    const F o = __shfl(v, g * r.lanes, kWave);
+    const F o = read_lane(v, g * r.lanes);
     before += o > v || (o == v && g < group);
   }
   return before < r.kept;
@@ -133,8 +160,8 @@ __device__ __forceinline__ bool group_kept(const RouteRule& r, int group, F v) {
 
 // The k chosen experts of token t by scores in fp64: slot j's in lane j.  Not
 // inlined, and reads its logits again: the usual way keeps its registers.
-template <int V>
-__device__ __noinline__ int select_exact(RouteRule r, const void* logits, const float* bias, int t, float top, int lane,
+template <int V, bool BF16>
+__device__ __forceinline__ int select_exact(const RouteRule& r, const void* logits, const float* bias, int t, float top, int lane,
                                          int group, int e0, int count) {
   const double kMasked = -__builtin_huge_val();
   double c[V];
@@ -142,7 +169,7 @@ __device__ __noinline__ int select_exact(RouteRule r, const void* logits, const 
   float z[V], b[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    z[i] = i < count ? load_logit(logits, r.bf16, (size_t)t * r.E + e0 + i) : -kInf;
+    z[i] = i < count ? mask_logit(load_logit<BF16>(logits, (size_t)t * r.E + e0 + i)) : -kInf;
     b[i] = i < count && bias ? bias[e0 + i] : 0.0f;
     b[i] = b[i] > kLowest ? b[i] : -kInf;
   }
@@ -195,51 +222,52 @@ __device__ __noinline__ int select_exact(RouteRule r, const void* logits, const 
   return mine;
 }
 
-// Token t: slot j's expert and weight in lane j.
-template <int V>
+// Token t: slot j's expert and weight in lane j.  s_row: 2E floats of LDS, the
+// wavefront's own.
+template <int V, bool BF16>
 __device__ __forceinline__ void select_grouped(const RouteRule& r, const void* __restrict__ logits,
-                                               const float* __restrict__ bias, int t, int lane, int& my_e, float& my_w) {
+                                               const float* __restrict__ bias, int t, int lane, float* s_row, int& my_e,
+                                               float& my_w) {
   const int size = r.E / r.groups, group = lane / r.lanes, at = lane % r.lanes * r.per_lane;
   const int e0 = group * size + at;
   const int count = group < r.groups ? max(min(r.per_lane, size - at), 0) : 0;
   const size_t row = (size_t)t * r.E;
   float z[V], b[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) z[i] = -kInf, b[i] = 0.0f;
   bool wide = false;
-  if constexpr (V >= 4) wide = r.per_lane == V && size % 4 == 0 && r.E % 4 == 0;       // every count is a multiple of 4
+  if constexpr (V >= 4) wide = r.per_lane == V && size % 4 == 0;        // every count and row start a multiple of 4
   if (wide) {
     if constexpr (V >= 4) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4)
-        if (i < count) {
-          float4 v;
-          if (r.bf16) {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + row + e0 + i);
-            v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                            __uint_as_float(u.y & 0xFFFF0000u));
-          } else {
-            v = *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row + e0 + i);
-          }
+      for (int i = 0; i < V; i += 4) {                       // (past the lane's experts: any four, not used)
+        const int e = min(e0 + i, r.E - 4);
+        if constexpr (BF16) {
+          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + row + e);
+          z[i] = __uint_as_float(u.x << 16), z[i + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+          z[i + 2] = __uint_as_float(u.y << 16), z[i + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+        } else {
+          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row + e);
           z[i] = v.x, z[i + 1] = v.y, z[i + 2] = v.z, z[i + 3] = v.w;
-          if (bias) {
-            const float4 w = *reinterpret_cast<const float4*>(bias + e0 + i);
-            b[i] = w.x, b[i + 1] = w.y, b[i + 2] = w.z, b[i + 3] = w.w;
-          }
         }
-#pragma unroll
-      for (int i = 0; i < V; ++i) z[i] = mask_logit(z[i]);
+        const float4 w = bias ? *reinterpret_cast<const float4*>(bias + e) : make_float4(0, 0, 0, 0);
+        b[i] = w.x, b[i + 1] = w.y, b[i + 2] = w.z, b[i + 3] = w.w;
+      }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < count) {
-        z[i] = load_logit(logits, r.bf16, row + e0 + i);
-        if (bias) b[i] = bias[e0 + i];
-      }
+    for (int i = 0; i < V; ++i) {
+      const int e = min(e0 + i, r.E - 1);
+      z[i] = load_logit<BF16>(logits, row + e);
+      b[i] = bias ? bias[e] : 0.0f;
+    }
   }
+  float* const s_z = s_row;
+  float* const s_b = s_row + r.E;
 #pragma unroll
-  for (int i = 0; i < V; ++i) b[i] = b[i] > kLowest ? b[i] : -kInf;
+  for (int i = 0; i < V; ++i) {
+    z[i] = i < count ? mask_logit(z[i]) : -kInf;
+    b[i] = b[i] > kLowest ? b[i] : -kInf;
+    if (i < count) s_z[e0 + i] = z[i], s_b[e0 + i] = b[i];
+  }
 
   // fp32 scores
   float top = 0.0f, unit = 1.0f, s[V];
@@ -276,7 +304,7 @@ __device__ __forceinline__ void select_grouped(const RouteRule& r, const void* _
   sort_keys(K);
   auto value = [](uint64_t key) { return (uint32_t)(key >> 32) > 1u ? from_ordered((uint32_t)(key >> 32)) : -kInf; };
 
-  bool doubt = false;                                        // wave-uniform
+  int doubt = 0;                                             // wave-uniform; 1: of experts, 2: of groups
   if (r.kept < r.groups) {
     float x = value(K[0]), y = V > 1 ? value(K[V > 1 ? 1 : 0]) : -kInf;
     group_best(r.lanes, x, y);
@@ -286,49 +314,76 @@ __device__ __forceinline__ void select_grouped(const RouteRule& r, const void* _
     const float low = -wave_max_f32(real && in ? -v : -kInf), high = wave_max_f32(real && !in ? v : -kInf);
     // (groups with no expert left tie exactly)
     const float most = wave_max_f32(fmaxf(x > -kInf ? fabsf(x) : 0.0f, y > -kInf ? fabsf(y) : 0.0f));
-    doubt = high > -kInf && !(low - high > 2.0f * tol(most) + 3e-7f * most);
+    doubt = high > -kInf && !(low - high > 2.0f * tol(most) + 3e-7f * most) ? 2 : 0;
     if (!in)
 #pragma unroll
       for (int i = 0; i < V; ++i) K[i] = 0;
   }
   uint32_t my_key = 0;
+  int n = 0;                                                 // slots filled: k, and two to five more
   my_e = 0;
-  for (int j = 0; j <= r.k; ++j) {                           // and the first that is not chosen
-    uint32_t best;
-    const int e = select_round<V>(K, lane, &best);
-    if (lane == j) my_key = best, my_e = e;
+  for (; n < r.k + 2; n += 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t best;
+      const int e = select_round<V>(K, lane, &best);
+      if (lane == n + j) my_key = best, my_e = e;
+    }
   }
+  my_e = my_key > 0u ? my_e : 0;                             // (no expert left)
+  float mz = s_z[my_e], mb = s_b[my_e];
   // lane j: slot j against the next
-  my_e = lane < r.k ? my_e : 0;
-  float mz = load_logit(logits, r.bf16, row + my_e), mb = bias ? bias[my_e] : 0.0f;
+  const float c = from_ordered(my_key);
   {
     const uint32_t next = __shfl_down(my_key, 1, kWave);
     const float nz = __shfl_down(mz, 1, kWave), nb = __shfl_down(mb, 1, kWave);
-    const float c = from_ordered(my_key);
     const bool same = lane < r.k - 1 && mz == nz && mb == nb;
     const bool near = lane < r.k && next > 1u && !same && !(c - from_ordered(next) > tol(c));
-    doubt = doubt || __any(near);
+    doubt |= __any(near) ? 1 : 0;
   }
+  const bool need_total = r.softmax && (doubt || !r.renormalise);
+  double total = 1.0;
+  if (need_total) {
+    double sum = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const float x = s_z[e0 + i];
+      if (x > -kInf) sum += exp((double)x - (double)top);
+    }
+    total = wave_sum_f64(sum);
+  }
+  auto score = [&](float x) {
+    if (!(x > -kInf)) return 0.0;
+    return r.softmax ? exp((double)x - (double)top) : 1.0 / (1.0 + exp(-(double)x));
+  };
+  double w = score(mz);
   if (doubt) {
-    my_e = select_exact<V>(r, logits, bias, t, top, lane, group, e0, count);
-    my_e = lane < r.k ? my_e : 0;
-    mz = load_logit(logits, r.bf16, row + my_e), mb = bias ? bias[my_e] : 0.0f;
+    const float cut = read_lane(c, r.k - 1), last = read_lane(c, n - 1);
+    const bool past = __builtin_amdgcn_readlane(my_key, n - 1) <= 1u || cut - last > tol(cut);
+    if (doubt == 1 && past) {
+      // masked ones after all others, lanes without an expert last
+      const bool live = my_key > 1u;
+      double v = live ? w / total + (double)mb : my_key == 1u ? -1e300 : -1e306;
+      const int id = my_key > 0u ? my_e : r.E + lane;
+      int rank = 0;
+      for (int i = 0; i < n; ++i) {
+        const double o = read_lane(v, i);
+        rank += o > v || (o == v && __builtin_amdgcn_readlane(id, i) < id);
+      }
+      const int to = (lane < n ? rank : lane) * 4;
+      my_e = __builtin_amdgcn_ds_permute(to, my_e);
+      my_e = lane < r.k ? my_e : 0;
+    } else {
+      my_e = select_exact<V, BF16>(r, logits, bias, t, top, lane, group, e0, count);
+      my_e = lane < r.k ? my_e : 0;
+    }
+    mz = s_z[my_e], mb = s_b[my_e];
+    w = score(mz);
   }
 
   // weights in fp64
-  const bool live = lane < r.k && mz > -kInf && mb > kLowest;
-  double w = 0.0;
-  if (live) w = r.softmax ? exp((double)mz - (double)top) : 1.0 / (1.0 + exp(-(double)mz));
-  double total = 1.0;
-  if (r.renormalise) {
-    total = wave_sum_f64(w);
-  } else if (r.softmax) {
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (z[i] > -kInf) sum += exp((double)z[i] - (double)top);
-    total = wave_sum_f64(sum);
-  }
+  w = lane < r.k && mb > -kInf ? w : 0.0;
+  if (r.renormalise) total = wave_sum_f64(w);
   w = total > 0.0 ? w / total : 0.0;
   my_w = (float)(w * (double)r.scale);
 }
