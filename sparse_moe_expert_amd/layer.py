@@ -2,14 +2,14 @@
 products with 4-bit weights and the 4-bit shared expert (argument marshalling
 only, as in _lib).
 
-These calls are a few microseconds of GPU work each, so what does not change
-from call to call is checked once: a RouteRule and a QuantWeight check
-themselves when they are made, and a call checks its own tensors.
+These calls are a few microseconds of GPU work each, less than a call costs
+the host, so what does not change from call to call is checked once: a
+RouteRule and a QuantWeight check themselves when they are made, and a call
+checks its own tensors.
 """
 
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import torch
@@ -20,21 +20,29 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1}        # moe_dtype
 _SCORES = {"softmax": 0, "sigmoid": 1}                 # moe_score
 _FORMATS = {"nvfp4": (0, 16), "mxfp4": (1, 32)}        # moe_quant_format, weights per scale
 
-_here = contextlib.nullcontext()
+Tensor = torch.Tensor
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+# the device and stream queries of torch.cuda without their Python layers
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on(device: torch.device):
-    """The library launches on the current device: make it the tensors' one."""
-    return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _call(name: str, index: int, *args):
+    """The library's call on the tensors' device, which it takes to be the
+    current one, and on torch's current stream there."""
+    fn = getattr(load_library(), name)
+    if _current_device() == index:
+        status = fn(*args, _current_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _current_stream(index))
+    if status != 0:
+        _check(name, status)
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _tensor(t: torch.Tensor, name: str, dtype, shape, device):
+def _tensor(t, name: str, dtype, shape, device, index: int):
     """_need's checks, with the passing case in one expression."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.shape == shape
+    if not (isinstance(t, Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape
             and t.is_contiguous()):
         _need(t, name, dtype, shape, device)
 
@@ -58,34 +66,33 @@ class RouteRule:
 
 
 def _route_args(logits, bias, rule, topk_idx, topk_w):
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+    if not isinstance(logits, Tensor) or logits.dim() != 2:
         raise TypeError("logits must be a [T, E] tensor")
-    if logits.dtype not in _DTYPES:
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    (T, E), k, dev = logits.shape, rule.k, logits.device
-    _tensor(logits, "logits", logits.dtype, (T, E), dev)
-    if not logits.is_cuda:
-        raise ValueError("logits must be a device tensor")
+    (T, E), k, dev, index = logits.shape, rule.k, logits.device, logits.get_device()
+    if index < 0 or not logits.is_contiguous():
+        _need(logits, "logits", logits.dtype)
     if bias is not None:
-        _tensor(bias, "bias", torch.float32, (E,), dev)
+        _tensor(bias, "bias", _F32, (E,), dev, index)
     if topk_idx is None:
-        topk_idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+        topk_idx = torch.empty((T, max(k, 0)), dtype=_I32, device=dev)
     if topk_w is None:
-        topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
-    _tensor(topk_idx, "topk_idx", torch.int32, (T, k), dev)
-    _tensor(topk_w, "topk_w", torch.float32, (T, k), dev)
-    args = (logits.data_ptr(), _DTYPES[logits.dtype], None if bias is None else bias.data_ptr(), T, E, k, *rule._args,
+        topk_w = torch.empty((T, max(k, 0)), dtype=_F32, device=dev)
+    _tensor(topk_idx, "topk_idx", _I32, (T, k), dev, index)
+    _tensor(topk_w, "topk_w", _F32, (T, k), dev, index)
+    args = (logits.data_ptr(), dtype, None if bias is None else bias.data_ptr(), T, E, k, *rule._args,
             topk_idx.data_ptr(), topk_w.data_ptr())
-    return args, T, E, k, dev, topk_idx, topk_w
+    return args, T, E, k, dev, index, topk_idx, topk_w
 
 
 def moe_route_grouped(logits: torch.Tensor, bias: Optional[torch.Tensor], rule: RouteRule,
                       topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None):
     """Expert ids (int32 [T,k]) and gate weights (fp32 [T,k]) of fp32 or bf16
     logits [T,E] by a RouteRule; `bias` (fp32 [E]) counts in the selection only."""
-    args, _, _, _, dev, topk_idx, topk_w = _route_args(logits, bias, rule, topk_idx, topk_w)
-    with _on(dev):
-        _check("moe_route_grouped", load_library().moe_route_grouped(*args, _stream(dev)))
+    args, _, _, _, _, index, topk_idx, topk_w = _route_args(logits, bias, rule, topk_idx, topk_w)
+    _call("moe_route_grouped", index, *args)
     return topk_idx, topk_w
 
 
@@ -93,13 +100,17 @@ def moe_route_grouped_bucket(logits: torch.Tensor, bias: Optional[torch.Tensor],
                              topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
                              out: Optional[Buckets] = None):
     """moe_route_grouped and moe_bucket_routes in one call: ids, weights, buckets."""
-    args, T, E, k, dev, topk_idx, topk_w = _route_args(logits, bias, rule, topk_idx, topk_w)
+    args, T, E, k, dev, index, topk_idx, topk_w = _route_args(logits, bias, rule, topk_idx, topk_w)
     b = out if out is not None else empty_buckets(T, E, max(k, 0), dev)
-    for name, t, n in zip(Buckets._fields, b, (E, E + 1, E, 1, T * k, T * k)):
-        _tensor(t, name, torch.int32, (n,), dev)
-    with _on(dev):
-        _check("moe_route_grouped_bucket",
-               load_library().moe_route_grouped_bucket(*args, *(t.data_ptr() for t in b), _stream(dev)))
+    count, offset, active, n_active, src, pos = b
+    _tensor(count, "expert_count", _I32, (E,), dev, index)
+    _tensor(offset, "expert_offset", _I32, (E + 1,), dev, index)
+    _tensor(active, "active_experts", _I32, (E,), dev, index)
+    _tensor(n_active, "n_active", _I32, (1,), dev, index)
+    _tensor(src, "route_src", _I32, (T * k,), dev, index)
+    _tensor(pos, "route_pos", _I32, (T * k,), dev, index)
+    _call("moe_route_grouped_bucket", index, *args, count.data_ptr(), offset.data_ptr(), active.data_ptr(),
+          n_active.data_ptr(), src.data_ptr(), pos.data_ptr())
     return topk_idx, topk_w, b
 
 
@@ -108,7 +119,7 @@ class QuantWeight:
     `scales` uint8 [N, K/16] ("nvfp4") or [N, K/32] ("mxfp4") and the global
     scale, fp32 [1] (None: 1, "mxfp4" only)."""
 
-    __slots__ = ("codes", "scales", "g_scale", "format", "N", "K", "device", "_format")
+    __slots__ = ("codes", "scales", "g_scale", "format", "N", "K", "device", "_format", "_index")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, g_scale: Optional[torch.Tensor] = None,
                  format: str = "nvfp4"):
@@ -127,6 +138,7 @@ class QuantWeight:
         elif format == "nvfp4":
             raise ValueError("nvfp4 weights need their global scale (g_scale)")
         self.codes, self.scales, self.g_scale, self.format = codes, scales, g_scale, format
+        self._index = codes.get_device()
 
     @property
     def shape(self):
@@ -137,11 +149,12 @@ class QuantWeight:
         return self.codes.data_ptr(), self.scales.data_ptr(), None if g is None else g.data_ptr()
 
 
-def _check_quant_x(x, weight: QuantWeight):
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+def _check_quant_x(x, weight: QuantWeight) -> int:
+    if not isinstance(x, Tensor) or x.dim() != 2:
         raise TypeError("x must be a [T, K] tensor")
-    _tensor(x, "x", torch.bfloat16, (x.shape[0], weight.K), weight.device)
-    return x.shape[0]
+    T = x.shape[0]
+    _tensor(x, "x", _BF16, (T, weight.K), weight.device, weight._index)
+    return T
 
 
 def moe_quant_linear_workspace_size(T: int, N: int, K: int) -> int:
@@ -153,24 +166,22 @@ def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.
     """bf16 y [T,N] = x W^T + bias for bf16 x [T,K], a QuantWeight [N,K] and an
     optional bf16 bias [N].  The workspace (uint8, for batches that need one) is
     allocated where none is given."""
-    T, N, dev = _check_quant_x(x, weight), weight.N, weight.device
+    T, N, dev, index = _check_quant_x(x, weight), weight.N, weight.device, weight._index
     if bias is not None:
-        _tensor(bias, "bias", torch.bfloat16, (N,), dev)
+        _tensor(bias, "bias", _BF16, (N,), dev, index)
     if y is None:
-        y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        y = torch.empty((T, N), dtype=_BF16, device=dev)
     else:
-        _tensor(y, "y", torch.bfloat16, (T, N), dev)
-    lib = load_library()
+        _tensor(y, "y", _BF16, (T, N), dev, index)
     if workspace is not None:
-        _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        _tensor(workspace, "workspace", _U8, workspace.shape, dev, index)
     elif T > 4 or weight.K > 8192:                   # no workspace below that
-        need = lib.moe_quant_linear_workspace_size(T, N, weight.K)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-    with _on(dev):
-        _check("moe_quant_linear", lib.moe_quant_linear(
-            weight._format, x.data_ptr(), *weight._ptrs(), None if bias is None else bias.data_ptr(), T, N, weight.K,
-            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-            y.data_ptr(), _stream(dev)))
+        need = load_library().moe_quant_linear_workspace_size(T, N, weight.K)
+        workspace = torch.empty((need,), dtype=_U8, device=dev) if need else None
+    _call("moe_quant_linear", index, weight._format, x.data_ptr(), *weight._ptrs(),
+          None if bias is None else bias.data_ptr(), T, N, weight.K,
+          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+          y.data_ptr())
     return y
 
 
@@ -189,29 +200,27 @@ def moe_quant_shared_expert(x: torch.Tensor, gate: QuantWeight, up: QuantWeight,
     """The 4-bit shared expert: bf16 y [T,H] = add + sigmoid(x . token_gate) *
     W_down (SiLU(W_gate x) * (W_up x)), gate/up [Is,H] and down [H,Is] of one
     format; `token_gate` (bf16 [H]) and `add` (bf16 [T,H], may be y) optional."""
-    T, H, Is, dev = _check_quant_x(x, gate), gate.K, gate.N, gate.device
-    if up.shape != (Is, H) or down.shape != (H, Is):
+    T, H, Is, dev, index = _check_quant_x(x, gate), gate.K, gate.N, gate.device, gate._index
+    if up.N != Is or up.K != H or down.N != H or down.K != Is:
         raise ValueError(f"gate is {gate.shape}, up {up.shape}, down {down.shape}: up must be gate's shape, down its "
                          "transpose's")
     if not (gate._format == up._format == down._format):
         raise ValueError("gate, up and down must have one format")
-    if not (up.device == dev and down.device == dev):
+    if not (up._index == index and down._index == index):
         raise ValueError(f"gate is on {dev}, up on {up.device}, down on {down.device}")
     if token_gate is not None:
-        _tensor(token_gate, "token_gate", torch.bfloat16, (H,), dev)
+        _tensor(token_gate, "token_gate", _BF16, (H,), dev, index)
     if add is not None:
-        _tensor(add, "add", torch.bfloat16, (T, H), dev)
+        _tensor(add, "add", _BF16, (T, H), dev, index)
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        y = torch.empty((T, H), dtype=_BF16, device=dev)
     else:
-        _tensor(y, "y", torch.bfloat16, (T, H), dev)
+        _tensor(y, "y", _BF16, (T, H), dev, index)
     if workspace is None:
         workspace = make_quant_shared_workspace(T, H, Is, dev)
     else:
-        _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    with _on(dev):
-        _check("moe_quant_shared_expert", load_library().moe_quant_shared_expert(
-            gate._format, x.data_ptr(), *gate._ptrs(), *up._ptrs(), *down._ptrs(),
-            None if token_gate is None else token_gate.data_ptr(), None if add is None else add.data_ptr(),
-            T, H, Is, workspace.data_ptr(), workspace.numel(), y.data_ptr(), _stream(dev)))
+        _tensor(workspace, "workspace", _U8, workspace.shape, dev, index)
+    _call("moe_quant_shared_expert", index, gate._format, x.data_ptr(), *gate._ptrs(), *up._ptrs(), *down._ptrs(),
+          None if token_gate is None else token_gate.data_ptr(), None if add is None else add.data_ptr(),
+          T, H, Is, workspace.data_ptr(), workspace.numel(), y.data_ptr())
     return y
