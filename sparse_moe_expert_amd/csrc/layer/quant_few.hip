@@ -228,62 +228,74 @@ __global__ __launch_bounds__(kFewWaves * kWave, 4) void quant_few_kernel(DenseAr
 }
 
 // LDS bytes of a workgroup: the tokens, and its waves' scales
-uint32_t lds_bytes(int group, int T, int K, int waves) {
+uint32_t lds_bytes(int group, int tokens, int K, int waves) {
   const uint32_t S = (uint32_t)(K + kStepK - 1) / kStepK;
-  return (uint32_t)(T < kFewTokens ? T : kFewTokens) * S * 1024u + (uint32_t)waves * scale_bytes((uint32_t)(K / group));
+  return (uint32_t)tokens * S * 1024u + (uint32_t)waves * scale_bytes((uint32_t)(K / group));
 }
 
 constexpr uint32_t kFewLds = 160 * 1024;
 
 struct FewPlan {
-  int waves;
-  long long bytes;           // tokens and weights that the fullest compute unit loads, times 256
+  int tokens, waves;         // of a workgroup
+  long long bytes;           // tokens and weights that the workgroups load
 };
 
 // Waves of a workgroup.  While the tokens take little LDS several workgroups
 // share a compute unit, and small ones are best (T = 1 9999x4096: 7.3 us with
 // 4 waves, 7.8 with 8 or 10).  Else more waves share one copy of the tokens,
-// fewer spread over the 256 compute units more evenly.
-FewPlan plan(bool gate_up, int T, int N, int K) {
-  const long long tokens = T < kFewTokens ? T : kFewTokens;
-  const bool small = tokens * K * 2 <= 32 * 1024;
-  FewPlan best{0, 0};
+// fewer spread over the 256 compute units more evenly (`bytes`: of the fullest
+// of them, times 256).
+FewPlan plan(bool gate_up, int tokens, int T, int N, int K) {
+  const bool small = tokens * K * 2 <= 48 * 1024;
+  FewPlan best{tokens, 0, 0};
   for (int w = 4; w <= (small ? 4 : kFewWaves); w += 2) {
-    if (lds_bytes(16, T, K, w) > kFewLds) break;
+    if (lds_bytes(16, tokens, K, w) > kFewLds) break;
     const int rows = gate_up ? 2 * w : 4 * w;
-    long long wgs = (long long)((N + rows - 1) / rows) * ((T + kFewTokens - 1) / kFewTokens);
+    long long wgs = (long long)((N + rows - 1) / rows) * ((T + tokens - 1) / tokens);
     if (!small) wgs = (wgs + 255) / 256 * 256;
-    const long long bytes = wgs * (tokens * K * 2 + w * 4ll * K * 9 / 16);
-    if (!best.waves || bytes < best.bytes) best = {w, bytes};
+    const long long bytes = wgs * (tokens * K * 2ll + w * 4ll * K * 9 / 16);
+    if (!best.waves || bytes < best.bytes) best = {tokens, w, bytes};
   }
   return best;
 }
 
+// Above 8 tokens: tiles of 8 while they load little (T = 16 shared expert
+// 2048x512: 7.9 us against 9.1 with 16 tokens a workgroup; T = 24 2560x640:
+// 4.5 against 5.2; but T = 100 2048x2048, 83 MB: 11.3 against 9.3), else of 16.
+constexpr long long kEightBytes = 40 * 1000 * 1000;
+
+FewPlan plan(bool gate_up, int T, int N, int K) {
+  if (T <= 8) return plan(gate_up, T, T, N, K);
+  const FewPlan eight = plan(gate_up, 8, T, N, K);
+  return eight.waves && eight.bytes <= kEightBytes ? eight : plan(gate_up, T < kFewTokens ? T : kFewTokens, T, N, K);
+}
+
 template <int FMT, bool GU, int TT, int P>
-moe_status launch(const DenseArgs& p, hipStream_t s) {
-  const int waves = plan(GU, p.T, p.N, p.K).waves, rows = GU ? 2 * waves : 4 * waves;
+moe_status launch(const DenseArgs& p, const FewPlan& q, hipStream_t s) {
+  const int waves = q.waves, rows = GU ? 2 * waves : 4 * waves;
   const int row_tiles = (p.N + rows - 1) / rows, tiles = row_tiles * ((p.T + TT - 1) / TT);
   const int grid = tiles + (p.token_gate ? (p.T + waves - 1) / waves : 0);
-  const uint32_t lds = lds_bytes(kScaleGroup<FMT>, p.T, p.K, waves);
+  const uint32_t lds = lds_bytes(kScaleGroup<FMT>, q.tokens, p.K, waves);
   quant_few_kernel<FMT, GU, TT, P><<<(unsigned)grid, waves * kWave, lds, s>>>(p, row_tiles, tiles);
   return launch_status();
 }
 
 template <int FMT, bool GU, int TT>
-moe_status dispatch_steps(const DenseArgs& p, hipStream_t s) {
+moe_status dispatch_steps(const DenseArgs& p, const FewPlan& q, hipStream_t s) {
   // steps in flight: no more than there are, and than 128 registers hold
-  if (p.K <= 2 * kStepK) return launch<FMT, GU, TT, 2>(p, s);
-  if (p.K <= 4 * kStepK || TT > 8) return launch<FMT, GU, TT, 4>(p, s);
-  return launch<FMT, GU, TT, (TT > 8 ? 4 : 8)>(p, s);
+  if (p.K <= 2 * kStepK) return launch<FMT, GU, TT, 2>(p, q, s);
+  if (p.K <= 4 * kStepK || TT > 8) return launch<FMT, GU, TT, 4>(p, q, s);
+  return launch<FMT, GU, TT, (TT > 8 ? 4 : 8)>(p, q, s);
 }
 
 template <int FMT, bool GU>
 moe_status dispatch(const DenseArgs& p, hipStream_t s) {
-  if (p.T == 1) return dispatch_steps<FMT, GU, 1>(p, s);
-  if (p.T == 2) return dispatch_steps<FMT, GU, 2>(p, s);
-  if (p.T <= 4) return dispatch_steps<FMT, GU, 4>(p, s);
-  if (p.T <= 8) return dispatch_steps<FMT, GU, 8>(p, s);
-  return dispatch_steps<FMT, GU, 16>(p, s);
+  const FewPlan q = plan(GU, p.T, p.N, p.K);
+  if (q.tokens == 1) return dispatch_steps<FMT, GU, 1>(p, q, s);
+  if (q.tokens == 2) return dispatch_steps<FMT, GU, 2>(p, q, s);
+  if (q.tokens <= 4) return dispatch_steps<FMT, GU, 4>(p, q, s);
+  if (q.tokens <= 8) return dispatch_steps<FMT, GU, 8>(p, q, s);
+  return dispatch_steps<FMT, GU, 16>(p, q, s);
 }
 
 }  // namespace

@@ -221,7 +221,7 @@ moe_status launch(const DenseArgs& p, hipStream_t s) {
 
 bool quant_tile_ok(bool gate_up, int T, int N) {
   const int rows = gate_up ? 128 : 256;
-  return T > 64 && (long long)((N + rows - 1) / rows) * ((T + kTileTokens - 1) / kTileTokens) >= 128;
+  return T > 64 && (long long)((N + rows - 1) / rows) * ((T + kTileTokens - 1) / kTileTokens) >= 256;
 }
 
 moe_status quant_tile(int format, bool gate_up, const DenseArgs& p, hipStream_t s) {
