@@ -1,22 +1,23 @@
-// 4-bit products of batches whose tiles are too few for the chip: 128 weight
-// rows by 16, 32 or 64 tokens, the reduction split over workgroups.
+// 4-bit products of batches whose tiles are too few for the chip: 64 or 128
+// weight rows by 16, 32 or 64 tokens, the reduction split over workgroups
+// where the tiles alone do not fill it.
 //
-// Tokens, codes and scales all go straight to LDS (buffer_load ... lds),
-// steps of 256 of the reduction, two steps ahead in a ring of three stages:
-// a row's 128 code bytes of a step are one cache line, which 8 lanes of one
-// load take whole.  (Loaded to registers, in the layout of the matrix tiles,
-// each load touches 16 bytes of 64 rows' lines, and the scales 2 bytes of
-// them: the lines that a compute unit's L1 then fetches again and again were
-// 4 times the bytes used, and set the time.)
+// Tokens, codes and scales all go straight to LDS (buffer_load ... lds), steps
+// of 256 of the reduction, in a ring of as many stages as LDS holds: a row's
+// 128 code bytes of a step are one cache line, which 8 lanes of one load take
+// whole.  (Loaded to registers, in the layout of the matrix tiles, each load
+// touches 16 bytes of 64 rows' lines, and the scales 2 bytes of them: the
+// lines that a compute unit's L1 then fetches again and again were 4 times the
+// bytes used, and set the time.)
 //
-// Eight waves: wave w takes 32 rows (w % 4) and half of each step (w / 4),
-// so that every weight is decoded once.  Of a gate/up pair a workgroup has 64
-// rows each, waves with w % 4 >= 2 the second matrix's.
+// Eight waves: with RG = rows / 32, wave w takes 32 rows (w % RG) and the
+// 8/RG-th part w / RG of each step, so that every weight is decoded once.  Of a
+// gate/up pair the first half of the rows is the first matrix's.
 // v_mfma_f32_32x32x16_bf16, weights as A: lane l holds row l%32, reduction
 // indices 8*(l/32)..+8; tokens as B: column l%32, the same indices; D
 // register r is row 8*(r/4) + 4*(l/32) + r%4, column l%32.  The reduction
-// index is permuted alike in both: of a wave's 128 the lane half h covers
-// 64h .. 64h+64.
+// index is permuted alike in both: the lane halves take the halves of a wave's
+// part, and a lane's codes of it are one or two 16-byte chunks.
 //
 // LDS: a token's step is 512 bytes, its 16-byte chunk c at c ^ (t & 15); a
 // row's codes 128 bytes, chunk c at c ^ ((r >> 1) & 7): the reads of 16 lanes
@@ -36,31 +37,32 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kSplitWaves = 8;
 constexpr int kSplitThreads = kSplitWaves * kWave;
-constexpr int kSplitRows = 128;                              // of one matrix, or 64 of each of two
 constexpr int kSplitK = 256;
-constexpr int kStages = 3;
+constexpr uint32_t kSplitLds = 160 * 1024;
 constexpr int kMaxSplits = 16;
 
 // WIDE: the scales of a row's step start at a multiple of four bytes and go
 // to LDS with the rest; else every lane loads its own, two bytes at a time
 // (NVFP4) or one.
-template <int FMT, bool GU, int TOK, bool WIDE>
+template <int FMT, bool GU, int ROWS, int TOK, bool WIDE>
 struct SplitTile {
-  static constexpr int kTokenBytes = TOK * kSplitK * 2, kCodeBytes = kSplitRows * kSplitK / 2;
+  static constexpr int kTokenBytes = TOK * kSplitK * 2, kCodeBytes = ROWS * kSplitK / 2;
   static constexpr int kScaleBytes = WIDE ? kSplitThreads * 4 : 0;
   static constexpr int kStageBytes = kTokenBytes + kCodeBytes + kScaleBytes;
+  static constexpr int kFit = kSplitLds / kStageBytes, kStages = kFit < 6 ? kFit : 6;
+  static constexpr int RG = ROWS / 32, KP = kSplitWaves / RG, U = 4 / KP;      // row groups, parts of a step, chunks a lane
   static constexpr int XL = kTokenBytes / 1024 / kSplitWaves, CL = kCodeBytes / 1024 / kSplitWaves;
-  static constexpr int kLoads = XL + CL + (WIDE ? 1 : 2);    // a step's, per wave
+  static constexpr int kLoads = XL + CL + (WIDE ? 1 : U);    // a step's, per wave
   __amdgpu_buffer_rsrc_t rc, rs, rx;                         // the wave's matrix, the tokens
   uint32_t c_off[CL], s_off, x_off[XL];
-  uint16_t ws[kStages][2];
+  uint16_t ws[kStages][U];
 
   template <int S>
   __device__ __forceinline__ void issue(uint8_t* stage, int wave, uint32_t step) {
 #pragma unroll
     for (int i = 0; i < XL; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, stage + (i * kSplitWaves + wave) * 1024, 16, x_off[i] + step * 512u, 0, 0, 0);
-    // wave w loads the codes of rows 16w .. 16w+16, and of one matrix only
+    // wave w loads the codes of ROWS/8 rows from w * ROWS/8 on, of one matrix only
 #pragma unroll
     for (int i = 0; i < CL; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, stage + kTokenBytes + (wave * CL + i) * 1024, 16, c_off[i] + step * 128u, 0, 0, 0);
@@ -69,7 +71,7 @@ struct SplitTile {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, stage + kTokenBytes + kCodeBytes + wave * 256, 4, s_off + step * kStep, 0, 0, 0);
     } else {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < U; ++u) {
         if constexpr (FMT == MOE_QUANT_NVFP4) ws[S][u] = __builtin_amdgcn_raw_buffer_load_b16(rs, s_off + step * kStep + u * 2u, 0, 0);
         else ws[S][u] = __builtin_amdgcn_raw_buffer_load_b8(rs, s_off + step * kStep + u, 0, 0);
       }
@@ -77,17 +79,30 @@ struct SplitTile {
   }
 };
 
-template <int FMT, bool GU, int TOK, bool WIDE>
-__global__ __launch_bounds__(kSplitThreads, TOK > 16 ? 2 : 4) void quant_split_kernel(DenseArgs p, int row_tiles, int tiles,
-                                                                                   int splits, float* __restrict__ sums) {
-  using Tile = SplitTile<FMT, GU, TOK, WIDE>;
-  constexpr int JT = TOK < 32 ? 1 : TOK / 32, kRows = GU ? kSplitRows / 2 : kSplitRows;
-  static_assert(JT * 16384 <= Tile::kStageBytes, "the waves' sums fit the ring");
+template <int FMT, bool GU, int ROWS, int TOK, bool WIDE>
+__global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs p, int row_tiles, int tiles, int splits,
+                                                                       float* __restrict__ sums) {
+  using Tile = SplitTile<FMT, GU, ROWS, TOK, WIDE>;
+  constexpr int NS = Tile::kStages, RG = Tile::RG, KP = Tile::KP, U = Tile::U;
+  constexpr int JT = TOK < 32 ? 1 : TOK / 32, kRows = GU ? ROWS / 2 : ROWS;
+  static_assert(NS >= 3 && JT * 16384 <= Tile::kStageBytes, "three stages or more; the waves' sums fit the first ones");
   // one array per stage, so that reads of one stage are seen not to alias the
   // loads in flight to the others
   __shared__ __align__(16) uint8_t s_0[Tile::kStageBytes];
   __shared__ __align__(16) uint8_t s_1[Tile::kStageBytes];
   __shared__ __align__(16) uint8_t s_2[Tile::kStageBytes];
+  __shared__ __align__(16) uint8_t s_3[NS > 3 ? Tile::kStageBytes : 16];
+  __shared__ __align__(16) uint8_t s_4[NS > 4 ? Tile::kStageBytes : 16];
+  __shared__ __align__(16) uint8_t s_5[NS > 5 ? Tile::kStageBytes : 16];
+  auto stage_at = [&](auto g) -> uint8_t* {
+    constexpr int G = decltype(g)::value % NS;
+    if constexpr (G == 0) return s_0;
+    else if constexpr (G == 1) return s_1;
+    else if constexpr (G == 2) return s_2;
+    else if constexpr (G == 3) return s_3;
+    else if constexpr (G == 4) return s_4;
+    else return s_5;
+  };
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if ((int)blockIdx.x >= tiles * splits) {                   // token gates, one wave a token
@@ -97,19 +112,19 @@ __global__ __launch_bounds__(kSplitThreads, TOK > 16 ? 2 : 4) void quant_split_k
   }
   const int split = (int)blockIdx.x / tiles, tile = (int)blockIdx.x % tiles;
   const int n0 = (tile % row_tiles) * kRows, t0 = (tile / row_tiles) * TOK;
-  const int l32 = lane & 31, half = lane >> 5, rg = wave & 3, kh = wave >> 2;
+  const int l32 = lane & 31, half = lane >> 5, rg = wave % RG, kp = wave / RG;
   const int rows = min(kRows, p.N - n0), toks = min(TOK, p.T - t0);
 
   Tile tl;
   const uint32_t code_row = (uint32_t)p.K / 2, scale_row = (uint32_t)(p.K / kScaleGroup<FMT>);
-  // loads: 16 rows a wave, the second half of the waves the second matrix of a pair
+  // loads: ROWS/8 rows a wave, the second half of the waves the second matrix of a pair
   const QuantMat wc = GU && wave >= 4 ? p.b : p.a;
   tl.rc = make_rsrc(wc.codes + (size_t)n0 * code_row, (uint32_t)rows * code_row);
   tl.rx = make_rsrc(p.x + (size_t)t0 * p.K, (uint32_t)toks * (uint32_t)p.K * 2u);
 #pragma unroll
   for (int i = 0; i < Tile::CL; ++i) {
     const int r = (wave * Tile::CL + i) * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
-    tl.c_off[i] = (uint32_t)(GU ? r & 63 : r) * code_row + (uint32_t)c * 16u;
+    tl.c_off[i] = (uint32_t)(r % kRows) * code_row + (uint32_t)c * 16u;
   }
 #pragma unroll
   for (int i = 0; i < Tile::XL; ++i) {
@@ -120,14 +135,13 @@ __global__ __launch_bounds__(kSplitThreads, TOK > 16 ? 2 : 4) void quant_split_k
     // dword w*64 + l of the stage's scales: row by row, 4 (NVFP4) or 2 (MXFP4) a row
     constexpr int kPer = FMT == MOE_QUANT_NVFP4 ? 4 : 2;
     const int r = tid / kPer;
-    const QuantMat ws = GU && wave * kWave / kPer >= 64 ? p.b : p.a;   // a wave's rows are of one matrix
+    const QuantMat ws = GU && wave * kWave / kPer >= kRows ? p.b : p.a;   // a wave's rows are of one matrix
     tl.rs = make_rsrc(ws.scales + (size_t)n0 * scale_row, (uint32_t)rows * scale_row);
-    tl.s_off = r < kSplitRows ? (uint32_t)(GU ? r & 63 : r) * scale_row + (uint32_t)(tid % kPer) * 4u : kOutside;
+    tl.s_off = r < ROWS ? (uint32_t)(r % kRows) * scale_row + (uint32_t)(tid % kPer) * 4u : kOutside;
   } else {
-    const QuantMat ws = GU && rg >= 2 ? p.b : p.a;
+    const QuantMat ws = GU && rg >= RG / 2 ? p.b : p.a;
     tl.rs = make_rsrc(ws.scales + (size_t)n0 * scale_row, (uint32_t)rows * scale_row);
-    tl.s_off = (uint32_t)((GU ? rg & 1 : rg) * 32 + l32) * scale_row +
-               (uint32_t)(kh * 2 + half) * (FMT == MOE_QUANT_NVFP4 ? 4u : 2u);
+    tl.s_off = (uint32_t)((rg * 32 + l32) % kRows) * scale_row + (uint32_t)((kp * 2 + half) * U) * (FMT == MOE_QUANT_NVFP4 ? 2u : 1u);
   }
   const int all = (p.K + kSplitK - 1) / kSplitK, each = all / splits, more = all % splits;
   const int first = split * each + min(split, more), S = each + (split < more ? 1 : 0);
@@ -137,14 +151,17 @@ __global__ __launch_bounds__(kSplitThreads, TOK > 16 ? 2 : 4) void quant_split_k
 
   // a step past this part's last is issued out of range: it reads nothing
   auto at = [&](int s) { return s < S ? (uint32_t)(first + s) : kOutside / 1024u; };
-  tl.template issue<0>(s_0, wave, at(0));
-  fence();
-  tl.template issue<1>(s_1, wave, at(1));
-  fence();
+#define MOE_ISSUE(J)                                                                          \
+  if constexpr (J < NS - 1) {                                                                 \
+    tl.template issue<J>(stage_at(std::integral_constant<int, J>{}), wave, at(J));            \
+    fence();                                                                                  \
+  }
+  MOE_ISSUE(0) MOE_ISSUE(1) MOE_ISSUE(2) MOE_ISSUE(3) MOE_ISSUE(4)
+#undef MOE_ISSUE
   auto body = [&](auto stage_c, int s) {
-    constexpr int G = decltype(stage_c)::value, F = (G + 2) % kStages;
-    wait_vm<Tile::kLoads>();                                 // this wave's part of step s is here
-    uint8_t* const stage = G == 0 ? s_0 : G == 1 ? s_1 : s_2;
+    constexpr int G = decltype(stage_c)::value, F = (G + NS - 1) % NS;
+    wait_vm<(NS - 2) * Tile::kLoads>();                      // this wave's part of step s is here
+    uint8_t* const stage = stage_at(stage_c);
     const int left = p.K - (first + s) * kSplitK;
     if (left < kSplitK) {                                    // what follows a token's row is not its
 #pragma unroll
@@ -156,44 +173,50 @@ __global__ __launch_bounds__(kSplitThreads, TOK > 16 ? 2 : 4) void quant_split_k
     }
     wait_lds();                                              // and its reads of step s-1 have returned
     barrier();                                               // so the stage of step s-1 may be filled again
-    tl.template issue<F>(F == 0 ? s_0 : F == 1 ? s_1 : s_2, wave, at(s + 2));
+    tl.template issue<F>(stage_at(std::integral_constant<int, F>{}), wave, at(s + NS - 1));
     const int r = rg * 32 + l32;
-    uint32_t sb[2];
+    uint32_t sb[U];
     if constexpr (WIDE) {
       const uint8_t* const sr = stage + Tile::kTokenBytes + Tile::kCodeBytes;
-      if constexpr (FMT == MOE_QUANT_NVFP4) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(sr + r * 16 + (kh * 2 + half) * 4);
-        sb[0] = v, sb[1] = v >> 16;
-      } else {
-        const uint32_t v = *reinterpret_cast<const uint16_t*>(sr + r * 8 + (kh * 2 + half) * 2);
-        sb[0] = v & 0xFFu, sb[1] = v >> 8;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = (kp * 2 + half) * U + u;
+        if constexpr (FMT == MOE_QUANT_NVFP4) sb[u] = *reinterpret_cast<const uint16_t*>(sr + r * 16 + c * 2);
+        else sb[u] = sr[r * 8 + c];
       }
     } else {
-      sb[0] = tl.ws[G][0], sb[1] = tl.ws[G][1];
-    }
-    bf16x8 af[2][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int c = (kh * 4 + half * 2 + u) ^ ((r >> 1) & 7);
+      for (int u = 0; u < U; ++u) sb[u] = tl.ws[G][u];
+    }
+    bf16x8 af[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = ((kp * 2 + half) * U + u) ^ ((r >> 1) & 7);
       dequant32<FMT>(*reinterpret_cast<const uint4*>(stage + Tile::kTokenBytes + r * 128 + c * 16), sb[u], af[u]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4 * U; ++i)
 #pragma unroll
       for (int j = 0; j < JT; ++j) {
         const int t = TOK < 32 ? l32 & (TOK - 1) : j * 32 + l32;
-        const bf16x8 b = *reinterpret_cast<const bf16x8*>(stage + t * 512 + (((kh * 16 + half * 8 + i) ^ (t & 15)) << 4));
+        const bf16x8 b = *reinterpret_cast<const bf16x8*>(stage + t * 512 + ((((kp * 2 + half) * 4 * U + i) ^ (t & 15)) << 4));
         acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[i / 4][i % 4], b, acc[j], 0, 0, 0);
       }
   };
+  // whole rings in the loop (one pattern of loads in flight at the back edge), then the rest
   int s0 = 0;
-  for (; s0 + kStages <= S; s0 += kStages) {
-    body(std::integral_constant<int, 0>{}, s0);
-    body(std::integral_constant<int, 1>{}, s0 + 1);
-    body(std::integral_constant<int, 2>{}, s0 + 2);
+#define MOE_STEP(J) \
+  if constexpr (J < NS) body(std::integral_constant<int, J>{}, s0 + J);
+#define MOE_REST(J)           \
+  if constexpr (J < NS - 1) { \
+    if (s0 + J < S) body(std::integral_constant<int, J>{}, s0 + J); \
   }
-  if (s0 < S) body(std::integral_constant<int, 0>{}, s0);
-  if (s0 + 1 < S) body(std::integral_constant<int, 1>{}, s0 + 1);
+  for (; s0 + NS <= S; s0 += NS) {
+    MOE_STEP(0) MOE_STEP(1) MOE_STEP(2) MOE_STEP(3) MOE_STEP(4) MOE_STEP(5)
+  }
+  MOE_REST(0) MOE_REST(1) MOE_REST(2) MOE_REST(3) MOE_REST(4)
+#undef MOE_STEP
+#undef MOE_REST
   wait_vm<0>();                                              // the loads past the last step have landed
   __syncthreads();
 
@@ -219,9 +242,12 @@ __global__ __launch_bounds__(kSplitThreads, TOK > 16 ? 2 : 4) void quant_split_k
     const int w = piece >> 3, g = (piece >> 1) & 3, h = piece & 1, j = tok >> 5, l = h * 32 + (tok & 31);
     auto sum = [&](int v) {
       const int at_l = g * 64 + (l ^ ((v * 8 + g * 2 + h) & 15));
-      return area(v, j)[at_l] + area(v + 4, j)[at_l];
+      f32x4 x = area(v, j)[at_l];
+#pragma unroll
+      for (int k = 1; k < KP; ++k) x += area(v + k * RG, j)[at_l];
+      return x;
     };
-    const f32x4 a = sum(w), b = GU ? sum(w + 2) : a;
+    const f32x4 a = sum(w), b = GU ? sum(w + RG / 2) : a;
     const int t = t0 + tok, n = n0 + piece * 4;
     if (splits == 1) {
       write4<GU>(p, t, n, a, b);
@@ -259,31 +285,46 @@ __global__ __launch_bounds__(256) void quant_join_kernel(DenseArgs p, int np, in
   write4<GU>(p, t, n, v[0], v[NA - 1]);
 }
 
-// Workgroups wanted: one for each of the 256 compute units
-constexpr int kWanted = 256;
-
 struct SplitPlan {
-  int tokens, row_tiles, tiles, splits, np;
+  int tokens, rows, row_tiles, tiles, splits, np;
 };
 
+// Rows of a tile and parts of the reduction, by the time they should take: one
+// workgroup a compute unit (LDS), `rounds` of them, their steps at the time
+// measured for a step, and for more than one part the join (its launch, and
+// its sums written and read).  T = 64 10240x2560: 13.1 us as 64 rows in one
+// part, 17.4 as 128 rows in three; T = 100, where 64 rows take two rounds:
+// 20.9 against 17.4 as 128 rows in one part.
 SplitPlan plan(bool gate_up, int T, int N, int K) {
-  SplitPlan q;
-  const int rows = gate_up ? kSplitRows / 2 : kSplitRows;
-  q.tokens = T <= 16 ? 16 : T <= 32 ? 32 : 64;
-  q.row_tiles = (N + rows - 1) / rows;
-  q.np = q.row_tiles * rows;
-  q.tiles = q.row_tiles * ((T + q.tokens - 1) / q.tokens);
-  const int steps = (K + kSplitK - 1) / kSplitK;
-  const int most = steps < kMaxSplits ? steps : kMaxSplits, want = kWanted / q.tiles;
-  q.splits = want < 1 ? 1 : want < most ? want : most;
-  return q;
+  constexpr int kUnits = 256;
+  constexpr float kStep64[] = {0.75f, 0.92f}, kStep128[] = {1.2f, 1.4f};      // us, up to 32 and 64 tokens
+  constexpr float kJoin = 3.5f, kJoinBytes = 5e6f;                            // us, and bytes a us
+  SplitPlan best{};
+  float least = 0.0f;
+  const int tokens = T <= 16 ? 16 : T <= 32 ? 32 : 64, steps = (K + kSplitK - 1) / kSplitK;
+  for (int rows = 64; rows <= (tokens == 16 ? 64 : 128); rows += 64) {
+    const int own = gate_up ? rows / 2 : rows, row_tiles = (N + own - 1) / own;
+    const int tiles = row_tiles * ((T + tokens - 1) / tokens);
+    for (int splits = 1; splits <= kMaxSplits && splits <= steps; ++splits) {
+      if (splits > 1 && (long long)tiles * splits > kUnits) break;
+      const int rounds = (tiles * splits + kUnits - 1) / kUnits;
+      float us = (float)rounds * (float)((steps + splits - 1) / splits) * (rows == 64 ? kStep64 : kStep128)[tokens > 32];
+      if (splits > 1) us += kJoin + 8.0f * splits * (gate_up ? 2 : 1) * (float)T * (float)(row_tiles * own) / kJoinBytes;
+      if (best.splits == 0 || us < least) {
+        best = {tokens, rows, row_tiles, tiles, splits, row_tiles * own};
+        least = us;
+      }
+    }
+  }
+  return best;
 }
 
-template <int FMT, bool GU, int TOK, bool WIDE>
+template <int FMT, bool GU, int ROWS, int TOK, bool WIDE>
 moe_status launch(const DenseArgs& p, const SplitPlan& q, void* workspace, hipStream_t s) {
   float* const sums = static_cast<float*>(workspace);
   const int grid = q.tiles * q.splits + (p.token_gate ? (p.T + kSplitWaves - 1) / kSplitWaves : 0);
-  quant_split_kernel<FMT, GU, TOK, WIDE><<<(unsigned)grid, kSplitThreads, 0, s>>>(p, q.row_tiles, q.tiles, q.splits, sums);
+  quant_split_kernel<FMT, GU, ROWS, TOK, WIDE>
+      <<<(unsigned)grid, kSplitThreads, 0, s>>>(p, q.row_tiles, q.tiles, q.splits, sums);
   const moe_status st = launch_status();
   if (st != MOE_OK || q.splits == 1) return st;
   const long long work = (long long)p.T * (q.np / 4);
@@ -295,11 +336,15 @@ template <int FMT, bool GU>
 moe_status dispatch(const DenseArgs& p, void* workspace, hipStream_t s) {
   const SplitPlan q = plan(GU, p.T, p.N, p.K);
   const bool wide = (p.K / kScaleGroup<FMT>) % 4 == 0;
-#define MOE_SPLIT(TOK) \
-  return wide ? launch<FMT, GU, TOK, true>(p, q, workspace, s) : launch<FMT, GU, TOK, false>(p, q, workspace, s)
-  if (q.tokens == 16) MOE_SPLIT(16);
-  if (q.tokens == 32) MOE_SPLIT(32);
-  MOE_SPLIT(64);
+#define MOE_SPLIT(ROWS, TOK) \
+  return wide ? launch<FMT, GU, ROWS, TOK, true>(p, q, workspace, s) : launch<FMT, GU, ROWS, TOK, false>(p, q, workspace, s)
+  if (q.tokens == 16) MOE_SPLIT(64, 16);
+  if (q.rows == 64) {
+    if (q.tokens == 32) MOE_SPLIT(64, 32);
+    MOE_SPLIT(64, 64);
+  }
+  if (q.tokens == 32) MOE_SPLIT(128, 32);
+  MOE_SPLIT(128, 64);
 #undef MOE_SPLIT
 }
 
