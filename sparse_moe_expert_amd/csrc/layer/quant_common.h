@@ -37,8 +37,10 @@ struct DenseArgs {
 
 // The products' kernels; `gate_up`: the pair a, b.  Arguments already checked.
 // quant_few and quant_tile take what their _ok says, quant_split anything
-// (with a workspace of quant_split_workspace bytes).
+// (with a workspace of quant_split_workspace bytes, in about quant_split_us
+// beyond a launch).
 size_t quant_split_workspace(bool gate_up, int T, int N, int K);
+float quant_split_us(bool gate_up, int T, int N, int K);
 moe_status quant_split(int format, bool gate_up, const DenseArgs& p, void* workspace, hipStream_t s);
 bool quant_tile_ok(bool gate_up, int T, int N);
 moe_status quant_tile(int format, bool gate_up, const DenseArgs& p, hipStream_t s);

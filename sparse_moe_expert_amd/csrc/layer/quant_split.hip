@@ -287,6 +287,7 @@ __global__ __launch_bounds__(256) void quant_join_kernel(DenseArgs p, int np, in
 
 struct SplitPlan {
   int tokens, rows, row_tiles, tiles, splits, np;
+  float us;
 };
 
 // Rows of a tile and parts of the reduction, by the time they should take: one
@@ -300,7 +301,6 @@ SplitPlan plan(bool gate_up, int T, int N, int K) {
   constexpr float kStep64[] = {0.75f, 0.92f}, kStep128[] = {1.2f, 1.4f};      // us, up to 32 and 64 tokens
   constexpr float kJoin = 3.5f, kJoinBytes = 5e6f;                            // us, and bytes a us
   SplitPlan best{};
-  float least = 0.0f;
   const int tokens = T <= 16 ? 16 : T <= 32 ? 32 : 64, steps = (K + kSplitK - 1) / kSplitK;
   for (int rows = 64; rows <= (tokens == 16 ? 64 : 128); rows += 64) {
     const int own = gate_up ? rows / 2 : rows, row_tiles = (N + own - 1) / own;
@@ -310,10 +310,7 @@ SplitPlan plan(bool gate_up, int T, int N, int K) {
       const int rounds = (tiles * splits + kUnits - 1) / kUnits;
       float us = (float)rounds * (float)((steps + splits - 1) / splits) * (rows == 64 ? kStep64 : kStep128)[tokens > 32];
       if (splits > 1) us += kJoin + 8.0f * splits * (gate_up ? 2 : 1) * (float)T * (float)(row_tiles * own) / kJoinBytes;
-      if (best.splits == 0 || us < least) {
-        best = {tokens, rows, row_tiles, tiles, splits, row_tiles * own};
-        least = us;
-      }
+      if (best.splits == 0 || us < best.us) best = {tokens, rows, row_tiles, tiles, splits, row_tiles * own, us};
     }
   }
   return best;
@@ -354,6 +351,8 @@ size_t quant_split_workspace(bool gate_up, int T, int N, int K) {
   const SplitPlan q = plan(gate_up, T, N, K);
   return q.splits == 1 ? 0 : (size_t)q.splits * (gate_up ? 2 : 1) * (size_t)T * (size_t)q.np * 4;
 }
+
+float quant_split_us(bool gate_up, int T, int N, int K) { return plan(gate_up, T, N, K).us; }
 
 moe_status quant_split(int format, bool gate_up, const DenseArgs& p, void* workspace, hipStream_t s) {
   if (format == MOE_QUANT_NVFP4)
