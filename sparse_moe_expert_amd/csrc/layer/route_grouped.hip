@@ -11,7 +11,7 @@
 // agree to 32 bits, and which expert is taken would hang on the last bit of an
 // exponential.
 //
-// Up to 16 tokens one workgroup selects (a wavefront a token) and buckets; a
+// A few tokens: one workgroup selects (a wavefront a token) and buckets; a
 // larger batch selects over the chip, then buckets in a workgroup for each
 // 1024 routes, which counts all routes' experts itself (all of them, and those
 // before its own: no hand-off between workgroups).  From 2^18 routes that
@@ -19,6 +19,7 @@
 // that is not written yet.
 #include "moe_common.h"
 #include "route_rule.h"
+#include "row_dot.h"
 
 #include <type_traits>
 
@@ -26,7 +27,10 @@ namespace moe {
 namespace {
 
 constexpr int kRouteWaves = 4;                 // tokens of a selecting workgroup
-constexpr int kSmallTokens = 16;
+// One workgroup, with its waves four to a SIMD, while they have little to do:
+// T = 16, E = 256: 9.4 us, 9.6 by two launches; E = 512: 12.4 and 10.6; T = 8,
+// E = 512: 8.7 and 10.5.
+constexpr int kSmallTokens = 16, kSmallScores = 12 * 512;
 constexpr int kBkThreads = 1024, kBkWaves = kBkThreads / kWave;
 constexpr int kMaxExperts = 1024;
 
@@ -57,36 +61,30 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grouped_kernel(Route
   }
 }
 
-// Exclusive scan of one value a thread over the workgroup's `waves` waves, and
-// the total.  s_wave: 16 ints.
-__device__ __forceinline__ int scan_block(int v, int* s_wave, int waves, int& total) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
-  const int inc = wave_inclusive_scan(v);
-  if (lane == kWave - 1) s_wave[wave] = inc;
-  __syncthreads();
-  int base = 0;
-  total = 0;
-  for (int w = 0; w < waves; ++w) {
-    const int x = s_wave[w];
-    base += w < wave ? x : 0;
-    total += x;
-  }
-  __syncthreads();
-  return base + inc - v;
-}
-
 // Offsets and the active list from the counts s_cnt[E] in LDS, which become the
-// offsets; `write`: to global memory too.
-__device__ __forceinline__ void offsets_block(int* s_cnt, int* s_wave, int E, int threads, bool write, const BucketOut& o) {
+// offsets; `write`: to global memory too.  s_wave: a pair a wave.
+__device__ __forceinline__ void offsets_block(int* s_cnt, int2* s_wave, int E, int threads, bool write, const BucketOut& o) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6, waves = threads / kWave;
   const int per = (E + threads - 1) / threads, e0 = (int)threadIdx.x * per;
   int routes = 0, actives = 0;
   for (int e = e0; e < min(e0 + per, E); ++e) {
     routes += s_cnt[e];
     actives += s_cnt[e] > 0;
   }
-  int all, all_active;
-  int off = scan_block(routes, s_wave, threads / kWave, all);
-  int apos = scan_block(actives, s_wave, threads / kWave, all_active);
+  int off = wave_inclusive_scan(routes), apos = wave_inclusive_scan(actives);
+  if (lane == kWave - 1) s_wave[wave] = make_int2(off, apos);
+  off -= routes;
+  apos -= actives;
+  __syncthreads();
+  int all = 0, all_active = 0;
+#pragma unroll
+  for (int w = 0; w < kBkWaves; ++w) {                       // (all read at once; absent waves' are not used)
+    const int2 x = s_wave[w];
+    off += w < wave ? x.x : 0;
+    apos += w < wave ? x.y : 0;
+    all += w < waves ? x.x : 0;
+    all_active += w < waves ? x.y : 0;
+  }
   for (int e = e0; e < min(e0 + per, E); ++e) {
     const int c = s_cnt[e];
     s_cnt[e] = off;
@@ -120,7 +118,8 @@ __device__ __forceinline__ uint64_t same_expert(int e, bool valid) {
 
 // Positions of the routes r0 .. r0 + threads: the base of the expert (its
 // offset, and its routes before r0), and its routes before this one in the
-// workgroup.  s_wcnt: a row of E bytes a wave, zero.
+// workgroup.  s_wcnt: a row of E bytes a wave that has routes, zero.
+template <int WAVES>
 __device__ __forceinline__ void place_block(const int* s_base, uint8_t (*s_wcnt)[kMaxExperts], int r, bool valid, int e,
                                             const BucketOut& o) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
@@ -129,15 +128,17 @@ __device__ __forceinline__ void place_block(const int* s_base, uint8_t (*s_wcnt)
   if (valid && rank == 0) s_wcnt[wave][e] = (uint8_t)__popcll(same);
   __syncthreads();
   if (valid) {
-    for (int w = 0; w < wave; ++w) rank += s_wcnt[w][e];
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) rank += w < wave ? s_wcnt[w][e] : 0;
     const int pos = s_base[e] + rank;
     o.src[pos] = r;
     o.pos[r] = pos;
   }
 }
 
+// `bytes` a multiple of 16, as is p
 __device__ __forceinline__ void clear(void* p, int bytes, int threads) {
-  for (int i = threadIdx.x; i < bytes / 4; i += threads) static_cast<int*>(p)[i] = 0;
+  for (int i = threadIdx.x; i < bytes / 16; i += threads) static_cast<int4*>(p)[i] = make_int4(0, 0, 0, 0);
 }
 
 // Selection and buckets of up to 16 tokens; a workgroup of max(T, T*k/64) waves
@@ -147,10 +148,10 @@ __global__ __launch_bounds__(kBkThreads) void route_bucket_grouped_kernel(RouteR
                                                                           int32_t* __restrict__ topk_idx,
                                                                           float* __restrict__ topk_w, BucketOut o) {
   extern __shared__ __align__(16) float s_rows[];            // 2E a token
-  __shared__ int s_cnt[kMaxExperts];
+  __shared__ __align__(16) int s_cnt[kMaxExperts];
   __shared__ int s_ids[kSmallTokens * 32];
-  __shared__ int s_wave[kBkWaves];
-  __shared__ __align__(4) uint8_t s_wcnt[kSmallTokens * 32 / kWave][kMaxExperts];      // of the waves that have routes
+  __shared__ int2 s_wave[kBkWaves];
+  __shared__ __align__(16) uint8_t s_wcnt[kSmallTokens * 32 / kWave][kMaxExperts];      // of the waves that have routes
   const int tid = threadIdx.x, lane = tid & (kWave - 1), threads = (int)blockDim.x;
   const int t = __builtin_amdgcn_readfirstlane(tid >> 6), R = r.T * r.k;
   clear(s_cnt, sizeof(s_cnt), threads);
@@ -171,56 +172,55 @@ __global__ __launch_bounds__(kBkThreads) void route_bucket_grouped_kernel(RouteR
   if (valid) atomicAdd(&s_cnt[e], 1);                        // integer counts: order-free
   __syncthreads();
   offsets_block(s_cnt, s_wave, r.E, threads, true, o);
-  place_block(s_cnt, s_wcnt, tid, valid, e, o);
+  place_block<kSmallTokens * 32 / kWave>(s_cnt, s_wcnt, tid, valid, e, o);
 }
 
 struct ChunkShared {
-  int all[kMaxExperts];
-  int before[kMaxExperts];
-  int wave[kBkWaves];
-  uint8_t wcnt[kBkWaves][kMaxExperts];
+  __align__(16) int after[kMaxExperts];                                    // routes from 1024c on
+  __align__(16) int before[kMaxExperts];
+  int2 wave[kBkWaves];
+  __align__(16) uint8_t wcnt[kBkWaves][kMaxExperts];
 };
 
-// Workgroup c: routes 1024c .. 1024c + 1024.  The routes before those are
-// counted first, and what is there by then is what earlier workgroups place.
+// Workgroup c: routes 1024c .. 1024c + 1024.  All routes are counted, those
+// before them apart: these are what earlier workgroups place.
 __global__ __launch_bounds__(kBkThreads) void bucket_chunk_kernel(const int32_t* __restrict__ ids, int R, int E, BucketOut o) {
   __shared__ ChunkShared sh;
   const int tid = threadIdx.x, mine = (int)blockIdx.x * kBkThreads;
-  clear(sh.all, sizeof(sh.all), kBkThreads);
-  clear(sh.wcnt, sizeof(sh.wcnt), kBkThreads);
-  __syncthreads();
-  // routes [from, to), from a multiple of 1024: four a thread at a time, eight such loads in flight
-  auto count = [&](int from, int to) {
-    constexpr int kLoads = 8;
-    for (int r0 = from; r0 < to; r0 += kLoads * 4 * kBkThreads) {
-      int4 v[kLoads];
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        const int r = r0 + (u * kBkThreads + tid) * 4;
-        v[u] = r + 4 <= to ? *reinterpret_cast<const int4*>(ids + r)
-                           : make_int4(r < to ? ids[r] : -1, r + 1 < to ? ids[r + 1] : -1, r + 2 < to ? ids[r + 2] : -1, -1);
-      }
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        if (v[u].x >= 0) atomicAdd(&sh.all[v[u].x], 1);
-        if (v[u].y >= 0) atomicAdd(&sh.all[v[u].y], 1);
-        if (v[u].z >= 0) atomicAdd(&sh.all[v[u].z], 1);
-        if (v[u].w >= 0) atomicAdd(&sh.all[v[u].w], 1);
-      }
-    }
-  };
-  count(0, mine);
-  __syncthreads();
-  if (tid < E) sh.before[tid] = sh.all[tid];
-  __syncthreads();
-  count(mine, R);
-  __syncthreads();
-  offsets_block(sh.all, sh.wave, E, kBkThreads, blockIdx.x == 0, o);
-  if (tid < E) sh.before[tid] += sh.all[tid];
+  // routes past the last read as 0 and are not counted
+  const auto all_ids = make_rsrc(ids, (uint32_t)R * 4u);
   const int r = mine + tid;
   const bool valid = r < R;
+  const int my_e = (int)__builtin_amdgcn_raw_buffer_load_b32(all_ids, (uint32_t)r * 4u, 0, 0);
+  clear(sh.after, sizeof(sh.after), kBkThreads);
+  clear(sh.before, sizeof(sh.before), kBkThreads);
+  clear(sh.wcnt, sizeof(sh.wcnt), kBkThreads);
   __syncthreads();
-  place_block(sh.before, sh.wcnt, r, valid, valid ? ids[r] : 0, o);
+  constexpr int kLoads = 8;                                  // four routes each, in flight
+  for (int r0 = 0; r0 < R; r0 += kLoads * 4 * kBkThreads) {
+    u32x4 v[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      v[u] = __builtin_amdgcn_raw_buffer_load_b128(all_ids, (uint32_t)(r0 + (u * kBkThreads + tid) * 4) * 4u, 0, 0);
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int at = r0 + (u * kBkThreads + tid) * 4;        // (a multiple of four, as is `mine`)
+      int* const cnt = at < mine ? sh.before : sh.after;
+      if (at + 4 <= R) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) atomicAdd(&cnt[v[u][i]], 1);
+      } else {
+        for (int i = 0; i < R - at; ++i) atomicAdd(&cnt[v[u][i]], 1);
+      }
+    }
+  }
+  __syncthreads();
+  if (tid < E) sh.after[tid] += sh.before[tid];
+  __syncthreads();
+  offsets_block(sh.after, sh.wave, E, kBkThreads, blockIdx.x == 0, o);
+  if (tid < E) sh.before[tid] += sh.after[tid];
+  // (place_block's own barrier is before its reads of `before`)
+  place_block<kBkWaves>(sh.before, sh.wcnt, r, valid, my_e, o);
 }
 
 // Many routes, in chunks of 2048: counts[c][e] of every chunk, their prefixes
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(kBkThreads) void count_kernel(const int32_t* __rest
 
 __global__ __launch_bounds__(kBkThreads) void prefix_kernel(int32_t* __restrict__ counts, int C, int E, BucketOut o) {
   __shared__ int s_cnt[kMaxExperts];
-  __shared__ int s_wave[kBkWaves];
+  __shared__ int2 s_wave[kBkWaves];
   const int e = threadIdx.x;
   constexpr int kTogether = 16;                              // counts in flight
   int run = 0;
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(kBkThreads) void prefix_kernel(int32_t* __restrict_
 __global__ __launch_bounds__(kBkThreads) void scatter_kernel(const int32_t* __restrict__ ids, int R, int E,
                                                              const int32_t* __restrict__ counts, BucketOut o) {
   __shared__ int s_base[kMaxExperts];
-  __shared__ uint8_t s_wcnt[kBkWaves][kMaxExperts];
+  __shared__ __align__(16) uint8_t s_wcnt[kBkWaves][kMaxExperts];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
   if (tid < E) s_base[tid] = o.offset[tid] + counts[(size_t)blockIdx.x * E + tid];
   for (int u = 0; u < 2; ++u) {
@@ -284,7 +284,8 @@ __global__ __launch_bounds__(kBkThreads) void scatter_kernel(const int32_t* __re
     int pos = 0;
     if (valid) {
       pos = s_base[e] + rank;
-      for (int w = 0; w < wave; ++w) pos += s_wcnt[w][e];
+#pragma unroll
+      for (int w = 0; w < kBkWaves; ++w) pos += w < wave ? s_wcnt[w][e] : 0;
       o.src[pos] = r;
     }
     __syncthreads();
@@ -298,8 +299,8 @@ __global__ __launch_bounds__(256) void invert_kernel(const int32_t* __restrict__
   if (p < R) pos[src[p]] = p;
 }
 
-// 2^18 routes: 19 us counted by every workgroup, and longer by its square;
-// once: four launches
+// 2^18 routes (E = 256): with the selection 62 us counted by every workgroup,
+// and longer by its square; counted once: four launches
 constexpr int kChunkRoutes = 1 << 18;
 
 moe_status bucket(const int32_t* ids, int R, int E, const BucketOut& o, hipStream_t s) {
@@ -398,7 +399,7 @@ extern "C" moe_status moe_route_grouped_bucket(const void* logits, int logits_ty
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const RouteRule r = make_rule(T, E, k, score, groups, groups_kept, group_top, renormalise, scale);
   const BucketOut o{expert_count, expert_offset, active_experts, n_active, route_src, route_pos};
-  if (T <= kSmallTokens) {
+  if (T <= kSmallTokens && T * E <= kSmallScores) {
     const int routes = (T * k + kWave - 1) / kWave, waves = T > routes ? T : routes;
     with_kernel(logits_type, r, [&](auto v, auto bf16) {
       route_bucket_grouped_kernel<decltype(v)::value, decltype(bf16)::value>
