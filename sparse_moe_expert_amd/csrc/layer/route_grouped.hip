@@ -14,7 +14,7 @@
 // A few tokens: one workgroup selects (a wavefront a token) and buckets; a
 // larger batch selects over the chip, then buckets in a workgroup for each
 // 1024 routes, which counts all routes' experts itself (all of them, and those
-// before its own: no hand-off between workgroups).  From 2^18 routes that
+// before its own: no hand-off between workgroups).  From 2^17 routes that
 // counting would take longer than counting once, in the place of an output
 // that is not written yet.
 #include "moe_common.h"
@@ -299,9 +299,10 @@ __global__ __launch_bounds__(256) void invert_kernel(const int32_t* __restrict__
   if (p < R) pos[src[p]] = p;
 }
 
-// 2^18 routes (E = 256): with the selection 62 us counted by every workgroup,
-// and longer by its square; counted once: four launches
-constexpr int kChunkRoutes = 1 << 18;
+// With the selection, E = 256, k = 8, counted by every workgroup and counted
+// once (four launches): 65536 routes 22.9 and 26.9 us, 131072 40.8 and 39.6,
+// 240000 64.5 and 57.4.
+constexpr int kChunkRoutes = (1 << 17) - 1;
 
 moe_status bucket(const int32_t* ids, int R, int E, const BucketOut& o, hipStream_t s) {
   if (R <= kChunkRoutes) {

@@ -22,6 +22,11 @@ LINEAR = [
     (4, 40, 12288), (4, 30, 32768), (600, 6500, 96), (513, 8200, 160), (300, 16390, 64),
     # split reductions: aligned scale rows or not, one to three token tiles, whole and partial steps
     (20, 33, 16384), (17, 1000, 4128), (33, 900, 8224), (60, 700, 8192), (130, 2600, 4160), (24, 130, 32736),
+    # rows that take two rounds of smaller tiles; few tokens whose activations do not fit one workgroup
+    (20, 16500, 544), (31, 16500, 512), (90, 10300, 544), (90, 10300, 512), (512, 640, 640), (16, 30, 32768),
+    (8, 70, 32736),
+    # enough tiles of 256 rows by 128 tokens for the chip: partial ones, and either side of a multiple of eight
+    (700, 11000, 96), (600, 13200, 1056), (300, 22000, 64), (1025, 7300, 160), (33000, 260, 32),
 ]
 
 
@@ -82,6 +87,8 @@ SHARED = [
     (32, 64, 2048, True, False), (33, 416, 352, True, True), (64, 256, 256, False, True), (100, 2560, 640, True, True),
     (130, 512, 128, True, True), (257, 160, 416, True, True), (1029, 2080, 2080, True, True),
     (20, 8224, 1056, True, True), (70, 4160, 2112, False, True), (150, 1056, 4192, True, False),
+    (24, 512, 8288, True, False), (30, 544, 8416, False, True), (90, 512, 5216, True, True), (90, 544, 5216, False, False),
+    (300, 96, 2080, True, True), (9, 5152, 96, True, True), (4100, 2080, 1024, True, True), (1301, 96, 3008, True, False),
 ]
 
 

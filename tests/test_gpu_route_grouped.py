@@ -14,12 +14,13 @@ pytestmark = pytest.mark.gpu
 
 # (T, E, k, groups, kept, group_top): one token to thousands; one expert; group sizes of one, odd, and not a divisor of
 # the lanes' share; all slots taken; the largest k; E below, at and above multiples of 64; tokens and routes either side
-# of 8, 16, 64 tokens and of 256, 1024 and 65536 routes
+# of 8, 16, 64 tokens and of 256, 1024 and 131072 routes; few tokens of many experts
 SHAPES = [
     (1, 1, 1, 1, 1, 1), (1, 256, 8, 8, 4, 2), (3, 8, 8, 4, 4, 2), (2, 64, 4, 64, 8, 2), (5, 60, 6, 12, 5, 1),
     (4, 512, 10, 1, 1, 1), (8, 512, 32, 16, 3, 2), (9, 96, 5, 3, 2, 2), (16, 160, 16, 8, 5, 1), (17, 65, 7, 5, 3, 2),
     (33, 1024, 32, 32, 7, 2), (40, 1000, 13, 1, 1, 1), (64, 63, 3, 7, 2, 2), (65, 768, 6, 6, 2, 1), (129, 128, 8, 8, 4, 2),
     (300, 320, 10, 5, 2, 2), (2049, 32, 32, 1, 1, 1), (4097, 16, 2, 4, 2, 2), (8200, 40, 32, 5, 5, 1),
+    (13, 1000, 9, 8, 3, 2), (12, 512, 10, 1, 1, 1), (2047, 48, 32, 6, 6, 1), (4095, 100, 32, 4, 3, 2), (4096, 64, 32, 8, 5, 2),
 ]
 
 
