@@ -302,18 +302,21 @@ moe_status dispatch(const DenseArgs& p, hipStream_t s) {
 
 // Above 16 tokens: while loading each token tile's copy of the weights and each
 // row tile's of the tokens (mostly from L2) at kFewRate takes less than the
-// split kernel should, which is kSplitMore slower to begin.  4096x4096, T = 32
-// (52 MB): 9.3 us against 11.0; T = 64 (70 MB): 14.6 against 12.4; 2048x2048,
-// T = 64 (17 MB): 6.3 against 9.3; 8192x1024, T = 64 (86 MB): 12.1 against 7.4;
-// 2560x640, T = 100 (33 MB): 8.3 against 6.7.
-// Past kFewBytes it never was the faster one.
-constexpr float kFewRate = 7e6f, kSplitMore = 0.5f;          // bytes a us, us
+// split kernel should, which is kSplitMore (of a pair kSplitPairMore) slower to
+// begin.
+// 4096x4096, T = 32 (52 MB): 9.7 us against 10.5; T = 64 (70 MB): 14.6 against
+// 12.4; 2048x2048, T = 64 (17 MB): 6.6 against 9.3; 8192x1024, T = 64 (86 MB):
+// 12.1 against 7.2; 2560x640, T = 100 (33 MB): 8.3 against 6.5; shared expert
+// 2048x4096, T = 32 (its pair 36 MB): 18.6 against 16.2; 4096x1024, T = 17 (36 MB): 12.0 against
+// 14.9.  Past kFewBytes it
+// never was the faster one.
+constexpr float kFewRate = 7e6f, kSplitMore = 1.0f, kSplitPairMore = 0.65f;      // bytes a us, us
 constexpr long long kFewBytes = 60 * 1000 * 1000;
 
 bool quant_few_ok(bool gate_up, int T, int N, int K) {
   const FewPlan q = plan(gate_up, T, N, K);
   if (!q.waves || T <= kFewTokens) return q.waves > 0;
-  return q.bytes <= kFewBytes && (float)q.bytes <= kFewRate * (quant_split_us(gate_up, T, N, K) + kSplitMore);
+  return q.bytes <= kFewBytes && (float)q.bytes <= kFewRate * (quant_split_us(gate_up, T, N, K) + (gate_up ? kSplitPairMore : kSplitMore));
 }
 
 moe_status quant_few(int format, bool gate_up, const DenseArgs& p, hipStream_t s) {

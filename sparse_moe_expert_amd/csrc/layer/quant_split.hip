@@ -3,9 +3,9 @@
 // where the tiles alone do not fill it.
 //
 // Tokens, codes and scales all go straight to LDS (buffer_load ... lds), steps
-// of 256 of the reduction, in a ring of as many stages as LDS holds: a row's
-// 128 code bytes of a step are one cache line, which 8 lanes of one load take
-// whole.  (Loaded to registers, in the layout of the matrix tiles, each load
+// of 256 or 512 of the reduction, in a ring of as many stages as LDS holds: a
+// row's code bytes of a step are whole cache lines, each taken by 8 lanes of
+// one load.  (Loaded to registers, in the layout of the matrix tiles, each load
 // touches 16 bytes of 64 rows' lines, and the scales 2 bytes of them: the
 // lines that a compute unit's L1 then fetches again and again were 4 times the
 // bytes used, and set the time.)
@@ -19,9 +19,9 @@
 // index is permuted alike in both: the lane halves take the halves of a wave's
 // part, and a lane's codes of it are one or two 16-byte chunks.
 //
-// LDS: a token's step is 512 bytes, its 16-byte chunk c at c ^ (t & 15); a
-// row's codes 128 bytes, chunk c at c ^ ((r >> 1) & 7): the reads of 16 lanes
-// hit all banks.
+// LDS: a token's step is its 16-byte chunks, c at c ^ (t & 15); a row's codes
+// 128 bytes, chunk c at c ^ ((r >> 1) & 7), or 256, c at c ^ (r & 15): the reads
+// of 16 lanes hit all banks.
 //
 // With more than one part (`splits`) the workgroups leave fp32 sums in the
 // workspace, [part][matrix][T][Np] (Np: N rounded up to whole tiles), and
@@ -37,20 +37,30 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kSplitWaves = 8;
 constexpr int kSplitThreads = kSplitWaves * kWave;
-constexpr int kSplitK = 256;
 constexpr uint32_t kSplitLds = 160 * 1024;
 constexpr int kMaxSplits = 16;
+
+// Reduction indices of a step, and the multiple of them that a part of the
+// reduction starts at.  NVFP4, whose weights take twice MXFP4's instructions,
+// has fewer barriers with longer steps, three stages of which LDS holds for up
+// to 32 tokens: T = 32 9999x4096, 512: 13.2 us, 256: 15.0; MXFP4, T = 32
+// 10240x2560, with less of its loads in flight: 11.0 and 9.8.
+constexpr int split_unit(int rows, int tokens) { return rows == 64 && tokens <= 32 ? 512 : 256; }
+constexpr int split_step(int format, int rows, int tokens) {
+  return format == MOE_QUANT_NVFP4 ? split_unit(rows, tokens) : 256;
+}
 
 // WIDE: the scales of a row's step start at a multiple of four bytes and go
 // to LDS with the rest; else every lane loads its own, two bytes at a time
 // (NVFP4) or one.
 template <int FMT, bool GU, int ROWS, int TOK, bool WIDE>
 struct SplitTile {
-  static constexpr int kTokenBytes = TOK * kSplitK * 2, kCodeBytes = ROWS * kSplitK / 2;
+  static constexpr int SK = split_step(FMT, ROWS, TOK);
+  static constexpr int kTokenBytes = TOK * SK * 2, kCodeBytes = ROWS * SK / 2;
   static constexpr int kScaleBytes = WIDE ? kSplitThreads * 4 : 0;
   static constexpr int kStageBytes = kTokenBytes + kCodeBytes + kScaleBytes;
   static constexpr int kFit = kSplitLds / kStageBytes, kStages = kFit < 6 ? kFit : 6;
-  static constexpr int RG = ROWS / 32, KP = kSplitWaves / RG, U = 4 / KP;      // row groups, parts of a step, chunks a lane
+  static constexpr int RG = ROWS / 32, KP = kSplitWaves / RG, U = SK / 64 / KP;      // row groups, parts of a step, chunks a lane
   static constexpr int XL = kTokenBytes / 1024 / kSplitWaves, CL = kCodeBytes / 1024 / kSplitWaves;
   static constexpr int kLoads = XL + CL + (WIDE ? 1 : U);    // a step's, per wave
   __amdgpu_buffer_rsrc_t rc, rs, rx;                         // the wave's matrix, the tokens
@@ -61,12 +71,12 @@ struct SplitTile {
   __device__ __forceinline__ void issue(uint8_t* stage, int wave, uint32_t step) {
 #pragma unroll
     for (int i = 0; i < XL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, stage + (i * kSplitWaves + wave) * 1024, 16, x_off[i] + step * 512u, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, stage + (i * kSplitWaves + wave) * 1024, 16, x_off[i] + step * (SK * 2u), 0, 0, 0);
     // wave w loads the codes of ROWS/8 rows from w * ROWS/8 on, of one matrix only
 #pragma unroll
     for (int i = 0; i < CL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, stage + kTokenBytes + (wave * CL + i) * 1024, 16, c_off[i] + step * 128u, 0, 0, 0);
-    constexpr uint32_t kStep = FMT == MOE_QUANT_NVFP4 ? 16 : 8;       // scale bytes of a row's step
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, stage + kTokenBytes + (wave * CL + i) * 1024, 16, c_off[i] + step * (SK / 2u), 0, 0, 0);
+    constexpr uint32_t kStep = SK / kScaleGroup<FMT>;        // scale bytes of a row's step
     if constexpr (WIDE) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, stage + kTokenBytes + kCodeBytes + wave * 256, 4, s_off + step * kStep, 0, 0, 0);
     } else {
@@ -83,7 +93,8 @@ template <int FMT, bool GU, int ROWS, int TOK, bool WIDE>
 __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs p, int row_tiles, int tiles, int splits,
                                                                        float* __restrict__ sums) {
   using Tile = SplitTile<FMT, GU, ROWS, TOK, WIDE>;
-  constexpr int NS = Tile::kStages, RG = Tile::RG, KP = Tile::KP, U = Tile::U;
+  constexpr int NS = Tile::kStages, RG = Tile::RG, KP = Tile::KP, U = Tile::U, SK = Tile::SK;
+  constexpr int kChunks = SK / 8, kCodeChunks = SK / 32;     // 16-byte pieces of a token's, of a row's step
   constexpr int JT = TOK < 32 ? 1 : TOK / 32, kRows = GU ? ROWS / 2 : ROWS;
   static_assert(NS >= 3 && JT * 16384 <= Tile::kStageBytes, "three stages or more; the waves' sums fit the first ones");
   // one array per stage, so that reads of one stage are seen not to alias the
@@ -115,6 +126,9 @@ __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs
   const int l32 = lane & 31, half = lane >> 5, rg = wave % RG, kp = wave / RG;
   const int rows = min(kRows, p.N - n0), toks = min(TOK, p.T - t0);
 
+  // LDS places: chunk c of row r's codes at c ^ code_swizzle(r)
+  auto code_swizzle = [](int r) { return SK == 256 ? (r >> 1) & 7 : r & 15; };
+  auto token_row = [&](int i) { return (i * kSplitWaves + wave) * (kWave / kChunks) + lane / kChunks; };
   Tile tl;
   const uint32_t code_row = (uint32_t)p.K / 2, scale_row = (uint32_t)(p.K / kScaleGroup<FMT>);
   // loads: ROWS/8 rows a wave, the second half of the waves the second matrix of a pair
@@ -123,17 +137,17 @@ __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs
   tl.rx = make_rsrc(p.x + (size_t)t0 * p.K, (uint32_t)toks * (uint32_t)p.K * 2u);
 #pragma unroll
   for (int i = 0; i < Tile::CL; ++i) {
-    const int r = (wave * Tile::CL + i) * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+    const int r = (wave * Tile::CL + i) * (kWave / kCodeChunks) + lane / kCodeChunks, c = lane % kCodeChunks ^ code_swizzle(r);
     tl.c_off[i] = (uint32_t)(r % kRows) * code_row + (uint32_t)c * 16u;
   }
 #pragma unroll
   for (int i = 0; i < Tile::XL; ++i) {
-    const int r = (i * kSplitWaves + wave) * 2 + half, c = l32 ^ (r & 15);
+    const int r = token_row(i), c = lane % kChunks ^ (r & 15);
     tl.x_off[i] = (uint32_t)min(r, toks - 1) * (uint32_t)p.K * 2u + (uint32_t)c * 16u;     // past the last token: it again
   }
   if constexpr (WIDE) {
-    // dword w*64 + l of the stage's scales: row by row, 4 (NVFP4) or 2 (MXFP4) a row
-    constexpr int kPer = FMT == MOE_QUANT_NVFP4 ? 4 : 2;
+    // dword w*64 + l of the stage's scales: row by row
+    constexpr int kPer = SK / kScaleGroup<FMT> / 4;
     const int r = tid / kPer;
     const QuantMat ws = GU && wave * kWave / kPer >= kRows ? p.b : p.a;   // a wave's rows are of one matrix
     tl.rs = make_rsrc(ws.scales + (size_t)n0 * scale_row, (uint32_t)rows * scale_row);
@@ -143,8 +157,10 @@ __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs
     tl.rs = make_rsrc(ws.scales + (size_t)n0 * scale_row, (uint32_t)rows * scale_row);
     tl.s_off = (uint32_t)((rg * 32 + l32) % kRows) * scale_row + (uint32_t)((kp * 2 + half) * U) * (FMT == MOE_QUANT_NVFP4 ? 2u : 1u);
   }
-  const int all = (p.K + kSplitK - 1) / kSplitK, each = all / splits, more = all % splits;
-  const int first = split * each + min(split, more), S = each + (split < more ? 1 : 0);
+  constexpr int kUnit = split_unit(ROWS, TOK), kPer = kUnit / SK;      // steps of a unit
+  const int units = (p.K + kUnit - 1) / kUnit, each = units / splits, more = units % splits;
+  const int first = (split * each + min(split, more)) * kPer;
+  const int S = min((each + (split < more ? 1 : 0)) * kPer, (p.K + SK - 1) / SK - first);
   f32x16 acc[JT];
 #pragma unroll
   for (int j = 0; j < JT; ++j) acc[j] = f32x16{};
@@ -162,12 +178,11 @@ __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs
     constexpr int G = decltype(stage_c)::value, F = (G + NS - 1) % NS;
     wait_vm<(NS - 2) * Tile::kLoads>();                      // this wave's part of step s is here
     uint8_t* const stage = stage_at(stage_c);
-    const int left = p.K - (first + s) * kSplitK;
-    if (left < kSplitK) {                                    // what follows a token's row is not its
+    const int left = p.K - (first + s) * SK;
+    if (left < SK) {                                    // what follows a token's row is not its
 #pragma unroll
       for (int i = 0; i < Tile::XL; ++i) {
-        const int r = (i * kSplitWaves + wave) * 2 + half;
-        if ((l32 ^ (r & 15)) * 8 >= left)
+        if ((lane % kChunks ^ (token_row(i) & 15)) * 8 >= left)
           *reinterpret_cast<uint4*>(stage + (i * kSplitWaves + wave) * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
       }
     }
@@ -181,8 +196,8 @@ __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = (kp * 2 + half) * U + u;
-        if constexpr (FMT == MOE_QUANT_NVFP4) sb[u] = *reinterpret_cast<const uint16_t*>(sr + r * 16 + c * 2);
-        else sb[u] = sr[r * 8 + c];
+        if constexpr (FMT == MOE_QUANT_NVFP4) sb[u] = *reinterpret_cast<const uint16_t*>(sr + r * (SK / 16) + c * 2);
+        else sb[u] = sr[r * (SK / 32) + c];
       }
     } else {
 #pragma unroll
@@ -191,15 +206,15 @@ __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs
     bf16x8 af[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = ((kp * 2 + half) * U + u) ^ ((r >> 1) & 7);
-      dequant32<FMT>(*reinterpret_cast<const uint4*>(stage + Tile::kTokenBytes + r * 128 + c * 16), sb[u], af[u]);
+      const int c = ((kp * 2 + half) * U + u) ^ code_swizzle(r);
+      dequant32<FMT>(*reinterpret_cast<const uint4*>(stage + Tile::kTokenBytes + r * (SK / 2) + c * 16), sb[u], af[u]);
     }
 #pragma unroll
     for (int i = 0; i < 4 * U; ++i)
 #pragma unroll
       for (int j = 0; j < JT; ++j) {
         const int t = TOK < 32 ? l32 & (TOK - 1) : j * 32 + l32;
-        const bf16x8 b = *reinterpret_cast<const bf16x8*>(stage + t * 512 + ((((kp * 2 + half) * 4 * U + i) ^ (t & 15)) << 4));
+        const bf16x8 b = *reinterpret_cast<const bf16x8*>(stage + t * (SK * 2) + ((((kp * 2 + half) * 4 * U + i) ^ (t & 15)) << 4));
         acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[i / 4][i % 4], b, acc[j], 0, 0, 0);
       }
   };
@@ -291,24 +306,24 @@ struct SplitPlan {
 };
 
 // Rows of a tile and parts of the reduction, by the time they should take: one
-// workgroup a compute unit (LDS), `rounds` of them, their steps at the time
-// measured for a step, and for more than one part the join (its launch, and
+// workgroup a compute unit (LDS), `rounds` of them, their units at the time
+// measured for a unit, and for more than one part the join (its launch, and
 // its sums written and read).  T = 64 10240x2560: 13.1 us as 64 rows in one
 // part, 17.4 as 128 rows in three; T = 100, where 64 rows take two rounds:
 // 20.9 against 17.4 as 128 rows in one part.
 SplitPlan plan(bool gate_up, int T, int N, int K) {
   constexpr int kUnits = 256;
-  constexpr float kStep64[] = {0.75f, 0.92f}, kStep128[] = {1.2f, 1.4f};      // us, up to 32 and 64 tokens
+  constexpr float kStep64[] = {1.1f, 0.9f}, kStep128[] = {1.2f, 1.4f};       // us a unit, up to 32 and 64 tokens
   constexpr float kJoin = 3.5f, kJoinBytes = 5e6f;                            // us, and bytes a us
   SplitPlan best{};
-  const int tokens = T <= 16 ? 16 : T <= 32 ? 32 : 64, steps = (K + kSplitK - 1) / kSplitK;
+  const int tokens = T <= 16 ? 16 : T <= 32 ? 32 : 64;
   for (int rows = 64; rows <= (tokens == 16 ? 64 : 128); rows += 64) {
     const int own = gate_up ? rows / 2 : rows, row_tiles = (N + own - 1) / own;
-    const int tiles = row_tiles * ((T + tokens - 1) / tokens);
-    for (int splits = 1; splits <= kMaxSplits && splits <= steps; ++splits) {
+    const int tiles = row_tiles * ((T + tokens - 1) / tokens), unit = split_unit(rows, tokens), units = (K + unit - 1) / unit;
+    for (int splits = 1; splits <= kMaxSplits && splits <= units; ++splits) {
       if (splits > 1 && (long long)tiles * splits > kUnits) break;
       const int rounds = (tiles * splits + kUnits - 1) / kUnits;
-      float us = (float)rounds * (float)((steps + splits - 1) / splits) * (rows == 64 ? kStep64 : kStep128)[tokens > 32];
+      float us = (float)rounds * (float)((units + splits - 1) / splits) * (rows == 64 ? kStep64 : kStep128)[tokens > 32];
       if (splits > 1) us += kJoin + 8.0f * splits * (gate_up ? 2 : 1) * (float)T * (float)(row_tiles * own) / kJoinBytes;
       if (best.splits == 0 || us < best.us) best = {tokens, rows, row_tiles, tiles, splits, row_tiles * own, us};
     }
