@@ -23,6 +23,7 @@ from ._lib import (
     moe_route_topk,
     moe_step,
 )
+from .layer import RouteRule, moe_route_grouped, moe_route_grouped_bucket
 
 
 def expert_weights_from_numpy(bank, device) -> ExpertWeights:
@@ -42,15 +43,24 @@ class MoeStep:
     path "step": moe_step (the whole step in one call).  "packed":
     moe_step_packed, with the weights' packed copy passed to run().  "calls":
     moe_route_bucket then moe_expert_ffn.  "calls_unfused": moe_route_topk,
-    moe_bucket_routes, moe_expert_ffn.  All of them produce the same outputs."""
+    moe_bucket_routes, moe_expert_ffn.  All of them produce the same outputs.
+    With a `rule` (of the same k; "calls" and "calls_unfused" only) the experts
+    are chosen by moe_route_grouped_bucket or moe_route_grouped in place of
+    moe_route_bucket and moe_route_topk."""
 
     PATHS = ("step", "packed", "calls", "calls_unfused")
 
-    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, path: str = "step"):
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, path: str = "step",
+                 rule: Optional[RouteRule] = None):
         if path not in self.PATHS:
             raise ValueError(f"path must be one of {self.PATHS}")
+        if rule is not None and path not in ("calls", "calls_unfused"):
+            raise ValueError('a rule is used on paths "calls" and "calls_unfused"')
+        if rule is not None and rule.k != k:
+            raise ValueError(f"rule.k must be k={k}, got {rule.k}")
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         self.path = path
+        self.rule = rule
         self.device = torch.device(device)
         self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=self.device)
         self.topk_w = torch.empty((T, k), dtype=torch.float32, device=self.device)
@@ -59,13 +69,19 @@ class MoeStep:
         self.y = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
 
     def route(self, logits: torch.Tensor, bias: Optional[torch.Tensor]):
-        moe_route_topk(logits, bias, self.k, self.topk_idx, self.topk_w)
+        if self.rule is not None:
+            moe_route_grouped(logits, bias, self.rule, self.topk_idx, self.topk_w)
+        else:
+            moe_route_topk(logits, bias, self.k, self.topk_idx, self.topk_w)
 
     def bucket(self):
         moe_bucket_routes(self.topk_idx, self.E, self.buckets)
 
     def route_bucket(self, logits: torch.Tensor, bias: Optional[torch.Tensor]):
-        moe_route_bucket(logits, bias, self.k, self.topk_idx, self.topk_w, self.buckets)
+        if self.rule is not None:
+            moe_route_grouped_bucket(logits, bias, self.rule, self.topk_idx, self.topk_w, self.buckets)
+        else:
+            moe_route_bucket(logits, bias, self.k, self.topk_idx, self.topk_w, self.buckets)
 
     def routing(self, logits: torch.Tensor, bias: Optional[torch.Tensor]):
         if self.path == "calls_unfused":

@@ -126,3 +126,12 @@ def test_binding_refusals():
         sme.QuantWeight(torch.zeros((4, 16), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8))
     with pytest.raises(TypeError, match="codes"):
         sme.QuantWeight(torch.zeros(16, dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8))
+
+
+def test_step_refusals():
+    rule = sme.RouteRule(4)
+    for path in ("step", "packed"):
+        with pytest.raises(ValueError, match="rule"):
+            sme.MoeStep(2, 64, 64, 8, 4, "cpu", path=path, rule=rule)
+    with pytest.raises(ValueError, match="rule.k"):
+        sme.MoeStep(2, 64, 64, 8, 2, "cpu", path="calls", rule=rule)

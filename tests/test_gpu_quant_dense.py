@@ -197,6 +197,37 @@ def test_other_stream():
     assert_near(f64(y), ref, linear_tolerance(ref, mag, 512), "side stream")
 
 
+@pytest.mark.parametrize("path", ["calls", "calls_unfused"])
+def test_step_with_rule(path):
+    """MoeStep with a rule against the operators called one by one: the same bits, eager and replayed on new inputs."""
+    from gpu_harness import device_weights, x_bits
+    from moe_inputs import make_workload
+    wl = make_workload("tiny")
+    T, H, I, E, k = wl.T, wl.H, wl.I, wl.E, wl.k
+    rule = sme.RouteRule(k, "softmax", 4, 2, 1, False, 2.0)
+    x, logits, bank = x_bits(wl.x), to_dev(wl.logits), device_weights(wl.bank)
+    bias = to_dev(np.linspace(-0.1, 0.1, E, dtype=np.float32))
+    step = sme.MoeStep(T, H, I, E, k, DEV, path=path, rule=rule)
+
+    def check():
+        torch.cuda.synchronize()
+        idx, w, b = sme.moe_route_grouped_bucket(logits, bias, rule)
+        y = sme.moe_expert_ffn(x, bank, w, b, sme.make_workspace(T, H, I, E, k, DEV))
+        torch.cuda.synchronize()
+        assert torch.equal(step.topk_idx, idx) and torch.equal(step.topk_w, w)
+        assert torch.equal(step.y.view(torch.int16), y.view(torch.int16))
+
+    step.run(x, logits, bias, bank)
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.run(x, logits, bias, bank)
+    for i in range(3):
+        logits.copy_(torch.roll(logits, 5 + i, 1))
+        graph.replay()
+        check()
+
+
 def test_layer():
     """A layer as a user runs it: grouped routing and its buckets, the routed experts, the 4-bit shared expert summed
     onto their output, and a 4-bit projection of the sum, each against the oracle on what the one before gave."""
