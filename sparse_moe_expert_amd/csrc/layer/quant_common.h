@@ -46,7 +46,6 @@ bool quant_tile_ok(bool gate_up, int T, int N);
 moe_status quant_tile(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
 bool quant_few_ok(bool gate_up, int T, int N, int K);
 moe_status quant_few(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
-moe_status quant_stream(int format, bool gate_up, const DenseArgs& p, hipStream_t s);
 
 namespace {
 
@@ -72,25 +71,25 @@ __device__ __forceinline__ uint32_t fp4x2_scaled(uint32_t word, float scale) {
   }
 }
 
-// 32 weights (16 code bytes and their scale bytes: two e4m3, or one e8m0) ->
-// four fragments of 8 bf16.
+// 8 weights (a dword of codes) -> a fragment.  sb: the scale bytes of their 32
+// (two e4m3, or one e8m0); `second`: of the second 16.
+template <int FMT>
+__device__ __forceinline__ bf16x8 dequant8(uint32_t c, uint32_t sb, bool second) {
+  float s;
+  if constexpr (FMT == MOE_QUANT_NVFP4)
+    s = second ? __builtin_amdgcn_cvt_f32_fp8((int)sb, 1) : __builtin_amdgcn_cvt_f32_fp8((int)sb, 0);
+  else
+    s = __uint_as_float(sb << 23);
+  return __builtin_bit_cast(bf16x8, make_uint4(fp4x2_scaled<FMT, 0>(c, s), fp4x2_scaled<FMT, 1>(c, s),
+                                               fp4x2_scaled<FMT, 2>(c, s), fp4x2_scaled<FMT, 3>(c, s)));
+}
+
+// 32 weights (16 code bytes and their scale bytes) -> four fragments
 template <int FMT>
 __device__ __forceinline__ void dequant32(const uint4 codes, uint32_t sb, bf16x8 (&fr)[4]) {
-  float s0, s1;
-  if constexpr (FMT == MOE_QUANT_NVFP4) {
-    s0 = __builtin_amdgcn_cvt_f32_fp8((int)sb, 0);
-    s1 = __builtin_amdgcn_cvt_f32_fp8((int)sb, 1);
-  } else {
-    s0 = s1 = __uint_as_float(sb << 23);
-  }
   const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float s = i < 2 ? s0 : s1;
-    const uint4 v = make_uint4(fp4x2_scaled<FMT, 0>(c[i], s), fp4x2_scaled<FMT, 1>(c[i], s),
-                               fp4x2_scaled<FMT, 2>(c[i], s), fp4x2_scaled<FMT, 3>(c[i], s));
-    fr[i] = __builtin_bit_cast(bf16x8, v);
-  }
+  for (int i = 0; i < 4; ++i) fr[i] = dequant8<FMT>(c[i], sb, i >= 2);
 }
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t bits) { return __uint_as_float(bits << 16); }

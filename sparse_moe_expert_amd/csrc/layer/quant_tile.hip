@@ -36,34 +36,67 @@ constexpr int kStages = 4, kLead = 2;
 constexpr int kStageBytes = kTileTokens * kTileK * 2;        // 16 KB
 constexpr int kXcds = 8;
 
-template <int FMT, bool GU>
+// WIDE: a row's scales of two steps are loaded at once, from a multiple of
+// four bytes; else step by step.
+template <int FMT, bool GU, bool WIDE>
 struct RowTile {
-  static constexpr int kLoads = 4 + 2 * 2;                   // a step's, per thread
+  static constexpr int kWeightLoads = 4 + (WIDE ? 2 : 4), kTokenLoads = 4;   // of two steps, of one
   __amdgpu_buffer_rsrc_t rc[GU ? 2 : 1], rs[GU ? 2 : 1], rx;
   uint32_t c_off[2], s_off[2], x_off[4];
+  int half;
   uint4 wc[kStages][2];
-  uint16_t ws[kStages][2];                                   // 16 bits until used: a widening would wait for its load
+  uint2 wide[kStages / 2][2];
+  uint16_t narrow[kStages][2];                               // 16 bits until used: a widening would wait for its load
 
+  // Codes and scales of the steps a and b = a + 1, of stages S and S + 1: their
+  // lines are fetched once for both
   template <int S>
-  __device__ __forceinline__ void issue(uint8_t* stage, int wave, uint32_t step) {
+  __device__ __forceinline__ void issue_weights(uint32_t a, uint32_t b) {
+    constexpr bool kNv = FMT == MOE_QUANT_NVFP4;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const int r = GU ? m : 0;
-      wc[S][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rc[r], c_off[m] + step * 32u, 0, 0));
-      if constexpr (FMT == MOE_QUANT_NVFP4)
-        ws[S][m] = __builtin_amdgcn_raw_buffer_load_b16(rs[r], s_off[m] + step * 4u, 0, 0);
-      else
-        ws[S][m] = __builtin_amdgcn_raw_buffer_load_b8(rs[r], s_off[m] + step * 2u, 0, 0);
+      wc[S][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rc[r], c_off[m] + a * 32u, 0, 0));
+      wc[S + 1][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rc[r], c_off[m] + b * 32u, 0, 0));
+      if constexpr (WIDE && kNv) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs[r], s_off[m] + a * 4u, 0, 0);
+        wide[S / 2][m] = make_uint2(v[0], v[1]);
+      } else if constexpr (WIDE) {
+        wide[S / 2][m].x = __builtin_amdgcn_raw_buffer_load_b32(rs[r], s_off[m] + a * 2u, 0, 0);
+      } else if constexpr (kNv) {
+        narrow[S][m] = __builtin_amdgcn_raw_buffer_load_b16(rs[r], s_off[m] + a * 4u, 0, 0);
+        narrow[S + 1][m] = __builtin_amdgcn_raw_buffer_load_b16(rs[r], s_off[m] + b * 4u, 0, 0);
+      } else {
+        narrow[S][m] = __builtin_amdgcn_raw_buffer_load_b8(rs[r], s_off[m] + a * 2u, 0, 0);
+        narrow[S + 1][m] = __builtin_amdgcn_raw_buffer_load_b8(rs[r], s_off[m] + b * 2u, 0, 0);
+      }
     }
+  }
+  __device__ __forceinline__ void issue_tokens(uint8_t* stage, int wave, uint32_t step) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, stage + (i * 4 + wave) * 1024, 16, x_off[i] + step * 128u, 0, 0, 0);
   }
+
+  // Row tile m, group i (8 weights) of the step in `stage`: codes and scale
+  __device__ __forceinline__ uint32_t word(int stage, int m, int i) const {
+    const uint4 c = wc[stage][m];
+    return i == 0 ? c.x : i == 1 ? c.y : i == 2 ? c.z : c.w;
+  }
+  __device__ __forceinline__ float scale(int stage, int m, int i) const {
+    constexpr bool kNv = FMT == MOE_QUANT_NVFP4;
+    uint32_t sb;
+    if constexpr (!WIDE) sb = narrow[stage][m];
+    else if constexpr (kNv) sb = (stage & 1 ? wide[stage / 2][m].y : wide[stage / 2][m].x) >> (half * 16);
+    else sb = (wide[stage / 2][m].x >> ((stage & 1) * 16 + half * 8)) & 0xFFu;
+    if constexpr (kNv) return i < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)sb, 0) : __builtin_amdgcn_cvt_f32_fp8((int)sb, 1);
+    else return __uint_as_float(sb << 23);
+  }
 };
 
-template <int FMT, bool GU>
+template <int FMT, bool GU, bool WIDE>
 __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p, int row_tiles, int tiles) {
-  using Tile = RowTile<FMT, GU>;
+  using Tile = RowTile<FMT, GU, WIDE>;
   constexpr int kRows = GU ? 128 : 256;
   // one array per stage, so that reads of one stage are seen not to alias the
   // loads in flight to the others
@@ -86,6 +119,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
   const int rows = min(kRows, p.N - n0), toks = min(kTileTokens, p.T - t0);
 
   Tile tl;
+  tl.half = half;
   const uint32_t code_row = (uint32_t)p.K / 2, scale_row = (uint32_t)(p.K / kScaleGroup<FMT>);
 #pragma unroll
   for (int m = 0; m < (GU ? 2 : 1); ++m) {
@@ -98,7 +132,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
   for (int m = 0; m < 2; ++m) {
     const uint32_t row = (uint32_t)((GU ? 0 : m * 128) + wave * 32 + l32);
     tl.c_off[m] = row * code_row + (uint32_t)half * 16u;
-    tl.s_off[m] = row * scale_row + (uint32_t)half * (FMT == MOE_QUANT_NVFP4 ? 2u : 1u);
+    tl.s_off[m] = row * scale_row + (WIDE ? 0u : (uint32_t)half * (FMT == MOE_QUANT_NVFP4 ? 2u : 1u));
   }
   // piece i of a wave: 8 token rows of 128 bytes; rows past the last token repeat it
 #pragma unroll
@@ -115,14 +149,29 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
 
   // a step past the last one is issued out of range: it reads nothing
   auto at = [&](int s) { return s < steps ? (uint32_t)s : kOutside / 128u; };
-  tl.template issue<0>(s_0, wave, at(0));
+  tl.template issue_weights<0>(at(0), at(1));
   fence();
-  tl.template issue<1>(s_1, wave, at(1));
+  tl.issue_tokens(s_0, wave, at(0));
   fence();
+  tl.issue_tokens(s_1, wave, at(1));
+  fence();
+  bf16x8 af[2];                                              // the next products' weights
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const uint32_t c = tl.word(0, m, 0);
+    const float s = tl.scale(0, m, 0);
+    af[m] = __builtin_bit_cast(bf16x8, make_uint4(fp4x2_scaled<FMT, 0>(c, s), fp4x2_scaled<FMT, 1>(c, s),
+                                                  fp4x2_scaled<FMT, 2>(c, s), fp4x2_scaled<FMT, 3>(c, s)));
+  }
   auto body = [&](auto stage_c, int s) {
     constexpr int S = decltype(stage_c)::value, F = (S + kLead) % kStages;
-    tl.template issue<F>(F == 0 ? s_0 : F == 1 ? s_1 : F == 2 ? s_2 : s_3, wave, at(s + kLead));
-    wait_vm<kLead * Tile::kLoads>();                         // this wave's part of step s is here
+    if constexpr (S % 2 == 0) {
+      tl.template issue_weights<F>(at(s + kLead), at(s + kLead + 1));
+      fence();
+    }
+    tl.issue_tokens(F == 0 ? s_0 : F == 1 ? s_1 : F == 2 ? s_2 : s_3, wave, at(s + kLead));
+    // this wave's tokens of step s are here; since then two steps' tokens and one pair of weights
+    wait_vm<kLead * Tile::kTokenLoads + Tile::kWeightLoads>();
     uint8_t* const stage = S == 0 ? s_0 : S == 1 ? s_1 : S == 2 ? s_2 : s_3;
     if (p.K - s * kTileK < kTileK) {                         // half a step: what follows a token's row is not its
 #pragma unroll
@@ -134,21 +183,33 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
     }
     wait_lds();                                              // and its reads of step s-1 have returned
     barrier();
-    bf16x8 af[2][4];
+    __builtin_amdgcn_sched_barrier(0);
+    // Four groups of eight products, of all four token tiles also where the
+    // last ones are past T (branches around them would keep the products of a
+    // tile apart).  Under a group's products the next group's weights are
+    // decoded and its tokens read.
+    bf16x8 b[2][4];
+    auto read = [&](int i, int j) {
+      const int row = j * 32 + l32;
+      b[i & 1][j] = *reinterpret_cast<const bf16x8*>(stage + row * 128 + (((half * 4 + i) ^ ((row >> 1) & 7)) << 4));
+    };
 #pragma unroll
-    for (int m = 0; m < 2; ++m) dequant32<FMT>(tl.wc[S][m], tl.ws[S][m], af[m]);
-    // all four token tiles, also where the last ones are past T: branches
-    // around them would keep the products of a tile apart
+    for (int j = 0; j < 4; ++j) read(0, j);
+    for_each<4>([&](auto i_c) {
+      constexpr int i = decltype(i_c)::value;
+      uint32_t next[2][4];
+      for_each<8>([&](auto n_c) {
+        constexpr int n = decltype(n_c)::value, j = n / 2, m = n % 2, D = n % 4, W = n / 4;
+        if constexpr (i < 3 && m == 0) read(i + 1, j);
+        acc[m][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[m], b[i & 1][j], acc[m][j], 0, 0, 0);
+        const float s = tl.scale(i < 3 ? S : (S + 1) % kStages, W, (i + 1) % 4);
+        next[W][D] = fp4x2_scaled<FMT, D>(tl.word(i < 3 ? S : (S + 1) % kStages, W, (i + 1) % 4), s);
+        asm volatile("" : "+v"(next[W][D]));
+        __builtin_amdgcn_sched_barrier(0);
+      });
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = j * 32 + l32;
-        const bf16x8 b = *reinterpret_cast<const bf16x8*>(stage + row * 128 + (((half * 4 + i) ^ ((row >> 1) & 7)) << 4));
-#pragma unroll
-        for (int m = 0; m < 2; ++m) acc[m][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[m][i], b, acc[m][j], 0, 0, 0);
-      }
-    }
+      for (int m = 0; m < 2; ++m) af[m] = __builtin_bit_cast(bf16x8, make_uint4(next[m][0], next[m][1], next[m][2], next[m][3]));
+    });
   };
   int s0 = 0;
   for (; s0 + kStages <= steps; s0 += kStages) {
@@ -207,13 +268,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
   }
 }
 
-template <int FMT, bool GU>
+template <int FMT, bool GU, bool WIDE>
 moe_status launch(const DenseArgs& p, hipStream_t s) {
   constexpr int kRows = GU ? 128 : 256;
   const int row_tiles = (p.N + kRows - 1) / kRows;
   const int tiles = row_tiles * ((p.T + kTileTokens - 1) / kTileTokens);      // at most 2^26 (N and T up to 2^20)
   const int grid = (tiles + kXcds - 1) / kXcds * kXcds + (p.token_gate ? (p.T + 3) / 4 : 0);
-  quant_tile_kernel<FMT, GU><<<(unsigned)grid, kTileThreads, 0, s>>>(p, row_tiles, tiles);
+  quant_tile_kernel<FMT, GU, WIDE><<<(unsigned)grid, kTileThreads, 0, s>>>(p, row_tiles, tiles);
   return launch_status();
 }
 
@@ -225,9 +286,12 @@ bool quant_tile_ok(bool gate_up, int T, int N) {
 }
 
 moe_status quant_tile(int format, bool gate_up, const DenseArgs& p, hipStream_t s) {
-  if (format == MOE_QUANT_NVFP4)
-    return gate_up ? launch<MOE_QUANT_NVFP4, true>(p, s) : launch<MOE_QUANT_NVFP4, false>(p, s);
-  return gate_up ? launch<MOE_QUANT_MXFP4, true>(p, s) : launch<MOE_QUANT_MXFP4, false>(p, s);
+  if (format == MOE_QUANT_NVFP4) {
+    if (p.K % 64 == 0) return gate_up ? launch<MOE_QUANT_NVFP4, true, true>(p, s) : launch<MOE_QUANT_NVFP4, false, true>(p, s);
+    return gate_up ? launch<MOE_QUANT_NVFP4, true, false>(p, s) : launch<MOE_QUANT_NVFP4, false, false>(p, s);
+  }
+  if (p.K % 128 == 0) return gate_up ? launch<MOE_QUANT_MXFP4, true, true>(p, s) : launch<MOE_QUANT_MXFP4, false, true>(p, s);
+  return gate_up ? launch<MOE_QUANT_MXFP4, true, false>(p, s) : launch<MOE_QUANT_MXFP4, false, false>(p, s);
 }
 
 }  // namespace moe
