@@ -36,16 +36,16 @@ constexpr int kStages = 4, kLead = 2;
 constexpr int kStageBytes = kTileTokens * kTileK * 2;        // 16 KB
 constexpr int kXcds = 8;
 
-// WIDE: a row's scales of two steps are loaded at once, from a multiple of
+// WIDE: a row's scales of four steps are loaded at once, from a multiple of
 // four bytes; else step by step.
 template <int FMT, bool GU, bool WIDE>
 struct RowTile {
-  static constexpr int kWeightLoads = 4 + (WIDE ? 2 : 4), kTokenLoads = 4;   // of two steps, of one
+  static constexpr int kCodeLoads = 4, kTokenLoads = 4;      // of two steps, of one
   __amdgpu_buffer_rsrc_t rc[GU ? 2 : 1], rs[GU ? 2 : 1], rx;
   uint32_t c_off[2], s_off[2], x_off[4];
   int half;
   uint4 wc[kStages][2];
-  uint2 wide[kStages / 2][2];
+  uint4 wide[2][2];                                          // scales of this ring, of the next
   uint16_t narrow[kStages][2];                               // 16 bits until used: a widening would wait for its load
 
   // Codes and scales of the steps a and b = a + 1, of stages S and S + 1: their
@@ -58,17 +58,29 @@ struct RowTile {
       const int r = GU ? m : 0;
       wc[S][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rc[r], c_off[m] + a * 32u, 0, 0));
       wc[S + 1][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rc[r], c_off[m] + b * 32u, 0, 0));
-      if constexpr (WIDE && kNv) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs[r], s_off[m] + a * 4u, 0, 0);
-        wide[S / 2][m] = make_uint2(v[0], v[1]);
-      } else if constexpr (WIDE) {
-        wide[S / 2][m].x = __builtin_amdgcn_raw_buffer_load_b32(rs[r], s_off[m] + a * 2u, 0, 0);
+      if constexpr (WIDE) {
       } else if constexpr (kNv) {
         narrow[S][m] = __builtin_amdgcn_raw_buffer_load_b16(rs[r], s_off[m] + a * 4u, 0, 0);
         narrow[S + 1][m] = __builtin_amdgcn_raw_buffer_load_b16(rs[r], s_off[m] + b * 4u, 0, 0);
       } else {
         narrow[S][m] = __builtin_amdgcn_raw_buffer_load_b8(rs[r], s_off[m] + a * 2u, 0, 0);
         narrow[S + 1][m] = __builtin_amdgcn_raw_buffer_load_b8(rs[r], s_off[m] + b * 2u, 0, 0);
+      }
+    }
+  }
+  // The scales of four steps
+  template <int W>
+  __device__ __forceinline__ void issue_scales(uint32_t step) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int r = GU ? m : 0;
+        if constexpr (FMT == MOE_QUANT_NVFP4) {
+          wide[W][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rs[r], s_off[m] + step * 4u, 0, 0));
+        } else {
+          const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs[r], s_off[m] + step * 2u, 0, 0);
+          wide[W][m].x = v[0], wide[W][m].y = v[1];
+        }
       }
     }
   }
@@ -83,12 +95,13 @@ struct RowTile {
     const uint4 c = wc[stage][m];
     return i == 0 ? c.x : i == 1 ? c.y : i == 2 ? c.z : c.w;
   }
-  __device__ __forceinline__ float scale(int stage, int m, int i) const {
+  __device__ __forceinline__ float scale(int S, bool next, int m, int i) const {
     constexpr bool kNv = FMT == MOE_QUANT_NVFP4;
+    const uint4 w = wide[next][m];
     uint32_t sb;
-    if constexpr (!WIDE) sb = narrow[stage][m];
-    else if constexpr (kNv) sb = (stage & 1 ? wide[stage / 2][m].y : wide[stage / 2][m].x) >> (half * 16);
-    else sb = (wide[stage / 2][m].x >> ((stage & 1) * 16 + half * 8)) & 0xFFu;
+    if constexpr (!WIDE) sb = narrow[S][m];
+    else if constexpr (kNv) sb = (S == 0 ? w.x : S == 1 ? w.y : S == 2 ? w.z : w.w) >> (half * 16);
+    else sb = ((S < 2 ? w.x : w.y) >> (S % 2 * 16 + half * 8)) & 0xFFu;
     if constexpr (kNv) return i < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)sb, 0) : __builtin_amdgcn_cvt_f32_fp8((int)sb, 1);
     else return __uint_as_float(sb << 23);
   }
@@ -149,6 +162,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
 
   // a step past the last one is issued out of range: it reads nothing
   auto at = [&](int s) { return s < steps ? (uint32_t)s : kOutside / 128u; };
+  tl.template issue_scales<0>(at(0));
   tl.template issue_weights<0>(at(0), at(1));
   fence();
   tl.issue_tokens(s_0, wave, at(0));
@@ -159,19 +173,21 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const uint32_t c = tl.word(0, m, 0);
-    const float s = tl.scale(0, m, 0);
+    const float s = tl.scale(0, false, m, 0);
     af[m] = __builtin_bit_cast(bf16x8, make_uint4(fp4x2_scaled<FMT, 0>(c, s), fp4x2_scaled<FMT, 1>(c, s),
                                                   fp4x2_scaled<FMT, 2>(c, s), fp4x2_scaled<FMT, 3>(c, s)));
   }
   auto body = [&](auto stage_c, int s) {
     constexpr int S = decltype(stage_c)::value, F = (S + kLead) % kStages;
     if constexpr (S % 2 == 0) {
+      if constexpr (F == 0) tl.template issue_scales<1>(at(s + kLead));
       tl.template issue_weights<F>(at(s + kLead), at(s + kLead + 1));
       fence();
     }
     tl.issue_tokens(F == 0 ? s_0 : F == 1 ? s_1 : F == 2 ? s_2 : s_3, wave, at(s + kLead));
-    // this wave's tokens of step s are here; since then two steps' tokens and one pair of weights
-    wait_vm<kLead * Tile::kTokenLoads + Tile::kWeightLoads>();
+    // this wave's tokens of step s are here; since then two steps' tokens,
+    // the codes of a pair of steps, and scales
+    wait_vm<kLead * Tile::kTokenLoads + Tile::kCodeLoads + (!WIDE ? 4 : S < 2 ? 0 : 2)>();
     uint8_t* const stage = S == 0 ? s_0 : S == 1 ? s_1 : S == 2 ? s_2 : s_3;
     if (p.K - s * kTileK < kTileK) {                         // half a step: what follows a token's row is not its
 #pragma unroll
@@ -202,7 +218,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
         constexpr int n = decltype(n_c)::value, j = n / 2, m = n % 2, D = n % 4, W = n / 4;
         if constexpr (i < 3 && m == 0) read(i + 1, j);
         acc[m][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[m], b[i & 1][j], acc[m][j], 0, 0, 0);
-        const float s = tl.scale(i < 3 ? S : (S + 1) % kStages, W, (i + 1) % 4);
+        const float s = tl.scale(i < 3 ? S : (S + 1) % kStages, i == 3 && S == 3, W, (i + 1) % 4);
         next[W][D] = fp4x2_scaled<FMT, D>(tl.word(i < 3 ? S : (S + 1) % kStages, W, (i + 1) % 4), s);
         asm volatile("" : "+v"(next[W][D]));
         __builtin_amdgcn_sched_barrier(0);
@@ -217,6 +233,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
     body(std::integral_constant<int, 1>{}, s0 + 1);
     body(std::integral_constant<int, 2>{}, s0 + 2);
     body(std::integral_constant<int, 3>{}, s0 + 3);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) tl.wide[0][m] = tl.wide[1][m];
   }
   if (s0 < steps) body(std::integral_constant<int, 0>{}, s0);
   if (s0 + 1 < steps) body(std::integral_constant<int, 1>{}, s0 + 1);
