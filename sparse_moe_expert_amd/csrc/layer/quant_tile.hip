@@ -10,9 +10,17 @@
 // index is permuted alike in both: in a step of 64 the lane half h covers
 // 32h .. 32h+32, so that a lane's codes of a step are one 16-byte load.
 //
+// What it waits for is L1: every compute unit fetches a 128-byte line for each
+// row's codes and scales of a step, and with two workgroups there those are
+// out again before the next step asks for the rest of the line.  So a row's
+// codes of two steps are loaded together, and its scales of four: 4096^3
+// (NVFP4) 140 us loaded step by step, 128 with both by twos, 121 so; more do
+// not fit the registers.  A bf16 library product of the size takes 106 us (of
+// which 35 us power: it takes 67 us on zeros).
+//
 // Tokens go straight to a ring of four LDS stages (16-byte chunk c of token
 // row r at c ^ ((r >> 1) & 7): the reads of 16 lanes hit all banks), codes and
-// scales to a ring of registers, all issued two steps ahead.  With two stages
+// scales to rings of registers, issued two steps ahead.  With two stages
 // more than steps in flight one barrier a step is enough: the stage that step
 // s fills was read in step s-2, and a wave passes step s-1's barrier only when
 // every wave's reads of s-2 have returned.
@@ -298,9 +306,14 @@ moe_status launch(const DenseArgs& p, hipStream_t s) {
 
 }  // namespace
 
+// Fewer tiles than this leave too many compute units idle, and the split
+// kernel's smaller ones take less.  4096x4096, 128 tiles: 61.4 us and 47.2
+// split; 160 tiles: 61.7 and 65.1; 240 tiles: 66.3 and 87.1.
+constexpr long long kEnoughTiles = 160;
+
 bool quant_tile_ok(bool gate_up, int T, int N) {
   const int rows = gate_up ? 128 : 256;
-  return T > 64 && (long long)((N + rows - 1) / rows) * ((T + kTileTokens - 1) / kTileTokens) >= 256;
+  return T > 64 && (long long)((N + rows - 1) / rows) * ((T + kTileTokens - 1) / kTileTokens) >= kEnoughTiles;
 }
 
 moe_status quant_tile(int format, bool gate_up, const DenseArgs& p, hipStream_t s) {

@@ -27,6 +27,7 @@ LINEAR = [
     (8, 70, 32736),
     # enough tiles of 256 rows by 128 tokens for the chip: partial ones, and either side of a multiple of eight
     (700, 11000, 96), (600, 13200, 1056), (300, 22000, 64), (1025, 7300, 160), (33000, 260, 32),
+    (650, 11000, 640), (300, 16384, 448), (1300, 4090, 1152),
 ]
 
 
@@ -89,6 +90,7 @@ SHARED = [
     (20, 8224, 1056, True, True), (70, 4160, 2112, False, True), (150, 1056, 4192, True, False),
     (24, 512, 8288, True, False), (30, 544, 8416, False, True), (90, 512, 5216, True, True), (90, 544, 5216, False, False),
     (300, 96, 2080, True, True), (9, 5152, 96, True, True), (4100, 2080, 1024, True, True), (1301, 96, 3008, True, False),
+    (1300, 640, 3008, True, True), (1281, 896, 2080, False, True),
 ]
 
 
