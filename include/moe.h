@@ -566,8 +566,10 @@ typedef enum {
  *   the k of largest c are chosen, in that order;
  *   topk_w[t,j] = scale * s_j, divided by the sum of the chosen s where
  *   renormalise is not 0 (0 where that sum is 0).
- * Equal values go to the lower id, of groups and of experts.  Scores, choice
- * values and sums are computed in fp64 and the weights rounded once to fp32.
+ * Equal values go to the lower id, of groups and of experts.  The choice is
+ * that of scores, choice values and sums in fp64 (fp32 ones decide where they
+ * differ by more than their error); the weights are computed in fp64 and
+ * rounded once to fp32.
  *
  * Masks: an expert is masked where its logit or its bias is NaN or at or
  * below -3.3e38 (so -inf and the lowest value of fp32 and of bf16).  Masked
@@ -628,9 +630,9 @@ typedef enum {
 } moe_quant_format;
 
 /*
- * Bytes of device workspace moe_quant_linear needs: 0 for up to four tokens
- * and for batches whose output tiles fill the chip; else the fp32 sums of the
- * parts that the reduction is split into.
+ * Bytes of device workspace moe_quant_linear needs: the fp32 sums of the parts
+ * that the reduction is split into; 0 where it is not split, as for up to four
+ * tokens with K <= 8192 and for batches whose output tiles fill the chip.
  */
 size_t moe_quant_linear_workspace_size(int T, int N, int K);
 

@@ -24,8 +24,12 @@
 //
 // Tokens in LDS: a kilobyte for a token's step, its 16-byte chunk c at c ^ t
 // for token t, so that the reads of 16 lanes hit all banks.  Batches of more
-// than 16 tokens are workgroups of 16 each, while the weights are so small
+// than 16 tokens are workgroups of 8 or 16 each, while the weights are so small
 // that reading them again costs less than joining a split reduction.
+//
+// T = 1 4096x12288 shared expert (MXFP4, 80 MB): 16.6 us, 4.8 TB/s, as a large
+// copy; T = 1 9999x4096 7.4 us (23 MB); T = 4 10240x2560 (MXFP4, 14 MB) 5.7 us,
+// T = 1 2048x2048 3.0 us, of which 2.5 a launch.
 #include "quant_common.h"
 
 #include <type_traits>

@@ -26,6 +26,11 @@
 // With more than one part (`splits`) the workgroups leave fp32 sums in the
 // workspace, [part][matrix][T][Np] (Np: N rounded up to whole tiles), and
 // quant_join_kernel adds them in order and finishes the outputs.
+//
+// Bound by the steps, each a barrier with one workgroup a compute unit, more
+// than by bytes: T = 32 9999x4096 13.2 us, of which 8 steps on 157 of the 256
+// compute units are 9 (the weights, 23 MB, take 4.8 us at the rate of a copy);
+// splitting each tile in two takes a unit's time off and adds the join's.
 #include "quant_common.h"
 
 #include <type_traits>

@@ -6,10 +6,14 @@
 //   G_g = sum of the group_top largest c of group g (its unmasked experts),
 //   the groups_kept groups of largest G, in them the k experts of largest c,
 //   w_j = scale * s_j  (/ sum_i s_i over the chosen, where renormalised).
-// Equal values go to the lower id, of groups and of experts.  Scores and
-// choice values are held in 64 bits: sums s + b of different experts often
-// agree to 32 bits, and which expert is taken would hang on the last bit of an
-// exponential.
+// Equal values go to the lower id, of groups and of experts.  The choice is
+// that of scores and choice values in 64 bits (sums s + b of different experts
+// often agree to 32 bits, and which expert is taken would hang on the last bit
+// of an exponential); route_rule.h has how fp32 decides most of it.
+//
+// Bound by latency: one token of 256 experts takes 6 us, of which 2.5 are the
+// launch, to read a kilobyte; 4096 tokens of 512 experts 20 us, 11 of them the
+// selection (2 at the rate of a copy) and the rest the buckets.
 //
 // A few tokens: one workgroup selects (a wavefront a token) and buckets; a
 // larger batch selects over the chip, then buckets in a workgroup for each
