@@ -47,7 +47,20 @@ def _tensor(t, name: str, dtype, shape, device, index: int):
         _need(t, name, dtype, shape, device)
 
 
-class RouteRule:
+class _Fixed:
+    """Checked when made, so not to be changed afterwards."""
+
+    __slots__ = ()
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__} cannot be changed; make another")
+
+    def _set(self, **values):
+        for name, value in values.items():
+            object.__setattr__(self, name, value)
+
+
+class RouteRule(_Fixed):
     """How moe_route_grouped selects: k experts by `score` ("softmax" or
     "sigmoid") plus the bias, from the `groups_kept` best of `groups` groups (a
     group's value: the sum of its `group_top` best), weights renormalised over
@@ -59,10 +72,9 @@ class RouteRule:
                  group_top: int = 2, renormalise: bool = True, scale: float = 1.0):
         if score not in _SCORES:
             raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
-        self.k, self.score, self.groups = int(k), score, int(groups)
-        self.groups_kept = self.groups if groups_kept is None else int(groups_kept)
-        self.group_top, self.renormalise, self.scale = int(group_top), bool(renormalise), float(scale)
-        self._args = (_SCORES[score], self.groups, self.groups_kept, self.group_top, int(self.renormalise), self.scale)
+        self._set(k=int(k), score=score, groups=int(groups), group_top=int(group_top), renormalise=bool(renormalise),
+                  scale=float(scale), groups_kept=int(groups if groups_kept is None else groups_kept))
+        self._set(_args=(_SCORES[score], self.groups, self.groups_kept, self.group_top, int(self.renormalise), self.scale))
 
 
 def _route_args(logits, bias, rule, topk_idx, topk_w):
@@ -114,7 +126,7 @@ def moe_route_grouped_bucket(logits: torch.Tensor, bias: Optional[torch.Tensor],
     return topk_idx, topk_w, b
 
 
-class QuantWeight:
+class QuantWeight(_Fixed):
     """A dense 4-bit matrix [N, K] on the device: `codes` uint8 [N, K/2],
     `scales` uint8 [N, K/16] ("nvfp4") or [N, K/32] ("mxfp4") and the global
     scale, fp32 [1] (None: 1, "mxfp4" only)."""
@@ -125,20 +137,20 @@ class QuantWeight:
                  format: str = "nvfp4"):
         if format not in _FORMATS:
             raise ValueError(f"format must be one of {tuple(_FORMATS)}, got {format!r}")
-        self._format, group = _FORMATS[format]
+        number, group = _FORMATS[format]
         if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
             raise TypeError("codes must be a [N, K/2] tensor")
-        self.N, self.K, self.device = codes.shape[0], 2 * codes.shape[1], codes.device
-        if self.K % 32 != 0 or self.K == 0 or self.N == 0:
-            raise ValueError(f"a 4-bit matrix needs N >= 1 and K a multiple of 32, got N={self.N}, K={self.K}")
-        _need(codes, "codes", torch.uint8, None, self.device)
-        _need(scales, "scales", torch.uint8, (self.N, self.K // group), self.device)
+        N, K, device = codes.shape[0], 2 * codes.shape[1], codes.device
+        if K % 32 != 0 or K == 0 or N == 0:
+            raise ValueError(f"a 4-bit matrix needs N >= 1 and K a multiple of 32, got N={N}, K={K}")
+        _need(codes, "codes", torch.uint8, None, device)
+        _need(scales, "scales", torch.uint8, (N, K // group), device)
         if g_scale is not None:
-            _need(g_scale, "g_scale", torch.float32, (1,), self.device)
+            _need(g_scale, "g_scale", torch.float32, (1,), device)
         elif format == "nvfp4":
             raise ValueError("nvfp4 weights need their global scale (g_scale)")
-        self.codes, self.scales, self.g_scale, self.format = codes, scales, g_scale, format
-        self._index = codes.get_device()
+        self._set(codes=codes, scales=scales, g_scale=g_scale, format=format, N=N, K=K, device=device, _format=number,
+                  _index=codes.get_device())
 
     @property
     def shape(self):
@@ -178,10 +190,12 @@ def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.
     elif T > 4 or weight.K > 8192:                   # no workspace below that
         need = load_library().moe_quant_linear_workspace_size(T, N, weight.K)
         workspace = torch.empty((need,), dtype=_U8, device=dev) if need else None
-    _call("moe_quant_linear", index, weight._format, x.data_ptr(), *weight._ptrs(),
+    x_at, y_at = x.data_ptr(), y.data_ptr()
+    if x_at == y_at and T > 0:
+        raise ValueError("y must not be x: its rows are written while x is read")
+    _call("moe_quant_linear", index, weight._format, x_at, *weight._ptrs(),
           None if bias is None else bias.data_ptr(), T, N, weight.K,
-          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-          y.data_ptr())
+          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), y_at)
     return y
 
 
@@ -220,7 +234,10 @@ def moe_quant_shared_expert(x: torch.Tensor, gate: QuantWeight, up: QuantWeight,
         workspace = make_quant_shared_workspace(T, H, Is, dev)
     else:
         _tensor(workspace, "workspace", _U8, workspace.shape, dev, index)
-    _call("moe_quant_shared_expert", index, gate._format, x.data_ptr(), *gate._ptrs(), *up._ptrs(), *down._ptrs(),
+    x_at, y_at = x.data_ptr(), y.data_ptr()
+    if x_at == y_at and T > 0:
+        raise ValueError("y must not be x: its rows are written while x is read")
+    _call("moe_quant_shared_expert", index, gate._format, x_at, *gate._ptrs(), *up._ptrs(), *down._ptrs(),
           None if token_gate is None else token_gate.data_ptr(), None if add is None else add.data_ptr(),
-          T, H, Is, workspace.data_ptr(), workspace.numel(), y.data_ptr())
+          T, H, Is, workspace.data_ptr(), workspace.numel(), y_at)
     return y

@@ -112,6 +112,8 @@ def test_binding_refusals():
         sme.RouteRule(4, score="tanh")
     rule = sme.RouteRule(2)
     assert (rule.groups, rule.groups_kept, rule.group_top) == (1, 1, 2)
+    with pytest.raises(AttributeError, match="RouteRule"):
+        rule.scale = 2.0
     with pytest.raises(TypeError, match="logits"):
         sme.moe_route_grouped(torch.zeros(8), None, rule)
     with pytest.raises(TypeError, match="float32 or bfloat16"):

@@ -116,6 +116,26 @@ def test_shared(T, H, Is, gated, add, fmt):
     assert torch.equal(out.view(torch.int16), y.view(torch.int16))
 
 
+@pytest.mark.parametrize("T,N,K", [(4, 70, 96), (12, 70, 608), (40, 300, 8224), (130, 2600, 4160), (700, 11000, 96)])
+def test_linear_nonfinite_tokens(T, N, K):
+    """A token of infinities or NaN is its own row's matter: the others keep their bits, those before it too, whose
+    last step of the reduction runs into its row."""
+    rng = np.random.default_rng(T)
+    x = torch.from_numpy(rng.standard_normal((T, K))).to(DEV, torch.bfloat16)
+    bad = [1, T // 2, T - 1]
+    for fmt in ("nvfp4", "mxfp4"):
+        w = handle(weight(rng, N, K, fmt), fmt)
+        clean = sme.moe_quant_linear(x, w)
+        dirty = x.clone()
+        for t, v in zip(bad, (float("inf"), float("nan"), float("-inf"))):
+            dirty[t] = v
+        y = sme.moe_quant_linear(dirty, w)
+        rest = torch.ones(T, dtype=torch.bool, device=DEV)
+        rest[bad] = False
+        assert torch.equal(y[rest].view(torch.int16), clean[rest].view(torch.int16)), fmt
+        assert not torch.isfinite(y[bad].float()).all()
+
+
 def test_no_tokens():
     rng = np.random.default_rng(0)
     w = handle(weight(rng, 64, 64, "nvfp4"), "nvfp4")
@@ -140,6 +160,13 @@ def test_refusals():
     with pytest.raises(sme.MoeError) as e:                       # a misaligned view
         sme.moe_quant_linear(torch.zeros(65, dtype=torch.bfloat16, device=DEV)[1:].view(2, 32), w)
     assert e.value.status == 4
+    with pytest.raises(AttributeError, match="QuantWeight"):
+        w.codes = w.codes[:1]
+    square = handle(weight(rng, 32, 32, "nvfp4"), "nvfp4")
+    with pytest.raises(ValueError, match="y must not be x"):
+        sme.moe_quant_linear(x, square, None, x)
+    with pytest.raises(ValueError, match="y must not be x"):
+        sme.moe_quant_shared_expert(x, square, square, square, y=x)
     with pytest.raises(ValueError, match="global scale"):
         sme.QuantWeight(w.codes, w.scales)
     with pytest.raises(ValueError, match="scales"):
@@ -180,6 +207,43 @@ def test_graph_replays():
         torch.cuda.synchronize()
         assert torch.equal(y.view(torch.int16), z.view(torch.int16))
         assert torch.equal(p.view(torch.int16), sme.moe_quant_linear(x, hg).view(torch.int16))
+
+
+def test_split_captured_and_on_two_streams():
+    """A split reduction whose workspace the call allocates: captured and replayed, two such graphs in turn, and two
+    calls at once on streams of their own."""
+    rng = np.random.default_rng(21)
+    T, N, K = 40, 300, 8224
+    assert sme.moe_quant_linear_workspace_size(T, N, K) > 0
+    w = handle(weight(rng, N, K, "nvfp4"), "nvfp4")
+    xs = [torch.from_numpy(rng.standard_normal((T, K))).to(DEV, torch.bfloat16) for _ in range(2)]
+    want = [sme.moe_quant_linear(x, w) for x in xs]
+    torch.cuda.synchronize()
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))  # noqa: E731
+    graphs, outs, held = [], [], [x.clone() for x in xs]
+    for x in held:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(sme.moe_quant_linear(x, w))
+    for i in range(4):
+        swap = i % 2
+        held[0].copy_(xs[swap])
+        held[1].copy_(xs[1 - swap])
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert same(outs[0], want[swap]) and same(outs[1], want[1 - swap])
+        assert same(sme.moe_quant_linear(xs[0], w), want[0])
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                got.append(sme.moe_quant_linear(x, w))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert same(y, want[i % 2])
 
 
 def test_other_stream():
