@@ -252,6 +252,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
   // Sums to LDS as fp32, then whole 16-byte pieces of output rows.  One array
   // takes 32 tokens x 128 rows, chunk c of four rows of token t at c ^ (t & 15).
   constexpr int kRound = GU ? 4 : 2;                         // token tiles a round
+  const float g = !GU && p.a.g ? *p.a.g : 1.0f;
 #pragma unroll
   for (int j0 = 0; j0 < 4; j0 += kRound) {
     if (j0 * 32 >= toks) break;
@@ -280,13 +281,58 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
       }
     }
     __syncthreads();
-    const int pieces = min(toks - j0 * 32, kRound * 32) * (kRows / 8);
+    auto array = [&](int tok, int row) -> const uint8_t* {
+      const int a = GU ? tok >> 5 : (tok >> 5) * 2 + (row >> 7);
+      return (a == 0 ? s_0 : a == 1 ? s_1 : a == 2 ? s_2 : s_3) + (tok & 31) * 512;
+    };
+    const int here = min(toks - j0 * 32, kRound * 32);
+    if (p.N % 8 != 0) {
+      // Output rows that do not start at 16 bytes: pieces of eight that do,
+      // which begin up to seven rows before the tile, the outer ones one by
+      // one.  2048x4095x4096: 79.5 us, 92 with all outputs one by one (N = 4096: 71).
+      constexpr int kPieces = kRows / 8 + 1;
+      for (int i = tid; i < here * kPieces; i += kTileThreads) {
+        const int tok = i / kPieces, t = t0 + j0 * 32 + tok;
+        const size_t at = (size_t)t * p.N + n0;
+        const int r0 = i % kPieces * 8 - (int)(at & 7);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = min(max(r0 + k, 0), kRows - 1);
+          v[k] = *reinterpret_cast<const float*>(array(tok, row) + ((((row & 127) >> 2) ^ (tok & 15)) << 4) + (row & 3) * 4);
+        }
+        if constexpr (!GU) {
+          const float gate = p.gate ? p.gate[t] : 1.0f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int row = min(max(r0 + k, 0), rows - 1);
+            if (p.bias) v[k] = v[k] * g + bf16_to_f32(p.bias[n0 + row]);
+            else v[k] *= g;
+            v[k] *= gate;
+            if (p.add) v[k] += bf16_to_f32(p.add[at + row]);
+          }
+        }
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = f32_to_bf16_rne(v[k]);
+        if (r0 >= 0 && r0 + 8 <= rows) {
+          *reinterpret_cast<uint4*>(p.y + at + r0) =
+              make_uint4(o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (r0 + k >= 0 && r0 + k < rows) p.y[at + r0 + k] = (uint16_t)o[k];
+        }
+      }
+      continue;
+    }
+    const int pieces = here * (kRows / 8);
     for (int i = tid; i < pieces; i += kTileThreads) {
       const int tok = i / (kRows / 8), piece = i % (kRows / 8);        // a token's eight rows
       const int n = n0 + piece * 8, t = t0 + j0 * 32 + tok;
       if (n >= p.N) continue;
-      const int a = GU ? tok >> 5 : (tok >> 5) * 2 + (piece >> 4), c = (piece & 15) * 2;
-      const uint8_t* const in = (a == 0 ? s_0 : a == 1 ? s_1 : a == 2 ? s_2 : s_3) + (tok & 31) * 512;
+      const int c = (piece & 15) * 2;
+      const uint8_t* const in = array(tok, piece * 8);
       const f32x4 lo = *reinterpret_cast<const f32x4*>(in + ((c ^ (tok & 15)) << 4));
       const f32x4 hi = *reinterpret_cast<const f32x4*>(in + (((c + 1) ^ (tok & 15)) << 4));
       write8<GU>(p, t, n, lo, hi);
