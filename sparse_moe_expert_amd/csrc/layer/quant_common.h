@@ -114,32 +114,32 @@ __device__ __forceinline__ void token_gate_row(const DenseArgs& p, int t, int la
 
 // One output from its sum (and for a gate/up pair the other's)
 template <bool GU>
-__device__ __forceinline__ float output(const DenseArgs& p, int t, int n, float a, float b) {
+__device__ __forceinline__ void write1(const DenseArgs& p, int t, int n, float a, float b) {
+  const size_t at = (size_t)t * p.N + n;
   a = p.a.g ? a * *p.a.g : a;
   if constexpr (GU) {
     b = p.b.g ? b * *p.b.g : b;
-    return silu(a) * b;
+    a = silu(a) * b;
   } else {
     if (p.bias) a += bf16_to_f32(p.bias[n]);
     if (p.gate) a *= p.gate[t];
-    if (p.add) a += bf16_to_f32(p.add[(size_t)t * p.N + n]);
-    return a;
+    if (p.add) a += bf16_to_f32(p.add[at]);
   }
+  p.y[at] = (uint16_t)f32_to_bf16_rne(a);
 }
 
-template <bool GU>
-__device__ __forceinline__ void write1(const DenseArgs& p, int t, int n, float a, float b) {
-  p.y[(size_t)t * p.N + n] = (uint16_t)f32_to_bf16_rne(output<GU>(p, t, n, a, b));
-}
+// A matrix's global scale
+__device__ __forceinline__ float global_scale(const QuantMat& w) { return w.g ? *w.g : 1.0f; }
 
-// y[t, n .. n+3], rows at or past N left alone.  All loads come before the
-// first store: the compiler moves none across it (T = 32 9999x4096: XX us, 13.2
+// y[t, n .. n+3] from sums and the global scales; rows at or past N are left
+// alone.  All loads come before the
+// first store: the compiler moves none across it (T = 32 9999x4096: 12.6 us, 13.1
 // output by output).
 template <bool GU>
-__device__ __forceinline__ void write4(const DenseArgs& p, int t, int n, f32x4 a, f32x4 b) {
+__device__ __forceinline__ void write4(const DenseArgs& p, int t, int n, f32x4 a, f32x4 b, float ga, float gb) {
   if (n >= p.N) return;
   const size_t at = (size_t)t * p.N;
-  const float ga = p.a.g ? *p.a.g : 1.0f, gb = GU && p.b.g ? *p.b.g : 1.0f, gate = !GU && p.gate ? p.gate[t] : 1.0f;
+  const float gate = !GU && p.gate ? p.gate[t] : 1.0f;
   uint32_t v[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -166,11 +166,11 @@ __device__ __forceinline__ void write4(const DenseArgs& p, int t, int n, f32x4 a
 // y[t, n .. n+7] from sums (of a gate/up pair: from its outputs), N a
 // multiple of 8, n < N
 template <bool GU>
-__device__ __forceinline__ void write8(const DenseArgs& p, int t, int n, f32x4 lo, f32x4 hi) {
+__device__ __forceinline__ void write8(const DenseArgs& p, int t, int n, f32x4 lo, f32x4 hi, float g) {
   float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   const size_t at = (size_t)t * p.N + n;
   if constexpr (!GU) {
-    const float g = p.a.g ? *p.a.g : 1.0f, gate = p.gate ? p.gate[t] : 1.0f;
+    const float gate = p.gate ? p.gate[t] : 1.0f;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const uint4 bias = p.bias ? *reinterpret_cast<const uint4*>(p.bias + n) : zero;
     const uint4 add = p.add ? *reinterpret_cast<const uint4*>(p.add + at) : zero;

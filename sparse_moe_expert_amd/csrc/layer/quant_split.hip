@@ -134,6 +134,7 @@ __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs
   // LDS places: chunk c of row r's codes at c ^ code_swizzle(r)
   auto code_swizzle = [](int r) { return SK == 256 ? (r >> 1) & 7 : r & 15; };
   auto token_row = [&](int i) { return (i * kSplitWaves + wave) * (kWave / kChunks) + lane / kChunks; };
+  const float ga = global_scale(p.a), gb = GU ? global_scale(p.b) : 1.0f;       // (early: not when they are needed)
   Tile tl;
   const uint32_t code_row = (uint32_t)p.K / 2, scale_row = (uint32_t)(p.K / kScaleGroup<FMT>);
   // loads: ROWS/8 rows a wave, the second half of the waves the second matrix of a pair
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs
     const f32x4 a = sum(w), b = GU ? sum(w + RG / 2) : a;
     const int t = t0 + tok, n = n0 + piece * 4;
     if (splits == 1) {
-      write4<GU>(p, t, n, a, b);
+      write4<GU>(p, t, n, a, b, ga, gb);
     } else {
       *reinterpret_cast<f32x4*>(sums + ((size_t)(split * (GU ? 2 : 1)) * p.T + t) * np + n) = a;
       if constexpr (GU) *reinterpret_cast<f32x4*>(sums + ((size_t)(split * 2 + 1) * p.T + t) * np + n) = b;
@@ -285,6 +286,7 @@ __global__ __launch_bounds__(256) void quant_join_kernel(DenseArgs p, int np, in
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const int per = np / 4, t = (int)(i / per), n = (int)(i % per) * 4;
   if (t >= p.T || n >= p.N) return;
+  const float ga = global_scale(p.a), gb = GU ? global_scale(p.b) : 1.0f;
   const float* const at = sums + (size_t)t * np + n;
   const size_t part = (size_t)p.T * np;
   f32x4 v[NA] = {};
@@ -302,7 +304,7 @@ __global__ __launch_bounds__(256) void quant_join_kernel(DenseArgs p, int np, in
 #pragma unroll
         for (int m = 0; m < NA; ++m) v[m] += q[s][m];
   }
-  write4<GU>(p, t, n, v[0], v[NA - 1]);
+  write4<GU>(p, t, n, v[0], v[NA - 1], ga, gb);
 }
 
 struct SplitPlan {

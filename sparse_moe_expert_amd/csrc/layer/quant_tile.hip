@@ -139,6 +139,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
   const int l32 = lane & 31, half = lane >> 5;
   const int rows = min(kRows, p.N - n0), toks = min(kTileTokens, p.T - t0);
 
+  const float ga = global_scale(p.a), gb = GU ? global_scale(p.b) : 1.0f;       // (early: not when they are needed)
   Tile tl;
   tl.half = half;
   const uint32_t code_row = (uint32_t)p.K / 2, scale_row = (uint32_t)(p.K / kScaleGroup<FMT>);
@@ -252,7 +253,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
   // Sums to LDS as fp32, then whole 16-byte pieces of output rows.  One array
   // takes 32 tokens x 128 rows, chunk c of four rows of token t at c ^ (t & 15).
   constexpr int kRound = GU ? 4 : 2;                         // token tiles a round
-  const float g = !GU && p.a.g ? *p.a.g : 1.0f;
 #pragma unroll
   for (int j0 = 0; j0 < 4; j0 += kRound) {
     if (j0 * 32 >= toks) break;
@@ -271,7 +271,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
           for (int i = 0; i < 4; ++i) {
             v[i] = acc[m][j][r * 4 + i];
             if constexpr (GU) {
-              const float ga = p.a.g ? *p.a.g : 1.0f, gb = p.b.g ? *p.b.g : 1.0f;
               v[i] = silu(v[i] * ga) * (acc[1][j][r * 4 + i] * gb);
             }
           }
@@ -306,8 +305,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int row = min(max(r0 + k, 0), rows - 1);
-            if (p.bias) v[k] = v[k] * g + bf16_to_f32(p.bias[n0 + row]);
-            else v[k] *= g;
+            if (p.bias) v[k] = v[k] * ga + bf16_to_f32(p.bias[n0 + row]);
+            else v[k] *= ga;
             v[k] *= gate;
             if (p.add) v[k] += bf16_to_f32(p.add[at + row]);
           }
@@ -335,7 +334,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
       const uint8_t* const in = array(tok, piece * 8);
       const f32x4 lo = *reinterpret_cast<const f32x4*>(in + ((c ^ (tok & 15)) << 4));
       const f32x4 hi = *reinterpret_cast<const f32x4*>(in + (((c + 1) ^ (tok & 15)) << 4));
-      write8<GU>(p, t, n, lo, hi);
+      write8<GU>(p, t, n, lo, hi, ga);
     }
   }
 }
