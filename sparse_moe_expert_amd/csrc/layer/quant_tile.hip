@@ -44,51 +44,43 @@ constexpr int kStages = 4, kLead = 2;
 constexpr int kStageBytes = kTileTokens * kTileK * 2;        // 16 KB
 constexpr int kXcds = 8;
 
-// WIDE: a row's scales of four steps are loaded at once, from a multiple of
-// four bytes; else step by step.
+// A row's scales of four steps are loaded at once, from the dword they start
+// in.  WIDE: they always start at a multiple of four bytes; else they are
+// shifted into place (2048x4096x2592: 52.1 us, 56.7 loaded step by step; 2560:
+// 48.3).
 template <int FMT, bool GU, bool WIDE>
 struct RowTile {
   static constexpr int kCodeLoads = 4, kTokenLoads = 4;      // of two steps, of one
   __amdgpu_buffer_rsrc_t rc[GU ? 2 : 1], rs[GU ? 2 : 1], rx;
   uint32_t c_off[2], s_off[2], x_off[4];
+  uint32_t shift[2];                                         // bytes into the first dword
   int half;
   uint4 wc[kStages][2];
   uint4 wide[2][2];                                          // scales of this ring, of the next
-  uint16_t narrow[kStages][2];                               // 16 bits until used: a widening would wait for its load
 
-  // Codes and scales of the steps a and b = a + 1, of stages S and S + 1: their
-  // lines are fetched once for both
+  // Codes of the steps a and b = a + 1, of stages S and S + 1: their lines are
+  // fetched once for both
   template <int S>
   __device__ __forceinline__ void issue_weights(uint32_t a, uint32_t b) {
-    constexpr bool kNv = FMT == MOE_QUANT_NVFP4;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const int r = GU ? m : 0;
       wc[S][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rc[r], c_off[m] + a * 32u, 0, 0));
       wc[S + 1][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rc[r], c_off[m] + b * 32u, 0, 0));
-      if constexpr (WIDE) {
-      } else if constexpr (kNv) {
-        narrow[S][m] = __builtin_amdgcn_raw_buffer_load_b16(rs[r], s_off[m] + a * 4u, 0, 0);
-        narrow[S + 1][m] = __builtin_amdgcn_raw_buffer_load_b16(rs[r], s_off[m] + b * 4u, 0, 0);
-      } else {
-        narrow[S][m] = __builtin_amdgcn_raw_buffer_load_b8(rs[r], s_off[m] + a * 2u, 0, 0);
-        narrow[S + 1][m] = __builtin_amdgcn_raw_buffer_load_b8(rs[r], s_off[m] + b * 2u, 0, 0);
-      }
     }
   }
-  // The scales of four steps
+  // The scales of four steps (past the last one too: a shifted row ends in the
+  // dword after them)
   template <int W>
   __device__ __forceinline__ void issue_scales(uint32_t step) {
-    if constexpr (WIDE) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int r = GU ? m : 0;
-        if constexpr (FMT == MOE_QUANT_NVFP4) {
-          wide[W][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rs[r], s_off[m] + step * 4u, 0, 0));
-        } else {
-          const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs[r], s_off[m] + step * 2u, 0, 0);
-          wide[W][m].x = v[0], wide[W][m].y = v[1];
-        }
+    for (int m = 0; m < 2; ++m) {
+      const int r = GU ? m : 0;
+      if constexpr (FMT == MOE_QUANT_NVFP4) {
+        wide[W][m] = to_uint4(__builtin_amdgcn_raw_buffer_load_b128(rs[r], s_off[m] + step * 4u, 0, 0));
+      } else {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs[r], s_off[m] + step * 2u, 0, 0);
+        wide[W][m].x = v[0], wide[W][m].y = v[1];
       }
     }
   }
@@ -106,12 +98,17 @@ struct RowTile {
   __device__ __forceinline__ float scale(int S, bool next, int m, int i) const {
     constexpr bool kNv = FMT == MOE_QUANT_NVFP4;
     const uint4 w = wide[next][m];
-    uint32_t sb;
-    if constexpr (!WIDE) sb = narrow[S][m];
-    else if constexpr (kNv) sb = (S == 0 ? w.x : S == 1 ? w.y : S == 2 ? w.z : w.w) >> (half * 16);
-    else sb = ((S < 2 ? w.x : w.y) >> (S % 2 * 16 + half * 8)) & 0xFFu;
-    if constexpr (kNv) return i < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)sb, 0) : __builtin_amdgcn_cvt_f32_fp8((int)sb, 1);
-    else return __uint_as_float(sb << 23);
+    const uint32_t after = wide[1][m].x;                     // (next: stage 0 only, which needs none)
+    const int at = kNv ? S : S / 2;                          // the step's dword
+    uint32_t sb = at == 0 ? w.x : at == 1 ? w.y : at == 2 ? w.z : w.w;
+    if constexpr (!WIDE)
+      sb = __builtin_amdgcn_alignbyte(at == (kNv ? 3 : 1) ? after : at == 0 ? w.y : at == 1 ? w.z : w.w, sb, shift[m]);
+    if constexpr (kNv) {
+      sb >>= half * 16;
+      return i < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)sb, 0) : __builtin_amdgcn_cvt_f32_fp8((int)sb, 1);
+    } else {
+      return __uint_as_float((sb >> (S % 2 * 16 + half * 8) & 0xFFu) << 23);
+    }
   }
 };
 
@@ -147,14 +144,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
   for (int m = 0; m < (GU ? 2 : 1); ++m) {
     const QuantMat& w = m ? p.b : p.a;
     tl.rc[m] = make_rsrc(w.codes + (size_t)n0 * code_row, (uint32_t)rows * code_row);
-    tl.rs[m] = make_rsrc(w.scales + (size_t)n0 * scale_row, (uint32_t)rows * scale_row);
+    tl.rs[m] = make_rsrc(w.scales + (size_t)n0 * scale_row, ((uint32_t)rows * scale_row + 3u) & ~3u);
   }
   tl.rx = make_rsrc(p.x + (size_t)t0 * p.K, (uint32_t)toks * (uint32_t)p.K * 2u);
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const uint32_t row = (uint32_t)((GU ? 0 : m * 128) + wave * 32 + l32);
     tl.c_off[m] = row * code_row + (uint32_t)half * 16u;
-    tl.s_off[m] = row * scale_row + (WIDE ? 0u : (uint32_t)half * (FMT == MOE_QUANT_NVFP4 ? 2u : 1u));
+    tl.s_off[m] = row * scale_row & ~3u;
+    tl.shift[m] = row * scale_row & 3u;
   }
   // piece i of a wave: 8 token rows of 128 bytes; rows past the last token repeat it
 #pragma unroll
@@ -171,7 +169,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
 
   // a step past the last one is issued out of range: it reads nothing
   auto at = [&](int s) { return s < steps ? (uint32_t)s : kOutside / 128u; };
-  tl.template issue_scales<0>(at(0));
+  tl.template issue_scales<0>(0);
   tl.template issue_weights<0>(at(0), at(1));
   fence();
   tl.issue_tokens(s_0, wave, at(0));
@@ -188,15 +186,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
   }
   auto body = [&](auto stage_c, int s) {
     constexpr int S = decltype(stage_c)::value, F = (S + kLead) % kStages;
+    constexpr int kScalesAt = WIDE ? 2 : 0;                  // shifted ones are needed a step earlier
     if constexpr (S % 2 == 0) {
-      if constexpr (F == 0) tl.template issue_scales<1>(at(s + kLead));
+      if constexpr (S == kScalesAt) tl.template issue_scales<1>((uint32_t)(s - S) + kStages);
       tl.template issue_weights<F>(at(s + kLead), at(s + kLead + 1));
       fence();
     }
     tl.issue_tokens(F == 0 ? s_0 : F == 1 ? s_1 : F == 2 ? s_2 : s_3, wave, at(s + kLead));
     // this wave's tokens of step s are here; since then two steps' tokens,
-    // the codes of a pair of steps, and scales
-    wait_vm<kLead * Tile::kTokenLoads + Tile::kCodeLoads + (!WIDE ? 4 : S < 2 ? 0 : 2)>();
+    // the codes of a pair of steps, and scales where they were issued
+    wait_vm<kLead * Tile::kTokenLoads + Tile::kCodeLoads + (S / 2 == kScalesAt / 2 ? 2 : 0)>();
     uint8_t* const stage = S == 0 ? s_0 : S == 1 ? s_1 : S == 2 ? s_2 : s_3;
     if (p.K - s * kTileK < kTileK) {                         // half a step: what follows a token's row is not its
 #pragma unroll
