@@ -28,7 +28,7 @@
 // quant_join_kernel adds them in order and finishes the outputs.
 //
 // Bound by the steps, each a barrier with one workgroup a compute unit, more
-// than by bytes: T = 32 9999x4096 13.2 us, of which 8 steps on 157 of the 256
+// than by bytes: T = 32 9999x4096 12.6 us, of which 8 steps on 157 of the 256
 // compute units are 9 (the weights, 23 MB, take 4.8 us at the rate of a copy);
 // splitting each tile in two takes a unit's time off and adds the join's.
 #include "quant_common.h"
