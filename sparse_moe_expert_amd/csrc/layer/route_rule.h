@@ -6,10 +6,12 @@
 // experts of the same logit and bias (which tie exactly, and go by their ids).
 // Else the first k and a few more, one to a lane, are ordered by scores in
 // fp64, as the rule defines them; and where those few do not reach past the
-// doubt, or the groups are in doubt, all experts are.  A few tokens in a
-// hundred with spread logits take the second way, hardly any the third.  An
-// fp32 score takes about 6 instructions, an fp64 one 60, and 512 experts of
-// them would set the time.
+// doubt, all experts are.  Groups in doubt are settled first, by all scores in
+// fp64 (4096 tokens of 512 experts with such a token among them: 22 us; 30 where
+// it then took the experts by those too).  A few tokens in a hundred with
+// spread logits take the second way, hardly any the last.  An fp32 score takes
+// about 6 instructions, an fp64 one 60, and 512 experts of them would set the
+// time.
 //
 // The error bound, u = 2^-24.  Sigmoid: e^-z is off by (1.5 |z| + 2) u of
 // itself (product and hardware exponential), the sum and the reciprocal by 3 u;
@@ -158,13 +160,13 @@ __device__ __forceinline__ bool group_kept(const RouteRule& r, int group, F v) {
   return before < r.kept;
 }
 
-// The k chosen experts of token t by scores in fp64: slot j's in lane j.  Not
-// inlined, and reads its logits again: the usual way keeps its registers.
+// The choice values of a lane's experts in fp64 (masked ones -inf), and whether
+// its group is kept by them.  Reads its logits again: the usual way keeps its
+// registers.
 template <int V, bool BF16>
-__device__ __forceinline__ int select_exact(const RouteRule& r, const void* logits, const float* bias, int t, float top, int lane,
-                                         int group, int e0, int count) {
+__device__ __forceinline__ bool kept_exact(const RouteRule& r, const void* logits, const float* bias, int t, float top,
+                                           int group, int e0, int count, double (&c)[V]) {
   const double kMasked = -__builtin_huge_val();
-  double c[V];
   double sum = 0.0;
   float z[V], b[V];
 #pragma unroll
@@ -190,7 +192,16 @@ __device__ __forceinline__ int select_exact(const RouteRule& r, const void* logi
     x = fmax(x, c[i]);
   }
   group_best(r.lanes, x, y);
-  const bool kept = group_kept(r, group, group_value(r.group_top, x, y));
+  return group_kept(r, group, group_value(r.group_top, x, y));
+}
+
+// The k chosen experts of token t by scores in fp64: slot j's in lane j
+template <int V, bool BF16>
+__device__ __forceinline__ int select_exact(const RouteRule& r, const void* logits, const float* bias, int t, float top, int lane,
+                                            int group, int e0, int count) {
+  const double kMasked = -__builtin_huge_val();
+  double c[V];
+  const bool kept = kept_exact<V, BF16>(r, logits, bias, t, top, group, e0, count, c);
   // the masked experts of the kept groups follow their others
   constexpr double kLast = -1e300, kTaken = -1e306;
 #pragma unroll
@@ -304,17 +315,19 @@ __device__ __forceinline__ void select_grouped(const RouteRule& r, const void* _
   sort_keys(K);
   auto value = [](uint64_t key) { return (uint32_t)(key >> 32) > 1u ? from_ordered((uint32_t)(key >> 32)) : -kInf; };
 
-  int doubt = 0;                                             // wave-uniform; 1: of experts, 2: of groups
   if (r.kept < r.groups) {
     float x = value(K[0]), y = V > 1 ? value(K[V > 1 ? 1 : 0]) : -kInf;
     group_best(r.lanes, x, y);
     const float v = group_value(r.group_top, x, y);
-    const bool in = group_kept(r, group, v);
+    bool in = group_kept(r, group, v);
     const bool real = group < r.groups;
     const float low = -wave_max_f32(real && in ? -v : -kInf), high = wave_max_f32(real && !in ? v : -kInf);
     // (groups with no expert left tie exactly)
     const float most = wave_max_f32(fmaxf(x > -kInf ? fabsf(x) : 0.0f, y > -kInf ? fabsf(y) : 0.0f));
-    doubt = high > -kInf && !(low - high > 2.0f * tol(most) + 3e-7f * most) ? 2 : 0;
+    if (high > -kInf && !(low - high > 2.0f * tol(most) + 3e-7f * most)) {
+      double exact[V];
+      in = kept_exact<V, BF16>(r, logits, bias, t, top, group, e0, count, exact);
+    }
     if (!in)
 #pragma unroll
       for (int i = 0; i < V; ++i) K[i] = 0;
@@ -333,13 +346,14 @@ __device__ __forceinline__ void select_grouped(const RouteRule& r, const void* _
   my_e = my_key > 0u ? my_e : 0;                             // (no expert left)
   float mz = s_z[my_e], mb = s_b[my_e];
   // lane j: slot j against the next
+  bool doubt;                                                // wave-uniform
   const float c = from_ordered(my_key);
   {
     const uint32_t next = __shfl_down(my_key, 1, kWave);
     const float nz = __shfl_down(mz, 1, kWave), nb = __shfl_down(mb, 1, kWave);
     const bool same = lane < r.k - 1 && mz == nz && mb == nb;
     const bool near = lane < r.k && next > 1u && !same && !(c - from_ordered(next) > tol(c));
-    doubt |= __any(near) ? 1 : 0;
+    doubt = __any(near);
   }
   const bool need_total = r.softmax && (doubt || !r.renormalise);
   double total = 1.0;
@@ -360,7 +374,7 @@ __device__ __forceinline__ void select_grouped(const RouteRule& r, const void* _
   if (doubt) {
     const float cut = read_lane(c, r.k - 1), last = read_lane(c, n - 1);
     const bool past = __builtin_amdgcn_readlane(my_key, n - 1) <= 1u || cut - last > tol(cut);
-    if (doubt == 1 && past) {
+    if (past) {
       // masked ones after all others, lanes without an expert last
       const bool live = my_key > 1u;
       double v = live ? w / total + (double)mb : my_key == 1u ? -1e300 : -1e306;
