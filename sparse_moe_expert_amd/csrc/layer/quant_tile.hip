@@ -54,7 +54,6 @@ struct RowTile {
   __amdgpu_buffer_rsrc_t rc[GU ? 2 : 1], rs[GU ? 2 : 1], rx;
   uint32_t c_off[2], s_off[2], x_off[4];
   uint32_t shift[2];                                         // bytes into the first dword
-  int half;
   uint4 wc[kStages][2];
   uint4 wide[2][2];                                          // scales of this ring, of the next
 
@@ -90,12 +89,13 @@ struct RowTile {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, stage + (i * 4 + wave) * 1024, 16, x_off[i] + step * 128u, 0, 0, 0);
   }
 
-  // Row tile m, group i (8 weights) of the step in `stage`: codes and scale
+  // Row tile m, group i (8 weights) of the step in `stage`: codes and scale (of
+  // the lane's half of the step)
   __device__ __forceinline__ uint32_t word(int stage, int m, int i) const {
     const uint4 c = wc[stage][m];
     return i == 0 ? c.x : i == 1 ? c.y : i == 2 ? c.z : c.w;
   }
-  __device__ __forceinline__ float scale(int S, bool next, int m, int i) const {
+  __device__ __forceinline__ float scale(int S, bool next, int m, int i, int half) const {
     constexpr bool kNv = FMT == MOE_QUANT_NVFP4;
     const uint4 w = wide[next][m];
     const uint32_t after = wide[1][m].x;                     // (next: stage 0 only, which needs none)
@@ -138,7 +138,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
 
   const float ga = global_scale(p.a), gb = GU ? global_scale(p.b) : 1.0f;       // (early: not when they are needed)
   Tile tl;
-  tl.half = half;
   const uint32_t code_row = (uint32_t)p.K / 2, scale_row = (uint32_t)(p.K / kScaleGroup<FMT>);
 #pragma unroll
   for (int m = 0; m < (GU ? 2 : 1); ++m) {
@@ -169,6 +168,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
 
   // a step past the last one is issued out of range: it reads nothing
   auto at = [&](int s) { return s < steps ? (uint32_t)s : kOutside / 128u; };
+  // The half of step s that a lane takes its scales of.  Where K ends with half a
+  // step the second half's tokens are zero, but its scale bytes may lie behind
+  // the matrix, and zero times a NaN would count: it takes the first half's.
+  auto scale_half = [&](int s) { return WIDE || p.K - s * kTileK >= kTileK ? half : 0; };
   tl.template issue_scales<0>(0);
   tl.template issue_weights<0>(at(0), at(1));
   fence();
@@ -180,7 +183,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const uint32_t c = tl.word(0, m, 0);
-    const float s = tl.scale(0, false, m, 0);
+    const float s = tl.scale(0, false, m, 0, scale_half(0));
     af[m] = __builtin_bit_cast(bf16x8, make_uint4(fp4x2_scaled<FMT, 0>(c, s), fp4x2_scaled<FMT, 1>(c, s),
                                                   fp4x2_scaled<FMT, 2>(c, s), fp4x2_scaled<FMT, 3>(c, s)));
   }
@@ -208,6 +211,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
     wait_lds();                                              // and its reads of step s-1 have returned
     barrier();
     __builtin_amdgcn_sched_barrier(0);
+    const int half_here = scale_half(s), half_next = scale_half(s + 1);
     // Four groups of eight products, of all four token tiles also where the
     // last ones are past T (branches around them would keep the products of a
     // tile apart).  Under a group's products the next group's weights are
@@ -226,8 +230,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
         constexpr int n = decltype(n_c)::value, j = n / 2, m = n % 2, D = n % 4, W = n / 4;
         if constexpr (i < 3 && m == 0) read(i + 1, j);
         acc[m][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[m], b[i & 1][j], acc[m][j], 0, 0, 0);
-        const float s = tl.scale(i < 3 ? S : (S + 1) % kStages, i == 3 && S == 3, W, (i + 1) % 4);
-        next[W][D] = fp4x2_scaled<FMT, D>(tl.word(i < 3 ? S : (S + 1) % kStages, W, (i + 1) % 4), s);
+        const float sc = tl.scale(i < 3 ? S : (S + 1) % kStages, i == 3 && S == 3, W, (i + 1) % 4, i < 3 ? half_here : half_next);
+        next[W][D] = fp4x2_scaled<FMT, D>(tl.word(i < 3 ? S : (S + 1) % kStages, W, (i + 1) % 4), sc);
         asm volatile("" : "+v"(next[W][D]));
         __builtin_amdgcn_sched_barrier(0);
       });

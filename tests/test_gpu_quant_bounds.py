@@ -1,0 +1,80 @@
+"""The 4-bit products on operands that lie inside larger buffers: what follows
+an operand has no part in the result, and what follows an output, or the
+workspace of the size asked for, stays as it was."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sparse_moe_expert_amd as sme
+from gpu_harness import DEV, to_dev
+from layer_testlib import assert_near, bits, dev_bf16, f64, linear_tolerance, shared_reference, weight
+
+pytestmark = pytest.mark.gpu
+
+GUARD = 256
+
+
+def _followed(a: np.ndarray, fill: int) -> torch.Tensor:
+    """The array on the device, with bytes `fill` right behind it."""
+    raw = np.ascontiguousarray(a).view(np.uint8).reshape(-1)
+    t = to_dev(np.concatenate([raw, np.full(GUARD, fill, np.uint8)]))
+    dtype = {np.dtype(np.uint8): torch.uint8, np.dtype(np.uint16): torch.bfloat16}[a.dtype]
+    return t[:raw.size].view(dtype).view(a.shape)
+
+
+def _handle(w, fmt):
+    """Scales followed by 0xFF, which is NaN as e4m3 and as e8m0."""
+    codes, scales, g = w
+    return sme.QuantWeight(_followed(codes, 0xFF), _followed(scales, 0xFF),
+                           None if g is None else to_dev(np.array([g], np.float32)), fmt)
+
+
+def _guarded(shape, dtype):
+    """A tensor of 7s, and the whole buffer whose head it is."""
+    n = int(np.prod(shape))
+    whole = torch.full((n + GUARD,), 7, dtype=dtype, device=DEV)
+    return whole[:n].view(shape), whole[n:]
+
+
+# (T, N, K): odd outputs a token and token counts on every kernel; N * K/16 and N * K/32 of every remainder by 4 with K
+# an odd multiple of 32 (the last row's scales end inside a dword); split reductions of aligned and other scale rows
+LINEAR = [
+    (1, 7, 32), (3, 101, 160), (5, 17, 32), (7, 301, 672), (12, 33, 96), (15, 65, 4064), (17, 31, 224), (65, 257, 128),
+    (31, 999, 1056), (33, 899, 8224), (63, 71, 96), (127, 1, 64), (129, 385, 1088), (33, 4097, 4096), (20, 33, 16384),
+    (700, 11001, 96), (700, 11002, 96), (2501, 11003, 32), (300, 1001, 2080), (701, 11000, 160), (1301, 4091, 1184), (641, 8193, 608),
+    (300, 22001, 64), (2049, 2561, 224), (900, 10241, 128),
+]
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,N,K", LINEAR)
+def test_linear_in_larger_buffers(T, N, K, fmt):
+    rng = np.random.default_rng(T + 3 * N + K)
+    w = weight(rng, N, K, fmt)
+    x, bias = bits(rng.standard_normal((T, K))), bits(rng.standard_normal(N)) if N % 3 else None
+    y, behind = _guarded((T, N), torch.bfloat16)
+    ws, past = _guarded((sme.moe_quant_linear_workspace_size(T, N, K),), torch.uint8)
+    sme.moe_quant_linear(_followed(x, 0xFF), _handle(w, fmt), None if bias is None else _followed(bias, 0xFF), y, ws)
+    torch.cuda.synchronize()
+    assert torch.all(behind == 7) and torch.all(past == 7)
+    ref, mag = oracle.quant_linear(x, w, fmt, bias)
+    assert_near(f64(y), ref, linear_tolerance(ref, mag, K), (T, N, K, fmt))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,H,Is", [(3, 96, 160), (21, 416, 352), (100, 2080, 672), (1301, 96, 3040), (4100, 1056, 1056),
+                                    (90, 544, 5216)])
+def test_shared_in_larger_buffers(T, H, Is, fmt):
+    rng = np.random.default_rng(T + H + Is)
+    gate, up, down = weight(rng, Is, H, fmt), weight(rng, Is, H, fmt), weight(rng, H, Is, fmt)
+    x, v, a = bits(rng.standard_normal((T, H))), bits(rng.standard_normal(H) / np.sqrt(H)), bits(rng.standard_normal((T, H)))
+    y, behind = _guarded((T, H), torch.bfloat16)
+    ws, past = _guarded((sme.moe_quant_shared_expert_workspace_size(T, H, Is),), torch.uint8)
+    sme.moe_quant_shared_expert(_followed(x, 0xFF), *(_handle(m, fmt) for m in (gate, up, down)), _followed(v, 0xFF),
+                                _followed(a, 0xFF), y, ws)
+    torch.cuda.synchronize()
+    assert torch.all(behind == 7) and torch.all(past == 7)
+    ref, tol = shared_reference(x, gate, up, down, fmt, v, a)
+    assert_near(f64(y), ref, tol, (T, H, Is, fmt))
