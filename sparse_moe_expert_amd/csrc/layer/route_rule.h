@@ -322,9 +322,11 @@ __device__ __forceinline__ void select_grouped(const RouteRule& r, const void* _
     bool in = group_kept(r, group, v);
     const bool real = group < r.groups;
     const float low = -wave_max_f32(real && in ? -v : -kInf), high = wave_max_f32(real && !in ? v : -kInf);
-    // (groups with no expert left tie exactly)
+    // (groups with no expert left tie exactly; the sum of two finite values beyond
+    // half the largest float is infinite here and not in fp64)
+    const bool outside = x > -kInf && x < kInf && !(fabsf(v) < kInf);
     const float most = wave_max_f32(fmaxf(x > -kInf ? fabsf(x) : 0.0f, y > -kInf ? fabsf(y) : 0.0f));
-    if (high > -kInf && !(low - high > 2.0f * tol(most) + 3e-7f * most)) {
+    if (__any(outside) || (high > -kInf && !(low - high > 2.0f * tol(most) + 3e-7f * most))) {
       double exact[V];
       in = kept_exact<V, BF16>(r, logits, bias, t, top, group, e0, count, exact);
     }

@@ -45,11 +45,11 @@ def test_large_biases(score, T, E, k, groups, kept):
         bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
         for g in range(groups):
             part = slice(g * size, (g + 1) * size)
-            draw = rng.integers(0, 4) if g < groups - 1 else 0
+            draw = rng.integers(0, 8) if g < groups - 1 else 7
             far = rng.uniform(1.0e38, 3.29e38, size).astype(np.float32)
-            if draw == 1:
+            if 1 <= draw <= 2:
                 bias[part] = -np.inf
-            elif draw >= 2 or g == groups - 1:
+            elif draw > 2:
                 bias[part] = far if kind == "high" else -far if kind == "low" else far * rng.choice([-1, 1], size)
         for top in (1, 2):
             args = (k, score, groups, kept, top, True, 1.0)
