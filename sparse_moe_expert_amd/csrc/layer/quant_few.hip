@@ -6,7 +6,7 @@
 // own.  A lane's weights of a step are one 16-byte load, row l%4 and the 32
 // reduction indices 32*(l/4)..: a wavefront reads 256 contiguous bytes of
 // each of four rows, and eight instructions of 4 indices use them up.  For
-// NVFP4 the codes enter unscaled (one conversion for two weights): the four
+// NVFP4 the codes enter without their scales (one conversion for two weights): the four
 // instructions of a 16-weight scale block start from zero, and their results
 // (a lane's: the tokens' of its own row) are scaled as they are added to the
 // sums.  Decoding costs about half an instruction a weight instead of 2 for
@@ -42,6 +42,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kStepK = 512;
 constexpr int kFewTokens = 16;                               // at most, per workgroup
 constexpr int kFewWaves = 16;                                // at most, per workgroup
+// NVFP4 codes enter as 2^-7 of their value, exactly, and the sums leave by 2^7
+// of theirs: 16 codes of 6 against the largest tokens would pass fp32's range
+// before their scale, 2^-9 at least, is applied.
+constexpr float kCodeUnit = 1.0f / 128;
 
 template <int B>
 __device__ __forceinline__ uint32_t fp4x2_bits(uint32_t word, float scale) {
@@ -169,8 +173,8 @@ __global__ __launch_bounds__(kFewWaves * kWave, 4) void quant_few_kernel(DenseAr
     uint32_t w0[8], w1[8];
     if constexpr (FMT == MOE_QUANT_NVFP4) {
       s0 = __builtin_amdgcn_cvt_f32_fp8((int)sb, 0), s1 = __builtin_amdgcn_cvt_f32_fp8((int)sb, 1);
-      decode16(c.x, c.y, 1.0f, w0);
-      decode16(c.z, c.w, 1.0f, w1);
+      decode16(c.x, c.y, kCodeUnit, w0);
+      decode16(c.z, c.w, kCodeUnit, w1);
     } else {
       decode16(c.x, c.y, __uint_as_float(sb << 23), w0);
       decode16(c.z, c.w, __uint_as_float(sb << 23), w1);
@@ -219,6 +223,7 @@ __global__ __launch_bounds__(kFewWaves * kWave, 4) void quant_few_kernel(DenseAr
   float v = acc[0][0], u = 0.0f;
 #pragma unroll
   for (int t = 1; t < TT; ++t) v = b == t ? acc[t / 4][t % 4] : v;
+  if constexpr (FMT == MOE_QUANT_NVFP4) v *= 1.0f / kCodeUnit;
   if constexpr (GU) {
     // the scales' place is free once every wave is done with its own
     __syncthreads();

@@ -78,3 +78,38 @@ def test_shared_in_larger_buffers(T, H, Is, fmt):
     assert torch.all(behind == 7) and torch.all(past == 7)
     ref, tol = shared_reference(x, gate, up, down, fmt, v, a)
     assert_near(f64(y), ref, tol, (T, H, Is, fmt))
+
+
+# tokens on every kernel (the fewest, more of small weights, a split reduction, whole tiles), and the weight's sizes
+RANGE = [(1, 20, 32), (3, 20, 64), (8, 70, 608), (40, 70, 96), (40, 300, 8224), (600, 300, 2048), (700, 11000, 96)]
+
+
+@pytest.mark.parametrize("T,N,K", RANGE)
+def test_linear_large_tokens(T, N, K):
+    """Tokens of up to 2^124 with NVFP4 scales of 2^-6 .. 2^-9: every product and every sum of them lies inside fp32,
+    sums of unscaled codes (16 of up to 6) would not."""
+    rng = np.random.default_rng(K)
+    codes, _, _ = weight(rng, N, K, "nvfp4")
+    codes = codes & 0x77                                     # no signs: nothing cancels
+    scales = np.array([1, 2, 4, 8], np.uint8)[rng.integers(0, 4, (N, K // 16))]
+    w = (codes, scales, np.float32(2.0 ** -14))
+    x = np.full((T, K), 2.0 ** -20)
+    # 16 of every row: at most 16 * 6 * 2^124 * 2^-6 < 2^125
+    x[:, 16:32] = 2.0 ** 124
+    y = sme.moe_quant_linear(dev_bf16(bits(x)), sme.QuantWeight(to_dev(codes), to_dev(scales), to_dev(w[2].reshape(1))))
+    ref, mag = oracle.quant_linear(bits(x), w, "nvfp4")
+    assert_near(f64(y), ref, linear_tolerance(ref, mag, K), (T, N, K))
+
+
+@pytest.mark.parametrize("T,N,K", RANGE)
+def test_linear_small_tokens(T, N, K):
+    """Tokens of the smallest normal numbers: products with small codes lie below fp32's normal range, the outputs by
+    a large global scale do not."""
+    rng = np.random.default_rng(K + 1)
+    codes = weight(rng, N, K, "nvfp4")[0]
+    scales = rng.integers(0x70, 0x7F, (N, K // 16)).astype(np.uint8)
+    w = (codes, scales, np.float32(2.0 ** 60))
+    x = bits(rng.choice([-1.5, -1.0, 1.0, 1.9921875], (T, K)) * 2.0 ** -126)
+    y = sme.moe_quant_linear(dev_bf16(x), sme.QuantWeight(to_dev(codes), to_dev(scales), to_dev(w[2].reshape(1))))
+    ref, mag = oracle.quant_linear(x, w, "nvfp4")
+    assert_near(f64(y), ref, linear_tolerance(ref, mag, K), (T, N, K))
