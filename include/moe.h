@@ -621,8 +621,10 @@ moe_status moe_route_grouped_bucket(const void* logits, int logits_type, const f
  *   MOE_QUANT_MXFP4  an e8m0 scale 2^(byte - 127) per 32 weights, [N, K/32];
  *                    the global scale may be NULL (1)
  * Scale bytes are not NaN, and not negative (precondition); e8m0 bytes lie
- * in 2 .. 252 (2^-125 .. 2^125), so that every weight is a finite normal
- * bf16 value or zero.
+ * in 0 .. 252 (2^-127 .. 2^125): every weight is then a finite bf16 value.
+ * (Under 253 and 254 codes of 4 and 6, or from 2 on, are 2^128 and more:
+ * infinite, and not only in their own output, since a zero activation times
+ * an infinite weight is NaN.)
  */
 typedef enum {
   MOE_QUANT_NVFP4 = 0,

@@ -129,7 +129,8 @@ def moe_route_grouped_bucket(logits: torch.Tensor, bias: Optional[torch.Tensor],
 class QuantWeight(_Fixed):
     """A dense 4-bit matrix [N, K] on the device: `codes` uint8 [N, K/2],
     `scales` uint8 [N, K/16] ("nvfp4") or [N, K/32] ("mxfp4") and the global
-    scale, fp32 [1] (None: 1, "mxfp4" only)."""
+    scale, fp32 [1] (None: 1, "mxfp4" only).  The bytes are not read here: no
+    scale is NaN or negative, and those of "mxfp4" are at most 252."""
 
     __slots__ = ("codes", "scales", "g_scale", "format", "N", "K", "device", "_format", "_index")
 

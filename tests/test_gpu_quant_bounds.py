@@ -113,3 +113,19 @@ def test_linear_small_tokens(T, N, K):
     y = sme.moe_quant_linear(dev_bf16(x), sme.QuantWeight(to_dev(codes), to_dev(scales), to_dev(w[2].reshape(1))))
     ref, mag = oracle.quant_linear(x, w, "nvfp4")
     assert_near(f64(y), ref, linear_tolerance(ref, mag, K), (T, N, K))
+
+
+@pytest.mark.parametrize("T,N,K", RANGE)
+def test_linear_mxfp4_scale_range(T, N, K):
+    """Every code under the smallest and largest e8m0 scales: weights down to 2^-128, which bf16 has as subnormal numbers,
+    and up to 6 * 2^125.  One weight and one token value a row that are not zero: the product is exact."""
+    rng = np.random.default_rng(N)
+    for lo, hi, size in ((0, 3, 100), (250, 253, -30)):
+        codes = np.zeros((N, K // 2), np.uint8)
+        codes[:, 3] = np.arange(N) % 16 * 0x11
+        scales = rng.integers(lo, hi, (N, K // 32)).astype(np.uint8)
+        x = np.zeros((T, K))
+        x[np.arange(T), 6 + np.arange(T) % 2] = 2.0 ** size
+        y = sme.moe_quant_linear(dev_bf16(bits(x)), sme.QuantWeight(to_dev(codes), to_dev(scales), None, "mxfp4"))
+        ref, _ = oracle.quant_linear(bits(x), (codes, scales, None), "mxfp4")
+        assert np.array_equal(f64(y), ref), (lo, size)
