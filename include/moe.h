@@ -634,8 +634,11 @@ typedef enum {
 /*
  * Bytes of device workspace moe_quant_linear needs: the fp32 sums of the parts
  * that the reduction is split into; 0 where it is not split, as for up to four
- * tokens with K <= 8192 and for batches whose output tiles fill the chip.
+ * tokens with K <= 8192 and for batches whose output tiles fill the chip.  So
+ * the size does not grow with T: a smaller batch may need more.  It is never
+ * above MOE_QUANT_SUMS_BYTES, which serve every call.
  */
+#define MOE_QUANT_SUMS_BYTES (8u << 20)
 size_t moe_quant_linear_workspace_size(int T, int N, int K);
 
 /*
@@ -668,7 +671,8 @@ moe_status moe_quant_linear(int format, const uint16_t* x,
  * Bytes of device workspace moe_quant_shared_expert needs (0 when T <= 0 or
  * the sizes are outside the call's envelope): h (bf16 [T, Is]), the token
  * gates (fp32 [T]) and the sums of a product whose reduction is split, each
- * rounded up to 256.
+ * rounded up to 256.  The sums do not grow with T (see above): the first two
+ * for the largest batch and MOE_QUANT_SUMS_BYTES serve every batch up to it.
  */
 size_t moe_quant_shared_expert_workspace_size(int T, int H, int Is);
 

@@ -38,6 +38,7 @@ from ._lib import (
     pack_weights,
 )
 from .layer import (
+    QUANT_SUMS_BYTES,
     QuantWeight,
     RouteRule,
     make_quant_shared_workspace,
@@ -76,6 +77,7 @@ __all__ = [
     "moe_step_workspace_size",
     "NOALLOC_SCRATCH_BYTES",
     "pack_weights",
+    "QUANT_SUMS_BYTES",
     "QuantWeight",
     "RouteRule",
     "make_quant_shared_workspace",

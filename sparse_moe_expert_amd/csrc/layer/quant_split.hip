@@ -307,6 +307,11 @@ __global__ __launch_bounds__(256) void quant_join_kernel(DenseArgs p, int np, in
   write4<GU>(p, t, n, v[0], v[NA - 1], ga, gb);
 }
 
+constexpr int kUnits = 256;                                  // workgroups at once: one a compute unit (LDS)
+// More parts than one only where all their workgroups run at once: each leaves
+// at most 128 rows' sums of 64 tokens.
+static_assert(kUnits * 128ull * 64 * sizeof(float) <= MOE_QUANT_SUMS_BYTES, "what moe.h says of the workspace");
+
 struct SplitPlan {
   int tokens, rows, row_tiles, tiles, splits, np;
   float us;
@@ -319,7 +324,6 @@ struct SplitPlan {
 // part, 17.4 as 128 rows in three; T = 100, where 64 rows take two rounds:
 // 20.9 against 17.4 as 128 rows in one part.
 SplitPlan plan(bool gate_up, int T, int N, int K) {
-  constexpr int kUnits = 256;
   constexpr float kStep64[] = {1.1f, 0.9f}, kStep128[] = {1.2f, 1.4f};       // us a unit, up to 32 and 64 tokens
   constexpr float kJoin = 3.5f, kJoinBytes = 5e6f;                            // us, and bytes a us
   SplitPlan best{};

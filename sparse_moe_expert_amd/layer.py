@@ -170,6 +170,9 @@ def _check_quant_x(x, weight: QuantWeight) -> int:
     return T
 
 
+QUANT_SUMS_BYTES = 8 << 20         # MOE_QUANT_SUMS_BYTES
+
+
 def moe_quant_linear_workspace_size(T: int, N: int, K: int) -> int:
     return int(load_library().moe_quant_linear_workspace_size(T, N, K))
 
@@ -177,8 +180,8 @@ def moe_quant_linear_workspace_size(T: int, N: int, K: int) -> int:
 def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.Tensor] = None,
                      y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """bf16 y [T,N] = x W^T + bias for bf16 x [T,K], a QuantWeight [N,K] and an
-    optional bf16 bias [N].  The workspace (uint8, for batches that need one) is
-    allocated where none is given."""
+    optional bf16 bias [N].  The workspace (uint8, for batches that need one;
+    QUANT_SUMS_BYTES serve every batch) is allocated where none is given."""
     T, N, dev, index = _check_quant_x(x, weight), weight.N, weight.device, weight._index
     if bias is not None:
         _tensor(bias, "bias", _BF16, (N,), dev, index)
@@ -205,8 +208,12 @@ def moe_quant_shared_expert_workspace_size(T: int, H: int, Is: int) -> int:
 
 
 def make_quant_shared_workspace(T: int, H: int, Is: int, device) -> torch.Tensor:
-    """Workspace of the size moe_quant_shared_expert needs (reusable across calls)."""
-    return torch.empty((max(moe_quant_shared_expert_workspace_size(T, H, Is), 256),), dtype=torch.uint8, device=device)
+    """A workspace for moe_quant_shared_expert, reusable across calls of these
+    weights' sizes and of up to T tokens.  (The size that one call needs is not
+    the largest for the largest batch.)"""
+    up = lambda n: (n + 255) & ~255  # noqa: E731
+    T, Is = max(T, 0), max(Is, 0)
+    return torch.empty((up(2 * T * Is) + up(4 * T) + QUANT_SUMS_BYTES,), dtype=torch.uint8, device=device)
 
 
 def moe_quant_shared_expert(x: torch.Tensor, gate: QuantWeight, up: QuantWeight, down: QuantWeight,
@@ -232,7 +239,7 @@ def moe_quant_shared_expert(x: torch.Tensor, gate: QuantWeight, up: QuantWeight,
     else:
         _tensor(y, "y", _BF16, (T, H), dev, index)
     if workspace is None:
-        workspace = make_quant_shared_workspace(T, H, Is, dev)
+        workspace = torch.empty((moe_quant_shared_expert_workspace_size(T, H, Is),), dtype=_U8, device=dev)
     else:
         _tensor(workspace, "workspace", _U8, workspace.shape, dev, index)
     x_at, y_at = x.data_ptr(), y.data_ptr()
