@@ -22,9 +22,10 @@ _FORMATS = {"nvfp4": (0, 16), "mxfp4": (1, 32)}        # moe_quant_format, weigh
 
 Tensor = torch.Tensor
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-# the device and stream queries of torch.cuda without their Python layers
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# the device and stream queries of torch.cuda without their Python layers, where
+# this torch has them (one built without a GPU has not)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(name: str, index: int, *args):

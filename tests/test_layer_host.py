@@ -1,7 +1,9 @@
 """Host side of the grouped routing and the 4-bit products that needs no device:
-workspace sizes over batches."""
+workspace sizes over batches, and importing the package on a torch without a GPU."""
 
 import os
+import subprocess
+import sys
 
 import pytest
 
@@ -31,3 +33,16 @@ def test_workspace_serves_smaller_batches(H, Is):
         assert made[T] >= most, T
         for N, K in ((H, Is), (Is, H), (9999, H), (257, Is)):
             assert sme.moe_quant_linear_workspace_size(T, N, K) <= sme.QUANT_SUMS_BYTES, (T, N, K)
+
+
+def test_import_without_gpu_functions():
+    """A torch that was built without a GPU lacks the device and stream queries the calls use."""
+    code = ("import torch\n"
+            "for name in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "import sparse_moe_expert_amd as sme\n"
+            "print(sme.RouteRule(4).k)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == ["4"]
