@@ -21,7 +21,7 @@ struct QuantMat {
 
 // y[t,n] = bf16( add[t,n] + gate[t] * (x_t . a_n + bias[n]) ), or for a
 // gate/up pair y[t,n] = bf16( SiLU(x_t . a_n) * (x_t . b_n) ); a null bias,
-// gate or add leaves its term out.  With `token_gate` the launch also fills
+// gate or add leaves its term out.  With `token_gate` a pair's launch also fills
 // gate_out[t] = sigmoid(x_t . token_gate).
 struct DenseArgs {
   const uint16_t* x;
@@ -154,7 +154,7 @@ __device__ __forceinline__ void write4(const DenseArgs& p, int t, int n, f32x4 a
     }
     v[j] = f32_to_bf16_rne(o);
   }
-  if (p.N % 4 == 0) {                          // 8-byte aligned, and whole fours
+  if (GU || p.N % 4 == 0) {                    // 8-byte aligned, and whole fours (a pair's N is a multiple of 32)
     *reinterpret_cast<uint2*>(p.y + at + n) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
   } else {
 #pragma unroll

@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kFewWaves * kWave, 4) void quant_few_kernel(DenseAr
   extern __shared__ __align__(16) uint8_t s_mem[];           // tokens, then the waves' scales
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = (int)blockDim.x / kWave;
-  if ((int)blockIdx.x >= tiles) {                            // token gates, one wave a token
+  if (GU && (int)blockIdx.x >= tiles) {                      // token gates, one wave a token
     const int t = ((int)blockIdx.x - tiles) * waves + wave;
     if (t < p.T) token_gate_row(p, t, lane);
     return;
@@ -283,7 +283,7 @@ template <int FMT, bool GU, int TT, int P>
 moe_status launch(const DenseArgs& p, const FewPlan& q, hipStream_t s) {
   const int waves = q.waves, rows = GU ? 2 * waves : 4 * waves;
   const int row_tiles = (p.N + rows - 1) / rows, tiles = row_tiles * ((p.T + TT - 1) / TT);
-  const int grid = tiles + (p.token_gate ? (p.T + waves - 1) / waves : 0);
+  const int grid = tiles + (GU && p.token_gate ? (p.T + waves - 1) / waves : 0);
   const uint32_t lds = lds_bytes(kScaleGroup<FMT>, q.tokens, p.K, waves);
   quant_few_kernel<FMT, GU, TT, P><<<(unsigned)grid, waves * kWave, lds, s>>>(p, row_tiles, tiles);
   return launch_status();

@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kSplitThreads, 2) void quant_split_kernel(DenseArgs
   };
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if ((int)blockIdx.x >= tiles * splits) {                   // token gates, one wave a token
+  if (GU && (int)blockIdx.x >= tiles * splits) {             // token gates, one wave a token
     const int t = ((int)blockIdx.x - tiles * splits) * kSplitWaves + wave;
     if (t < p.T) token_gate_row(p, t, lane);
     return;
@@ -345,7 +345,7 @@ SplitPlan plan(bool gate_up, int T, int N, int K) {
 template <int FMT, bool GU, int ROWS, int TOK, bool WIDE>
 moe_status launch(const DenseArgs& p, const SplitPlan& q, void* workspace, hipStream_t s) {
   float* const sums = static_cast<float*>(workspace);
-  const int grid = q.tiles * q.splits + (p.token_gate ? (p.T + kSplitWaves - 1) / kSplitWaves : 0);
+  const int grid = q.tiles * q.splits + (GU && p.token_gate ? (p.T + kSplitWaves - 1) / kSplitWaves : 0);
   quant_split_kernel<FMT, GU, ROWS, TOK, WIDE>
       <<<(unsigned)grid, kSplitThreads, 0, s>>>(p, q.row_tiles, q.tiles, q.splits, sums);
   const moe_status st = launch_status();

@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int per = (tiles + kXcds - 1) / kXcds;
-  if ((int)blockIdx.x >= per * kXcds) {                      // token gates, one wave a token
+  if (GU && (int)blockIdx.x >= per * kXcds) {                // token gates, one wave a token
     const int t = ((int)blockIdx.x - per * kXcds) * 4 + wave;
     if (t < p.T) token_gate_row(p, t, lane);
     return;
@@ -288,8 +288,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
       return (a == 0 ? s_0 : a == 1 ? s_1 : a == 2 ? s_2 : s_3) + (tok & 31) * 512;
     };
     const int here = min(toks - j0 * 32, kRound * 32);
-    if (p.N % 8 != 0) {
-      // Output rows that do not start at 16 bytes: pieces of eight that do,
+    if (!GU && p.N % 8 != 0) {
+      // Output rows that do not start at 16 bytes (never a pair's): pieces of eight that do,
       // which begin up to seven rows before the tile, the outer ones one by
       // one.  2048x4095x4096: 79.5 us, 92 with all outputs one by one (N = 4096: 71).
       constexpr int kPieces = kRows / 8 + 1;
@@ -303,16 +303,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
           const int row = min(max(r0 + k, 0), kRows - 1);
           v[k] = *reinterpret_cast<const float*>(array(tok, row) + ((((row & 127) >> 2) ^ (tok & 15)) << 4) + (row & 3) * 4);
         }
-        if constexpr (!GU) {
-          const float gate = p.gate ? p.gate[t] : 1.0f;
+        const float gate = p.gate ? p.gate[t] : 1.0f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int row = min(max(r0 + k, 0), rows - 1);
-            if (p.bias) v[k] = v[k] * ga + bf16_to_f32(p.bias[n0 + row]);
-            else v[k] *= ga;
-            v[k] *= gate;
-            if (p.add) v[k] += bf16_to_f32(p.add[at + row]);
-          }
+        for (int k = 0; k < 8; ++k) {
+          const int row = min(max(r0 + k, 0), rows - 1);
+          if (p.bias) v[k] = v[k] * ga + bf16_to_f32(p.bias[n0 + row]);
+          else v[k] *= ga;
+          v[k] *= gate;
+          if (p.add) v[k] += bf16_to_f32(p.add[at + row]);
         }
         uint32_t o[8];
 #pragma unroll
@@ -347,7 +345,7 @@ moe_status launch(const DenseArgs& p, hipStream_t s) {
   constexpr int kRows = GU ? 128 : 256;
   const int row_tiles = (p.N + kRows - 1) / kRows;
   const int tiles = row_tiles * ((p.T + kTileTokens - 1) / kTileTokens);      // at most 2^26 (N and T up to 2^20)
-  const int grid = (tiles + kXcds - 1) / kXcds * kXcds + (p.token_gate ? (p.T + 3) / 4 : 0);
+  const int grid = (tiles + kXcds - 1) / kXcds * kXcds + (GU && p.token_gate ? (p.T + 3) / 4 : 0);
   quant_tile_kernel<FMT, GU, WIDE><<<(unsigned)grid, kTileThreads, 0, s>>>(p, row_tiles, tiles);
   return launch_status();
 }
