@@ -21,11 +21,23 @@ _SCORES = {"softmax": 0, "sigmoid": 1}                 # moe_score
 _FORMATS = {"nvfp4": (0, 16), "mxfp4": (1, 32)}        # moe_quant_format, weights per scale
 
 Tensor = torch.Tensor
+_MAX_INT = (1 << 31) - 1
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 # the device and stream queries of torch.cuda without their Python layers, where
 # this torch has them (one built without a GPU has not)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _int(value, name: str) -> int:
+    """A whole number of 32 bits, as the library takes sizes: ctypes would drop
+    what is beyond, and make another size of it."""
+    n = int(value)
+    if n != value:
+        raise ValueError(f"{name} must be a whole number, got {value!r}")
+    if not -_MAX_INT <= n <= _MAX_INT:
+        raise ValueError(f"{name} must be at most 2^31 - 1, got {n}")
+    return n
 
 
 def _call(name: str, index: int, *args):
@@ -73,8 +85,9 @@ class RouteRule(_Fixed):
                  group_top: int = 2, renormalise: bool = True, scale: float = 1.0):
         if score not in _SCORES:
             raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
-        self._set(k=int(k), score=score, groups=int(groups), group_top=int(group_top), renormalise=bool(renormalise),
-                  scale=float(scale), groups_kept=int(groups if groups_kept is None else groups_kept))
+        self._set(k=_int(k, "k"), score=score, groups=_int(groups, "groups"), group_top=_int(group_top, "group_top"),
+                  groups_kept=_int(groups if groups_kept is None else groups_kept, "groups_kept"),
+                  renormalise=bool(renormalise), scale=float(scale))
         self._set(_args=(_SCORES[score], self.groups, self.groups_kept, self.group_top, int(self.renormalise), self.scale))
 
 
@@ -85,6 +98,8 @@ def _route_args(logits, bias, rule, topk_idx, topk_w):
     if dtype is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     (T, E), k, dev, index = logits.shape, rule.k, logits.device, logits.get_device()
+    if T > _MAX_INT or E > _MAX_INT:
+        raise ValueError(f"logits must have at most 2^31 - 1 tokens and experts, got {T} and {E}")
     if index < 0 or not logits.is_contiguous():
         _need(logits, "logits", logits.dtype)
     if bias is not None:
@@ -145,6 +160,7 @@ class QuantWeight(_Fixed):
         N, K, device = codes.shape[0], 2 * codes.shape[1], codes.device
         if K % 32 != 0 or K == 0 or N == 0:
             raise ValueError(f"a 4-bit matrix needs N >= 1 and K a multiple of 32, got N={N}, K={K}")
+        _int(N, "N"), _int(K, "K")
         _need(codes, "codes", torch.uint8, None, device)
         _need(scales, "scales", torch.uint8, (N, K // group), device)
         if g_scale is not None:
@@ -167,6 +183,8 @@ def _check_quant_x(x, weight: QuantWeight) -> int:
     if not isinstance(x, Tensor) or x.dim() != 2:
         raise TypeError("x must be a [T, K] tensor")
     T = x.shape[0]
+    if T > _MAX_INT:
+        raise ValueError(f"x must have at most 2^31 - 1 tokens, got {T}")
     _tensor(x, "x", _BF16, (T, weight.K), weight.device, weight._index)
     return T
 
@@ -175,7 +193,7 @@ QUANT_SUMS_BYTES = 8 << 20         # MOE_QUANT_SUMS_BYTES
 
 
 def moe_quant_linear_workspace_size(T: int, N: int, K: int) -> int:
-    return int(load_library().moe_quant_linear_workspace_size(T, N, K))
+    return int(load_library().moe_quant_linear_workspace_size(_int(T, "T"), _int(N, "N"), _int(K, "K")))
 
 
 def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.Tensor] = None,
@@ -205,7 +223,7 @@ def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.
 
 
 def moe_quant_shared_expert_workspace_size(T: int, H: int, Is: int) -> int:
-    return int(load_library().moe_quant_shared_expert_workspace_size(T, H, Is))
+    return int(load_library().moe_quant_shared_expert_workspace_size(_int(T, "T"), _int(H, "H"), _int(Is, "Is")))
 
 
 def make_quant_shared_workspace(T: int, H: int, Is: int, device) -> torch.Tensor:

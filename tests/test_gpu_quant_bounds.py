@@ -129,3 +129,14 @@ def test_linear_mxfp4_scale_range(T, N, K):
         y = sme.moe_quant_linear(dev_bf16(bits(x)), sme.QuantWeight(to_dev(codes), to_dev(scales), None, "mxfp4"))
         ref, _ = oracle.quant_linear(bits(x), (codes, scales, None), "mxfp4")
         assert np.array_equal(f64(y), ref), (lo, size)
+
+
+def test_refuses_tokens_beyond_32_bits():
+    """2^32 + 1 tokens are not one (a tensor without memory: refused by its size, before anything else)."""
+    w = sme.QuantWeight(torch.zeros((64, 16), dtype=torch.uint8, device=DEV),
+                        torch.zeros((64, 1), dtype=torch.uint8, device=DEV), format="mxfp4")
+    x = torch.empty(((1 << 32) + 1, 32), dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="tokens"):
+        sme.moe_quant_linear(x, w)
+    with pytest.raises(ValueError, match="tokens"):
+        sme.moe_quant_shared_expert(x, w, w, w)

@@ -1,11 +1,12 @@
 """Host side of the grouped routing and the 4-bit products that needs no device:
-workspace sizes over batches, and importing the package on a torch without a GPU."""
+workspace sizes over batches, sizes beyond 32 bits, and importing the package on a torch without a GPU."""
 
 import os
 import subprocess
 import sys
 
 import pytest
+import torch
 
 import sparse_moe_expert_amd as sme
 import sparse_moe_expert_amd.build
@@ -46,3 +47,25 @@ def test_import_without_gpu_functions():
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == ["4"]
+
+
+def test_sizes_beyond_32_bits():
+    """The library takes sizes of 32 bits; 2^32 + 8 is not 8."""
+    for kw in (dict(k=(1 << 32) + 8), dict(k=8, groups=(1 << 32) + 1), dict(k=8, groups=2, groups_kept=1 - (1 << 32)),
+               dict(k=8, group_top=(1 << 32) + 2)):
+        with pytest.raises(ValueError, match="at most"):
+            sme.RouteRule(**kw)
+    with pytest.raises(ValueError, match="whole number"):
+        sme.RouteRule(4.5)
+    assert sme.RouteRule(4.0).k == 4
+    for T, E in (((1 << 32) + 1, 1), (1, (1 << 32) + 1)):
+        with pytest.raises(ValueError, match="at most"):
+            sme.moe_route_grouped(torch.empty((T, E), device="meta"), None, sme.RouteRule(1))
+    with pytest.raises(ValueError, match="at most"):
+        sme.QuantWeight(torch.empty(((1 << 32) + 1, 16), dtype=torch.uint8, device="meta"),
+                        torch.empty(((1 << 32) + 1, 1), dtype=torch.uint8, device="meta"), format="mxfp4")
+    for sizes in (((1 << 32) + 64, 4096, 4096), (64, (1 << 32) + 4096, 4096), (64, 4096, (1 << 32) + 4096)):
+        for size in (sme.moe_quant_linear_workspace_size, sme.moe_quant_shared_expert_workspace_size):
+            with pytest.raises(ValueError, match="at most"):
+                size(*sizes)
+    assert sme.moe_quant_linear_workspace_size(-1, 64, 64) == 0
