@@ -209,7 +209,7 @@ def moe_quant_linear(x: torch.Tensor, weight: QuantWeight, bias: Optional[torch.
     else:
         _tensor(y, "y", _BF16, (T, N), dev, index)
     if workspace is not None:
-        _tensor(workspace, "workspace", _U8, workspace.shape, dev, index)
+        _tensor(workspace, "workspace", _U8, getattr(workspace, "shape", None), dev, index)
     elif T > 4 or weight.K > 8192:                   # no workspace below that
         need = load_library().moe_quant_linear_workspace_size(T, N, weight.K)
         workspace = torch.empty((need,), dtype=_U8, device=dev) if need else None
@@ -260,7 +260,7 @@ def moe_quant_shared_expert(x: torch.Tensor, gate: QuantWeight, up: QuantWeight,
     if workspace is None:
         workspace = torch.empty((moe_quant_shared_expert_workspace_size(T, H, Is),), dtype=_U8, device=dev)
     else:
-        _tensor(workspace, "workspace", _U8, workspace.shape, dev, index)
+        _tensor(workspace, "workspace", _U8, getattr(workspace, "shape", None), dev, index)
     x_at, y_at = x.data_ptr(), y.data_ptr()
     if x_at == y_at and T > 0:
         raise ValueError("y must not be x: its rows are written while x is read")

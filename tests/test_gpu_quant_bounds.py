@@ -140,3 +140,16 @@ def test_refuses_tokens_beyond_32_bits():
         sme.moe_quant_linear(x, w)
     with pytest.raises(ValueError, match="tokens"):
         sme.moe_quant_shared_expert(x, w, w, w)
+
+
+def test_refuses_a_workspace_that_is_no_tensor():
+    w = sme.QuantWeight(torch.zeros((32, 16), dtype=torch.uint8, device=DEV),
+                        torch.zeros((32, 1), dtype=torch.uint8, device=DEV), format="mxfp4")
+    x = torch.zeros((2, 32), dtype=torch.bfloat16, device=DEV)
+    for workspace in (bytearray(1024), 1024):
+        with pytest.raises(TypeError, match="workspace"):
+            sme.moe_quant_linear(x, w, workspace=workspace)
+        with pytest.raises(TypeError, match="workspace"):
+            sme.moe_quant_shared_expert(x, w, w, w, workspace=workspace)
+    with pytest.raises(ValueError, match="contiguous"):
+        sme.moe_quant_linear(x, w, workspace=torch.zeros((64, 32), dtype=torch.uint8, device=DEV).t())
