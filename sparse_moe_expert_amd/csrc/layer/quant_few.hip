@@ -27,9 +27,9 @@
 // than 16 tokens are workgroups of 8 or 16 each, while the weights are so small
 // that reading them again costs less than joining a split reduction.
 //
-// T = 1 4096x12288 shared expert (MXFP4, 80 MB): 16.6 us, 4.8 TB/s, as a large
-// copy; T = 1 9999x4096 7.4 us (23 MB); T = 4 10240x2560 (MXFP4, 14 MB) 5.7 us,
-// T = 1 2048x2048 3.0 us, of which 2.5 a launch.
+// T = 1 4096x12288 shared expert (MXFP4, 80 MB): 16.6 to 16.8 us, 4.8 TB/s, as a
+// large copy; T = 1 9999x4096 7.0 us (23 MB); T = 4 10240x2560 (MXFP4, 14 MB) 6.0 to
+// 6.4 us, T = 1 2048x2048 3.2 us, of which 2.5 a launch.
 #include "quant_common.h"
 
 #include <type_traits>
@@ -319,6 +319,12 @@ moe_status dispatch(const DenseArgs& p, hipStream_t s) {
 // 2048x4096, T = 32 (its pair 36 MB): 18.6 against 16.2; 4096x1024, T = 17 (36 MB): 12.0 against
 // 14.9.  Past kFewBytes it
 // never was the faster one.
+// Whole shared experts, NVFP4, their pair by this kernel and by the split one:
+// 2048x512 T = 64 9.4 and 12.5, T = 100 12.1 and 14.5, T = 150 14.6 and 15.1; 2560x640
+// T = 64 14.2 and 16.5, T = 100 15.7 both (MXFP4 14.7 and 15.1); 4096x1024 T = 32 12.9
+// and 14.4; 2048x2048 T = 32 11.9 and 12.0.  A pair's estimate is too low for its
+// largest batches, the last before the rule changes over: 2560x640 T = 150 19.6 and
+// 16.5, 2048x512 T = 200 17.3 and 15.4.
 constexpr float kFewRate = 7e6f, kSplitMore = 1.0f, kSplitPairMore = 0.65f;      // bytes a us, us
 constexpr long long kFewBytes = 60 * 1000 * 1000;
 

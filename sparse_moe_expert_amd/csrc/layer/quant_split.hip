@@ -28,9 +28,10 @@
 // quant_join_kernel adds them in order and finishes the outputs.
 //
 // Bound by the steps, each a barrier with one workgroup a compute unit, more
-// than by bytes: T = 32 9999x4096 12.6 us, of which 8 steps on 157 of the 256
-// compute units are 9 (the weights, 23 MB, take 4.8 us at the rate of a copy);
+// than by bytes: T = 32 9999x4096 11 to 12 us, most of it 8 steps on 157 of the
+// 256 compute units (the weights, 23 MB, take 4.8 us at the rate of a copy);
 // splitting each tile in two takes a unit's time off and adds the join's.
+// MXFP4, T = 32: 9999x4096 10.5 us, 10240x2560 8.0 to 8.7 (14 MB, 3.0 us).
 #include "quant_common.h"
 
 #include <type_traits>
@@ -48,8 +49,8 @@ constexpr int kMaxSplits = 16;
 // Reduction indices of a step, and the multiple of them that a part of the
 // reduction starts at.  NVFP4, whose weights take twice MXFP4's instructions,
 // has fewer barriers with longer steps, three stages of which LDS holds for up
-// to 32 tokens: T = 32 9999x4096, 512: 13.2 us, 256: 15.0; MXFP4, T = 32
-// 10240x2560, with less of its loads in flight: 11.0 and 9.8.
+// to 32 tokens: T = 32 9999x4096, measured in turn, 512: 13.2 us, 256: 15.0; MXFP4,
+// T = 32 10240x2560, with less of its loads in flight: 11.0 and 9.8.
 constexpr int split_unit(int rows, int tokens) { return rows == 64 && tokens <= 32 ? 512 : 256; }
 constexpr int split_step(int format, int rows, int tokens) {
   return format == MOE_QUANT_NVFP4 ? split_unit(rows, tokens) : 256;

@@ -14,9 +14,10 @@
 // row's codes and scales of a step, and with two workgroups there those are
 // out again before the next step asks for the rest of the line.  So a row's
 // codes of two steps are loaded together, and its scales of four: 4096^3
-// (NVFP4) 140 us loaded step by step, 128 with both by twos, 121 so; more do
-// not fit the registers.  A bf16 library product of the size takes 106 us (of
-// which 35 us power: it takes 67 us on zeros).
+// (NVFP4) 140 us loaded step by step, 128 with both by twos, 121 so (118 to 127
+// over boxes, MXFP4 112 to 116); more do not fit the registers.  A bf16 library
+// product of the size takes 106 us (of which 35 us power: it takes 67 us on
+// zeros).
 //
 // Tokens go straight to a ring of four LDS stages (16-byte chunk c of token
 // row r at c ^ ((r >> 1) & 7): the reads of 16 lanes hit all banks), codes and
@@ -291,7 +292,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void quant_tile_kernel(DenseArgs p
     if (!GU && p.N % 8 != 0) {
       // Output rows that do not start at 16 bytes (never a pair's): pieces of eight that do,
       // which begin up to seven rows before the tile, the outer ones one by
-      // one.  2048x4095x4096: 79.5 us, 92 with all outputs one by one (N = 4096: 71).
+      // one.  2048x4095x4096: 79.5 us, 92 with all outputs one by one (N = 4096: 71);
+      // with a bias, read one by one, 88 (69).
       constexpr int kPieces = kRows / 8 + 1;
       for (int i = tid; i < here * kPieces; i += kTileThreads) {
         const int tok = i / kPieces, t = t0 + j0 * 32 + tok;
