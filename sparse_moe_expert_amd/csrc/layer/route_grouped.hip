@@ -308,7 +308,7 @@ __global__ __launch_bounds__(256) void invert_kernel(const int32_t* __restrict__
 
 // With the selection, E = 256, k = 8, counted by every workgroup and counted
 // once (four launches): 65536 routes 22.9 and 26.9 us, 131072 40.8 and 39.6,
-// 240000 64.5 and 57.4 (the bytes 7; by a tracer the selection 44, the four
+// 240000 64.5 and 57.4 (the bytes 7; by a tracer the selection 40 to 44, the four
 // launches 24: each passes over the routes in little more than a launch's
 // time, the prefix over 118 chunks is one workgroup's 8.6).
 constexpr int kChunkRoutes = (1 << 17) - 1;

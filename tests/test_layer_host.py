@@ -1,7 +1,11 @@
 """Host side of the grouped routing and the 4-bit products that needs no device:
-workspace sizes over batches, sizes beyond 32 bits, and importing the package on a torch without a GPU."""
+workspace sizes over batches, sizes beyond 32 bits, importing the package on a torch
+without a GPU; and that the profile of their kernels is of the sources as they stand."""
 
+import glob
+import hashlib
 import os
+import re
 import subprocess
 import sys
 
@@ -69,3 +73,18 @@ def test_sizes_beyond_32_bits():
             with pytest.raises(ValueError, match="at most"):
                 size(*sizes)
     assert sme.moe_quant_linear_workspace_size(-1, 64, 64) == 0
+
+
+def test_profile_names_the_current_sources():
+    """The summary of these operators' kernels names the digest of csrc/layer/*.hip and *.h (contents concatenated in
+    sorted path order), which that of csrc/*.hip and *.h does not cover."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    layer = os.path.join(root, "sparse_moe_expert_amd", "csrc", "layer")
+    h = hashlib.sha256()
+    for name in sorted(glob.glob(os.path.join(layer, "*.hip")) + glob.glob(os.path.join(layer, "*.h"))):
+        with open(name, "rb") as f:
+            h.update(f.read())
+    with open(os.path.join(root, "profiles", "layer_operators_kernel_stats.md")) as f:
+        m = re.search(r"csrc/layer/[^`]*sha256 prefix: `([0-9a-f]{16})`", f.read())
+    assert m, "the summary names no digest of csrc/layer"
+    assert m.group(1) == h.hexdigest()[:16], "the summary was taken on other sources"
