@@ -31,7 +31,7 @@
 // than by bytes: T = 32 9999x4096 11 to 12 us, most of it 8 steps on 157 of the
 // 256 compute units (the weights, 23 MB, take 4.8 us at the rate of a copy);
 // splitting each tile in two takes a unit's time off and adds the join's.
-// MXFP4, T = 32: 9999x4096 10.5 us, 10240x2560 8.0 to 8.7 (14 MB, 3.0 us).
+// MXFP4, T = 32: 9999x4096 10.5 us, 10240x2560 8 to 9 (14 MB, 3.0 us).
 #include "quant_common.h"
 
 #include <type_traits>

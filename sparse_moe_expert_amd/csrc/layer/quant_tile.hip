@@ -15,9 +15,9 @@
 // out again before the next step asks for the rest of the line.  So a row's
 // codes of two steps are loaded together, and its scales of four: 4096^3
 // (NVFP4) 140 us loaded step by step, 128 with both by twos, 121 so (118 to 127
-// over boxes, MXFP4 112 to 116); more do not fit the registers.  A bf16 library
-// product of the size takes 106 us (of which 35 us power: it takes 67 us on
-// zeros).
+// from card to card, MXFP4 112 to 119); more do not fit the registers.  A bf16
+// library product of the size takes 106 us (of which 35 us power: it takes 67 us
+// on zeros).
 //
 // Tokens go straight to a ring of four LDS stages (16-byte chunk c of token
 // row r at c ^ ((r >> 1) & 7): the reads of 16 lanes hit all banks), codes and
