@@ -2,10 +2,10 @@
 
 The 8-bit (e4m3) form of one sparse-MoE layer, a scale for each 128 values of a token and for each 128 x 128 block of a
 weight:
-  norm      moe_norm_fp8         r = x + residual; y = RMSNorm(r) * weight; y in 8 bits (and in bf16, for the router)
-  quantize  moe_fp8_quantize     tokens in 8 bits
-  linear    moe_fp8_linear       y = x W^T + bias, tokens and weights in 8 bits
-  ffn       moe_fp8_expert_ffn   the routed experts, their products grouped by expert:
+  norm      moe_norm_quantize         r = x + residual; y = RMSNorm(r) * weight; y in 8 bits (and in bf16, for the router)
+  quantize  moe_block_quantize     tokens in 8 bits
+  linear    moe_block_linear       y = x W^T + bias, tokens and weights in 8 bits
+  ffn       moe_block_expert_ffn   the routed experts, their products grouped by expert:
                                  y_t = sum_j w_tj W_down,e h_tj with h_tj = SiLU(W_gate,e x_t) * (W_up,e x_t) in 8 bits
 
 With `own` false, run() computes them with elementary torch operations; with `own` true it calls the library.
@@ -158,7 +158,7 @@ def prepare(case, seed):
         if own:
             import sparse_moe_expert_amd as sme
             s["x"], s["w"] = sme.Fp8Tokens(*s["x"]), sme.Fp8Weight(*s["w"])
-            s["ws"] = sme.make_fp8_linear_workspace(DEV)
+            s["ws"] = sme.make_block_linear_workspace(DEV)
         return s
     H, I, E, k = case["H"], case["I"], case["E"], case["k"]
     s["x"] = _tokens(_activations(gen, T, H))
@@ -181,7 +181,7 @@ def prepare(case, seed):
         s["x"] = sme.Fp8Tokens(*s["x"])
         s["experts"] = sme.Fp8Experts(*s["gate"], *s["up"], *s["down"])
         s["buckets"] = sme.moe_bucket_routes(s["idx"], E)
-        s["ws"] = sme.make_fp8_ffn_workspace(T, H, I, E, k, DEV)
+        s["ws"] = sme.make_block_ffn_workspace(T, H, I, E, k, DEV)
     return s
 
 
@@ -241,14 +241,14 @@ def _own_run(s):
     import sparse_moe_expert_amd as sme
     c = s["case"]
     if c["op"] == "norm":
-        tokens, r = sme.moe_norm_fp8(s["x"], s["weight"], s["residual"], eps=1e-6, weight_offset=c["offset"], out=s["out"],
+        tokens, r = sme.moe_norm_quantize(s["x"], s["weight"], s["residual"], eps=1e-6, weight_offset=c["offset"], out=s["out"],
                                      residual_out=s["residual_out"], y=s["y"])
         return tokens.q, tokens.scale, r, s["y"]
     if c["op"] == "quantize":
-        return tuple(sme.moe_fp8_quantize(s["x"], s["out"]))
+        return tuple(sme.moe_block_quantize(s["x"], s["out"]))
     if c["op"] == "linear":
-        return sme.moe_fp8_linear(s["x"], s["w"], s["bias"], s["y"], s["ws"])
-    return sme.moe_fp8_expert_ffn(s["x"], s["experts"], s["w"], s["buckets"], s["ws"], s["y"])
+        return sme.moe_block_linear(s["x"], s["w"], s["bias"], s["y"], s["ws"])
+    return sme.moe_block_expert_ffn(s["x"], s["experts"], s["w"], s["buckets"], s["ws"], s["y"])
 
 
 def run(state):
