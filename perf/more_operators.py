@@ -2,7 +2,7 @@
 
 The 8-bit (e4m3) form of one sparse-MoE layer, a scale for each 128 values of a token and for each 128 x 128 block of a
 weight:
-  norm      moe_norm_quantize         r = x + residual; y = RMSNorm(r) * weight; y in 8 bits (and in bf16, for the router)
+  norm      moe_norm_quantize      r = x + residual; y = RMSNorm(r) * weight; y in 8 bits (and in bf16, for the router)
   quantize  moe_block_quantize     tokens in 8 bits
   linear    moe_block_linear       y = x W^T + bias, tokens and weights in 8 bits
   ffn       moe_block_expert_ffn   the routed experts, their products grouped by expert:
