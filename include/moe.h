@@ -708,6 +708,125 @@ moe_status moe_quant_shared_expert(int format, const uint16_t* x,
                                    void* workspace, size_t workspace_bytes,
                                    uint16_t* y, void* stream);
 
+/*
+ * Block-scaled 8-bit values: e4m3 (OCP E4M3FN) codes with fp32 scales.
+ *   tokens  [T, K] codes and [T, ceil(K/128)] scales, one for 128 consecutive
+ *           values of a row (the row's last block may be shorter)
+ *   weights [N, K] codes and [ceil(N/128), ceil(K/128)] scales, one for a
+ *           block of 128 x 128 (shorter at the edges)
+ * A value is its code times its scale.  Weight scales are finite; a token's
+ * are what moe_norm_quantize and moe_block_quantize write, or any finite ones.
+ * K (and H and I) are multiples of 16.
+ *
+ * Encoding of values v: per block s = max(amax |v| / 448, 2^-126), codes
+ * e4m3(v / s), to nearest even.  An infinite or NaN v has no part in amax and
+ * its code is NaN (e4m3 has no infinities); a product with it is NaN, in the
+ * outputs of its own token only.
+ *
+ * moe_norm_quantize — residual addition, RMS norm and encoding in one pass.
+ *
+ * Defines, per token,
+ *   r = x + residual, rounded once to the residual's type (r = x without one),
+ *   y = r / sqrt(mean(r^2) + eps) * (weight + weight_offset),
+ * mean over the H values of the rounded r, summed in fp64, and writes r, the
+ * encoding of y and, where `y` is not NULL, y as bf16 (of the same fp32 values,
+ * for a consumer such as moe_router_logits).
+ *   x             [T, H] bf16 bits       in
+ *   residual      [T, H] of residual_type (a moe_dtype) or NULL  in
+ *   weight        [H] bf16 bits          in
+ *   weight_offset 0, or 1 where weights are stored as their distance from one
+ *   eps           1e-30 or more
+ *   residual_out  as residual; may be residual itself; NULL where that is  out
+ *   y             [T, H] bf16 bits or NULL   out
+ *   q, scale      tokens [T, H]          out
+ * No output overlaps another or an input, but for residual_out and residual.
+ * Shapes: T >= 0 (T = 0 launches nothing), H a multiple of 16, eps and
+ * weight_offset finite (else MOE_ERR_INVALID_SHAPE).  Envelope: H up to 2^15,
+ * T up to 2^20 (else MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_norm_quantize(const uint16_t* x, const void* residual, int residual_type,
+                             const uint16_t* weight, float weight_offset, float eps, int T, int H,
+                             void* residual_out, uint16_t* y, uint8_t* q, float* scale, void* stream);
+
+/*
+ * moe_block_quantize — bf16 activations x [T, K] as block-scaled tokens
+ * (q, scale), encoded as above.  Shapes and envelope as for
+ * moe_norm_quantize; q and scale overlap nothing.
+ */
+moe_status moe_block_quantize(const uint16_t* x, int T, int K, uint8_t* q, float* scale, void* stream);
+
+/*
+ * Bytes of device workspace moe_block_linear needs: the fp32 sums of the parts
+ * that the reduction is split into, 0 where it is not split.  Never above
+ * MOE_BLOCK_SUMS_BYTES, which serve every call.
+ */
+#define MOE_BLOCK_SUMS_BYTES (16u << 20)
+size_t moe_block_linear_workspace_size(int T, int N, int K);
+
+/*
+ * moe_block_linear — a dense layer on block-scaled tokens and weights.
+ *
+ * Defines y[t,n] = bf16( sum_b x_scale[t,b] * w_scale[n/128,b] * d + bias[n] ),
+ * d the sum of the codes' products over the 128 reduction indices of block b;
+ * sums are fp32 in a fixed order and y is rounded once (RNE).  d is the matrix
+ * cores' 8-bit product: of the products of 8 neighbouring indices, bits more
+ * than 13 below the largest's leading one are dropped before they are added.
+ *   x, x_scale  tokens [T, K]            in
+ *   w, w_scale  a weight [N, K]          in
+ *   bias        [N] bf16 bits or NULL    in
+ *   workspace   >= moe_block_linear_workspace_size(T, N, K) bytes, owned by
+ *               the caller (NULL where that is 0); contents unspecified,
+ *               never needs a reset
+ *   y           [T, N] bf16 bits         out  overlaps no input
+ * Shapes: T >= 0 (T = 0 launches nothing), N >= 1 (any), K a multiple of 16
+ * (else MOE_ERR_INVALID_SHAPE).  Envelope: N and T up to 2^20, K up to 2^15
+ * (else MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_block_linear(const uint8_t* x, const float* x_scale,
+                            const uint8_t* w, const float* w_scale, const uint16_t* bias,
+                            int T, int N, int K, void* workspace, size_t workspace_bytes,
+                            uint16_t* y, void* stream);
+
+/*
+ * Bytes of device workspace moe_block_expert_ffn needs (0 when T <= 0 or the
+ * sizes are outside the call's envelope); grows with T.
+ */
+size_t moe_block_expert_ffn_workspace_size(int T, int H, int I, int E, int k);
+
+/*
+ * moe_block_expert_ffn — moe_expert_ffn with block-scaled tokens and experts.
+ *
+ * Defines, per route p = (t, j) with expert e = topk_idx[t,j],
+ *   h_p = SiLU(Wg_e x_t) * (Wu_e x_t) in fp32, then encoded as above,
+ *   o_p = Wd_e h_p,
+ *   y_t = sum_j topk_w[t,j] * o_(t,j), in slot order, rounded once to bf16,
+ * products and sums as in moe_block_linear.  Each chosen expert's weights are
+ * read once for all of its routes.
+ *   x, x_scale           tokens [T, H]             in
+ *   w_gate/w_up, s_*     E weights [I, H]: codes [E, I, H], scales
+ *                        [E, ceil(I/128), ceil(H/128)]    in
+ *   w_down, s_down       E weights [H, I]          in
+ *   topk_w, bucket arrays, k   as for moe_expert_ffn      in
+ *   workspace            >= moe_block_expert_ffn_workspace_size(T,H,I,E,k)
+ *                        bytes, owned by the caller; contents unspecified,
+ *                        never needs a reset
+ *   y                    [T, H] bf16 bits          out  overlaps no input
+ * Shapes: T >= 0 (T = 0 launches nothing), 1 <= k <= E, H and I multiples of
+ * 16.  Envelope: E <= 1024, k <= 32, H and I up to 2^15, T*k <= 2^24,
+ * T*H < 2^31 (else MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scale,
+                                const uint8_t* w_gate, const float* s_gate,
+                                const uint8_t* w_up, const float* s_up,
+                                const uint8_t* w_down, const float* s_down,
+                                const float* topk_w,
+                                const int32_t* expert_count, const int32_t* expert_offset,
+                                const int32_t* active_experts, const int32_t* n_active,
+                                const int32_t* route_src, const int32_t* route_pos,
+                                int T, int H, int I, int E, int k,
+                                void* workspace, size_t workspace_bytes,
+                                uint16_t* y, void* stream);
+
 /* Static English description of a status code (never NULL). */
 const char* moe_status_string(moe_status s);
 

@@ -15,6 +15,7 @@ What it computes (one routed-MoE step of a decode/verify batch):
   shared_expert_output  the dense BF16 shared expert for every token
   route_grouped   routing by scores, with a balance bias and groups
   quant_linear, quant_shared_expert  dense products with 4-bit weights
+  block           block-scaled 8-bit values: encoding, norm, dense product, routed experts
 
 Sources: the routing rule of the fused MoE routing kernel (page "How I forked
 vLLM and made Qwen3.8-Flash-Next decode 1.6x faster on one GPU", section
@@ -41,11 +42,13 @@ from .ffn import expert_route_output, moe_output, ExpertDecoder
 from .shared import shared_expert_output
 from .grouped import route_grouped
 from .quant import quant_linear, quant_shared_expert
+from . import block
 
 __all__ = [
     "route_grouped",
     "quant_linear",
     "quant_shared_expert",
+    "block",
     "shared_expert_output",
     "E2M1_VALUES",
     "e4m3_table",

@@ -58,6 +58,12 @@ SIGNATURES = {
     "moe_quant_linear": (_I, [_I] + [_P] * 5 + [_I] * 3 + [_P, ctypes.c_size_t, _P, _P]),
     "moe_quant_shared_expert_workspace_size": (ctypes.c_size_t, [_I, _I, _I]),
     "moe_quant_shared_expert": (_I, [_I] + [_P] * 12 + [_I] * 3 + [_P, ctypes.c_size_t, _P, _P]),
+    "moe_norm_quantize": (_I, [_P, _P, _I, _P, ctypes.c_float, ctypes.c_float, _I, _I] + [_P] * 5),
+    "moe_block_quantize": (_I, [_P, _I, _I, _P, _P, _P]),
+    "moe_block_linear_workspace_size": (ctypes.c_size_t, [_I, _I, _I]),
+    "moe_block_linear": (_I, [_P] * 5 + [_I] * 3 + [_P, ctypes.c_size_t, _P, _P]),
+    "moe_block_expert_ffn_workspace_size": (ctypes.c_size_t, [_I] * 5),
+    "moe_block_expert_ffn": (_I, [_P] * 15 + [_I] * 5 + [_P, ctypes.c_size_t, _P, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
 }
 

@@ -21,8 +21,10 @@ from ._lib import (
     moe_expert_ffn,
     moe_route_bucket,
     moe_route_topk,
+    moe_router_logits,
     moe_step,
 )
+from .block import Fp8Experts, empty_fp8_tokens, make_block_ffn_workspace, moe_block_expert_ffn, moe_norm_quantize
 from .layer import RouteRule, moe_route_grouped, moe_route_grouped_bucket
 
 
@@ -107,3 +109,45 @@ class MoeStep:
             self.routing(logits, bias)
             self.ffn(x, weights)
         return self.y
+
+
+class Fp8MoeStep:
+    """The step in 8 bits, from the attention's output on: residual addition and
+    norm, router, routing and buckets, the routed experts, all outputs and the
+    workspace owned here (and the step capturable) as in MoeStep.
+
+    run() computes r = x + residual and n = RMSNorm(r) * (norm_weight +
+    weight_offset), routes n (moe_router_logits on n in bf16; top-k, or by
+    `rule`) and returns y, the experts' output for n in 8 bits.  `residual`
+    (bf16, or fp32 with residual_dtype) holds r afterwards; the next layer's x
+    is y."""
+
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, rule: Optional[RouteRule] = None,
+                 residual_dtype: torch.dtype = torch.bfloat16, eps: float = 1e-6, weight_offset: float = 0.0):
+        if residual_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"residual_dtype must be bfloat16 or float32, got {residual_dtype}")
+        if rule is not None and rule.k != k:
+            raise ValueError(f"rule.k must be k={k}, got {rule.k}")
+        self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
+        self.rule, self.eps, self.weight_offset = rule, eps, weight_offset
+        self.device = torch.device(device)
+        self.residual = torch.empty((T, H), dtype=residual_dtype, device=self.device)
+        self.hidden = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+        self.tokens = empty_fp8_tokens(T, H, self.device)
+        self.logits = torch.empty((T, E), dtype=torch.float32, device=self.device)
+        self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=self.device)
+        self.topk_w = torch.empty((T, k), dtype=torch.float32, device=self.device)
+        self.buckets = empty_buckets(T, E, k, self.device)
+        self.workspace = make_block_ffn_workspace(T, H, I, E, k, self.device)
+        self.y = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+
+    def run(self, x: torch.Tensor, residual: torch.Tensor, norm_weight: torch.Tensor, w_router: torch.Tensor,
+            bias: Optional[torch.Tensor], experts: Fp8Experts) -> torch.Tensor:
+        """The step of bf16 x [T,H]; `residual` [T,H] may be self.residual, of the step before."""
+        moe_norm_quantize(x, norm_weight, residual, self.eps, self.weight_offset, self.tokens, self.residual, self.hidden)
+        moe_router_logits(self.hidden, w_router, self.logits)
+        if self.rule is not None:
+            moe_route_grouped_bucket(self.logits, bias, self.rule, self.topk_idx, self.topk_w, self.buckets)
+        else:
+            moe_route_bucket(self.logits, bias, self.k, self.topk_idx, self.topk_w, self.buckets)
+        return moe_block_expert_ffn(self.tokens, experts, self.topk_w, self.buckets, self.workspace, self.y)
