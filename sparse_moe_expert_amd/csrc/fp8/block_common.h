@@ -42,6 +42,7 @@ inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 namespace {
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -55,13 +56,9 @@ __device__ __forceinline__ uint32_t to_bf16(float f) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
-// The 32 bytes of a lane: chunks at byte offsets a and b of a resource
-__device__ __forceinline__ i32x8 fragment(const uint4 lo, const uint4 hi) {
-  return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-}
-__device__ __forceinline__ i32x8 load_fragment(__amdgpu_buffer_rsrc_t r, uint32_t a, uint32_t b) {
-  return fragment(to_uint4(__builtin_amdgcn_raw_buffer_load_b128(r, a, 0, 0)),
-                  to_uint4(__builtin_amdgcn_raw_buffer_load_b128(r, b, 0, 0)));
+// The 32 bytes of a lane: two chunks
+__device__ __forceinline__ i32x8 fragment(const i32x4 lo, const i32x4 hi) {
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // One block's products (scale operands of 0: the instruction without scales)

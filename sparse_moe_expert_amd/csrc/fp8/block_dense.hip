@@ -1,10 +1,8 @@
 // A dense layer in 8 bits: moe_block_linear.
-#include "block_common.h"
+#include "block_tile.h"
 
 namespace moe {
 namespace {
-
-constexpr int kLinThreads = 256;
 
 struct LinearArgs {
   const uint8_t* x;
@@ -15,35 +13,108 @@ struct LinearArgs {
   int T, N, K;
 };
 
-// A wavefront to 16 rows and 16 tokens, operands straight from memory
-__global__ __launch_bounds__(kLinThreads) void linear_kernel(LinearArgs p, int row_groups) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
-  const int n0 = ((int)(blockIdx.x % row_groups) * 4 + wave) * 16, t0 = (int)(blockIdx.x / row_groups) * 16;
-  if (n0 >= p.N) return;
-  const int l16 = lane & 15, g = lane >> 4, kb = blocks_of(p.K);
-  const int t = min(t0 + l16, p.T - 1);
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w.q + (size_t)n0 * p.K, (uint32_t)(min(16, p.N - n0) * p.K));
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + (size_t)t0 * p.K, (uint32_t)(min(16, p.T - t0) * p.K));
+// y[t, n .. n+3] from their sums; outputs at or past N are left alone
+__device__ __forceinline__ void write4(const LinearArgs& p, int t, int n, f32x4 v) {
+  const size_t at = (size_t)t * p.N + n;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = to_bf16(p.bias ? v[i] + bf16_to_f32(p.bias[min(n + i, p.N - 1)]) : v[i]);
+  if (p.N % 4 == 0) {
+    *reinterpret_cast<uint2*>(p.y + at) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < p.N) p.y[at + i] = (uint16_t)o[i];
+  }
+}
+
+// Tiles of 256 rows by TT tokens; with more than one part of the reduction
+// (`splits`) fp32 sums go to [part][T][Np], Np rows of whole tiles.
+template <int TT>
+__global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs p, int row_tiles, int token_tiles, int splits,
+                                                                      float* __restrict__ sums) {
+  using T = Tile<TT, false>;
+  MOE_TILE_STAGES(T)
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / T::WT, wt = wave % T::WT;
+  const int tiles = row_tiles * token_tiles, per = (tiles + kXcds - 1) / kXcds;
+  const int part = (int)blockIdx.x / (per * kXcds), at = (int)blockIdx.x % (per * kXcds);
+  const int tile = at % kXcds * per + at / kXcds;
+  if (tile >= tiles) return;
+  // groups of four token tiles, row tile by row tile
+  const int group = tile / (4 * row_tiles), in = tile % (4 * row_tiles), width = min(4, token_tiles - group * 4);
+  const int n0 = in / width * kTileRows, t0 = (group * 4 + in % width) * TT;
+  const int rows = min(kTileRows, p.N - n0), toks = min(TT, p.T - t0), kb = blocks_of(p.K);
+  const int first = (int)((long long)kb * part / splits), steps = (int)((long long)kb * (part + 1) / splits) - first;
+
+  T tl;
+  const uint8_t* const w = p.w.q + (size_t)n0 * p.K;
+  tl.weights(w, w, rows, p.K, wave, lane);
+  tl.rx = make_rsrc(p.x + (size_t)t0 * p.K, (uint32_t)toks * (uint32_t)p.K);
+  tl.tokens(wave, lane, [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)p.K; });
   const float* const sw = p.w.s + (size_t)(n0 / kBlock) * kb;
-  const float* const sx = p.sx + (size_t)t * kb;
-  const uint32_t row = (uint32_t)(l16 * p.K);
-  f32x4 acc{};
-  for (int b = 0; b < kb; ++b) {
-    const int lo = b * kBlock + g * 16, hi = lo + 64;
-    const uint32_t a0 = lo < p.K ? row + lo : kOutside, a1 = hi < p.K ? row + hi : kOutside;
-    const f32x4 d = block_product(load_fragment(rw, a0, a1), load_fragment(rx, a0, a1));
-    const float s = sx[b] * sw[b];
+  tl.scales(p.sx + (size_t)t0 * kb, (uint32_t)toks * (uint32_t)kb * 4u, sw, rows > kBlock ? sw + kb : sw, kb, wave, lane,
+            [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)kb * 4u; });
+  const int live = (toks - wt * T::JT * 16 + 15) / 16;
+  tl.template run<true>(stage_at, wave, wr, wt, lane, first, steps, p.K, live);
+
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], s, acc[i]);
-  }
-  if (t0 + l16 >= p.T) return;
+  for (int j = 0; j < T::JT; ++j) {
+    const int r = (wt * T::JT + j) * 16 + (lane & 15);
+    if (r >= toks) continue;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = n0 + g * 4 + i;
-    if (n >= p.N) continue;
-    const float v = p.bias ? acc[i] + bf16_to_f32(p.bias[n]) : acc[i];
-    p.y[(size_t)t * p.N + n] = (uint16_t)to_bf16(v);
+    for (int m = 0; m < T::MT; ++m) {
+      const int n = n0 + T::row_of(wr, m) + (lane >> 4) * 4;
+      if (n >= p.N) continue;
+      if (splits > 1) {
+        const size_t np = (size_t)row_tiles * kTileRows;
+        *reinterpret_cast<f32x4*>(sums + ((size_t)part * p.T + t0 + r) * np + n) = tl.acc[m][j];
+      } else {
+        write4(p, t0 + r, n, tl.acc[m][j]);
+      }
+    }
   }
+}
+
+// The parts' sums, in order, to outputs: a thread to four of a token
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs p, int np, int splits, const float* __restrict__ sums) {
+  const int quads = (p.N + 3) / 4;
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const int t = (int)(i / (size_t)quads), n = (int)(i - (size_t)t * quads) * 4;
+  if (t >= p.T) return;
+  f32x4 v{};
+  for (int s = 0; s < splits; ++s) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(sums + ((size_t)s * p.T + t) * (size_t)np + n);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += a[k];
+  }
+  write4(p, t, n, v);
+}
+
+struct Plan {
+  int tt, row_tiles, token_tiles, splits;
+  size_t sums() const { return splits > 1 ? (size_t)splits * row_tiles * kTileRows * 4 : 0; }      // a token
+};
+
+Plan plan_of(int T, int N, int K) {
+  Plan pl;
+  pl.row_tiles = (N + kTileRows - 1) / kTileRows;
+  pl.tt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
+  if (pl.tt == 256 && (long long)pl.row_tiles * ((T + 255) / 256) < 160) pl.tt = 128;
+  pl.token_tiles = (T + pl.tt - 1) / pl.tt;
+  const int tiles = pl.row_tiles * pl.token_tiles, kb = blocks_of(K);
+  pl.splits = tiles >= 128 ? 1 : 256 / tiles;
+  if (pl.splits > kb) pl.splits = kb;
+  if (pl.splits > 16) pl.splits = 16;
+  while (pl.splits > 1 && pl.sums() * T > MOE_BLOCK_SUMS_BYTES) --pl.splits;
+  return pl;
+}
+
+template <int TT>
+void launch_tiles(const LinearArgs& p, const Plan& pl, float* sums, hipStream_t s) {
+  const int tiles = pl.row_tiles * pl.token_tiles;
+  const unsigned grid = (unsigned)((tiles + kXcds - 1) / kXcds * kXcds) * (unsigned)pl.splits;
+  linear_tile_kernel<TT><<<grid, kTileThreads, 0, s>>>(p, pl.row_tiles, pl.token_tiles, pl.splits, sums);
 }
 
 inline bool linear_dims_ok(int N, int K) { return N >= 1 && K >= 16 && K % 16 == 0; }
@@ -54,8 +125,8 @@ inline bool linear_dims_fit(int N, int K) { return N <= (1 << 20) && K <= kBlock
 
 extern "C" size_t moe_block_linear_workspace_size(int T, int N, int K) {
   using namespace moe;
-  (void)T, (void)N, (void)K;
-  return 0;
+  if (T <= 0 || T > kBlockMaxTokens || !linear_dims_ok(N, K) || !linear_dims_fit(N, K)) return 0;
+  return align256(plan_of(T, N, K).sums() * T);
 }
 
 extern "C" moe_status moe_block_linear(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
@@ -74,8 +145,19 @@ extern "C" moe_status moe_block_linear(const uint8_t* x, const float* x_scale, c
   if (need > 0 && !aligned16(workspace)) return MOE_ERR_MISALIGNED;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const LinearArgs p{x, x_scale, {w, w_scale}, bias, y, T, N, K};
-  const int row_groups = (N + 63) / 64;
-  const unsigned grid = (unsigned)row_groups * (unsigned)((T + 15) / 16);       // at most 2^14 * 2^16
-  linear_kernel<<<grid, kLinThreads, 0, static_cast<hipStream_t>(stream)>>>(p, row_groups);
+  const Plan pl = plan_of(T, N, K);
+  float* const sums = static_cast<float*>(workspace);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (pl.tt) {
+    case 16: launch_tiles<16>(p, pl, sums, s); break;
+    case 32: launch_tiles<32>(p, pl, sums, s); break;
+    case 64: launch_tiles<64>(p, pl, sums, s); break;
+    case 128: launch_tiles<128>(p, pl, sums, s); break;
+    default: launch_tiles<256>(p, pl, sums, s);
+  }
+  if (pl.splits > 1) {
+    const size_t quads = (size_t)T * ((N + 3) / 4);
+    linear_join_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(p, pl.row_tiles * kTileRows, pl.splits, sums);
+  }
   return launch_status();
 }

@@ -3,12 +3,13 @@
 //   h_r = SiLU(Wg_e x_t) * (Wu_e x_t) in fp32, then in 8 bits by blocks of 128
 //   o_r = Wd_e h_r
 //   y_t = bf16( sum_j w[t,j] o_(t,j) ), in slot order
-#include "block_common.h"
+#include "block_tile.h"
 
 namespace moe {
 namespace {
 
 constexpr int kFfnThreads = 256;
+constexpr int kPlanThreads = 1024;
 
 struct FfnArgs {
   const uint8_t* x;
@@ -23,95 +24,180 @@ struct FfnArgs {
   const int32_t* pos;
   uint16_t* y;
   int T, H, I, E, k;
-  float* h;                // [R, I], by bucket position, as are those below
+  // by bucket position
   uint8_t* hq;             // [R, I]
   float* hs;               // [R, blocks of I]
   float* o;                // [R, H]
+  int4* items;             // {expert, first position, routes, 0}; null: each chosen expert is one item
+  int* n_items;
 };
 
-// 16 rows of `w` times 16 token columns
-__device__ __forceinline__ f32x4 tile_product(const BlockMat& w, int e, int n0, int N, int K, const uint8_t* xrow,
-                                              const float* sx, int lane) {
-  const int l16 = lane & 15, g = lane >> 4, kb = blocks_of(K);
-  const __amdgpu_buffer_rsrc_t rw =
-      make_rsrc(w.q + ((size_t)e * N + n0) * (size_t)K, (uint32_t)(min(16, N - n0) * K));
-  const float* const sw = w.s + ((size_t)e * blocks_of(N) + n0 / kBlock) * (size_t)kb;
-  f32x4 acc{};
-  for (int b = 0; b < kb; ++b) {
-    const int lo = b * kBlock + g * 16, hi = lo + 64;
-    const uint32_t row = (uint32_t)(l16 * K);
-    const i32x8 a = load_fragment(rw, lo < K ? row + lo : kOutside, hi < K ? row + hi : kOutside);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const i32x8 x = fragment(lo < K ? *reinterpret_cast<const uint4*>(xrow + lo) : zero,
-                             hi < K ? *reinterpret_cast<const uint4*>(xrow + hi) : zero);
-    const f32x4 d = block_product(a, x);
-    const float s = sx[b] * sw[b];
+// An expert's routes in pieces of up to `tt`, experts in order
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(FfnArgs p, int tt) {
+  __shared__ int s_sum[kPlanThreads / kWave];
+  const int e = threadIdx.x, lane = e & (kWave - 1), wave = e >> 6;
+  const int count = e < p.E ? p.count[e] : 0, first = e < p.E ? p.offset[e] : 0;
+  const int pieces = (count + tt - 1) / tt;
+  int sum = pieces;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], s, acc[i]);
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int v = __shfl_up(sum, d, kWave);
+    if (lane >= d) sum += v;
   }
-  return acc;
+  if (lane == kWave - 1) s_sum[wave] = sum;
+  __syncthreads();
+  int at = sum - pieces;
+  for (int w = 0; w < wave; ++w) at += s_sum[w];
+  for (int i = 0; i < pieces; ++i) p.items[at + i] = make_int4(e, first + i * tt, min(tt, count - i * tt), 0);
+  if (e == kPlanThreads - 1) *p.n_items = at + pieces;
 }
 
-// grid (active experts, rows / 64): a wavefront to 16 rows, all of the expert's routes
-template <bool GU>
-__global__ __launch_bounds__(kFfnThreads) void experts_kernel(FfnArgs p) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
-  if ((int)blockIdx.x >= *p.n_active) return;
-  const int e = p.active[blockIdx.x], first = p.offset[e], count = p.count[e];
-  const int N = GU ? p.I : p.H, K = GU ? p.H : p.I;
-  const int n0 = ((int)blockIdx.y * 4 + wave) * 16;
-  if (n0 >= N) return;
-  for (int c = 0; c < count; c += 16) {
-    const int r = first + min(c + (lane & 15), count - 1);
-    const size_t row = GU ? (size_t)(p.src[r] / p.k) : (size_t)r;
-    const uint8_t* const x = (GU ? p.x : p.hq) + row * K;
-    const float* const sx = (GU ? p.sx : p.hs) + row * blocks_of(K);
-    f32x4 v = tile_product(GU ? p.gate : p.down, e, n0, N, K, x, sx, lane);
-    if constexpr (GU) {
-      const f32x4 u = tile_product(p.up, e, n0, N, K, x, sx, lane);
+// The workgroup's item and row tile: the items go round the XCDs, an item's row
+// tiles stay on one, whose L2 then holds its tokens.  False: none.
+__device__ __forceinline__ bool item_of(const FfnArgs& p, int row_tiles, int4& item, int& tile) {
+  const int i = (int)blockIdx.x / kXcds / row_tiles * kXcds + (int)blockIdx.x % kXcds;
+  tile = (int)blockIdx.x / kXcds % row_tiles;
+  if (p.items) {
+    if (i >= *p.n_items) return false;
+    item = p.items[i];
+  } else {
+    if (i >= *p.n_active) return false;
+    item.x = p.active[i];
+    item.y = p.offset[item.x];
+    item.z = p.count[item.x];
+  }
+  return true;
+}
+
+// h of 128 rows of an item's routes, in 8 bits: the rows are one block, whose
+// largest value goes from wave to wave through LDS
+template <int TT>
+__global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int row_tiles) {
+  using T = Tile<TT, true>;
+  MOE_TILE_STAGES(T)
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / T::WT, wt = wave % T::WT;
+  int4 item;
+  int tile;
+  if (!item_of(p, row_tiles, item, tile)) return;
+  const int e = item.x, first = item.y, toks = item.z;
+  const int n0 = tile * kBlock, rows = min(kBlock, p.I - n0), kb = blocks_of(p.H), ib = blocks_of(p.I);
+  T tl;
+  const size_t at = ((size_t)e * p.I + n0) * (size_t)p.H, at_s = ((size_t)e * ib + tile) * (size_t)kb;
+  tl.weights(p.gate.q + at, p.up.q + at, rows, p.H, wave, lane);
+  auto token = [&](int r) { return (uint32_t)(p.src[first + min(r, toks - 1)] / p.k); };
+  tl.rx = make_rsrc(p.x, (uint32_t)p.T * (uint32_t)p.H);
+  tl.tokens(wave, lane, [&](int r) { return token(r) * (uint32_t)p.H; });
+  tl.scales(p.sx, (uint32_t)p.T * (uint32_t)kb * 4u, p.gate.s + at_s, p.up.s + at_s, kb, wave, lane,
+            [&](int r) { return token(r) * (uint32_t)kb * 4u; });
+  const int live = (toks - wt * T::JT * 16 + 15) / 16;
+  tl.template run<false>(stage_at, wave, wr, wt, lane, 0, kb, p.H, live);
+
+  constexpr int HT = T::MT / 2;
+  const int g = lane >> 4;
+  uint32_t* const s_max = reinterpret_cast<uint32_t*>(s_0);            // [WR][TT]
+  __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
-    }
-    if (c + (lane & 15) >= count) continue;
+  for (int j = 0; j < T::JT; ++j) {
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + (lane >> 4) * 4 + i;
-      if (n < N) (GU ? p.h : p.o)[(size_t)r * N + n] = v[i];
+    for (int m = 0; m < HT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float h = silu(tl.acc[m][j][i]) * tl.acc[m + HT][j][i];
+        tl.acc[m][j][i] = h;
+        top = max(top, finite_bits(h));
+      }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
+    if (g == 0) s_max[wr * TT + (wt * T::JT + j) * 16 + lane] = top;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < T::JT; ++j) {
+    const int r = (wt * T::JT + j) * 16 + (lane & 15);
+    if (r >= toks) continue;
+    uint32_t top = 0;
+#pragma unroll
+    for (int w = 0; w < T::WR; ++w) top = max(top, s_max[w * TT + r]);
+    const float s = block_scale(__uint_as_float(top)), inv = 1.0f / s;
+    const size_t row = (size_t)(first + r);
+    if (wr == 0 && g == 0) p.hs[row * ib + tile] = s;
+#pragma unroll
+    for (int m = 0; m < HT; ++m) {
+      const int n = n0 + T::row_of(wr, m) + g * 4;
+      const f32x4 v = tl.acc[m][j];
+      if (n < p.I) *reinterpret_cast<uint32_t*>(p.hq + row * p.I + n) = encode4(v[0], v[1], v[2], v[3], inv);
     }
   }
 }
 
-// h in 8 bits: 16 lanes to a block
-__global__ __launch_bounds__(kFfnThreads) void quantize_h_kernel(FfnArgs p, size_t blocks) {
-  const int ib = blocks_of(p.I);
-  const size_t block = (size_t)blockIdx.x * (kFfnThreads / 16) + (threadIdx.x >> 4);
-  if (block >= blocks) return;
-  const size_t r = block / (size_t)ib;
-  const int at = (int)(block - r * (size_t)ib) * kBlock + (threadIdx.x & 15) * 8;
-  float v[8] = {};
-  if (at < p.I)
-    for (int i = 0; i < 8; ++i) v[i] = p.h[r * p.I + at + i];
-  uint32_t m = 0;
-  for (int i = 0; i < 8; ++i) m = max(m, finite_bits(v[i]));
-  const float s = block_scale(__uint_as_float(max16(m)));
-  const float inv = 1.0f / s;
-  if (at >= p.I) return;
-  *reinterpret_cast<uint2*>(p.hq + r * p.I + at) =
-      make_uint2(encode4(v[0], v[1], v[2], v[3], inv), encode4(v[4], v[5], v[6], v[7], inv));
-  if ((threadIdx.x & 15) == 0) p.hs[block] = s;
+// o of 256 rows of an item's routes
+template <int TT>
+__global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int row_tiles) {
+  using T = Tile<TT, false>;
+  MOE_TILE_STAGES(T)
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / T::WT, wt = wave % T::WT;
+  int4 item;
+  int tile;
+  if (!item_of(p, row_tiles, item, tile)) return;
+  const int e = item.x, first = item.y, toks = item.z;
+  const int n0 = tile * kTileRows, rows = min(kTileRows, p.H - n0), kb = blocks_of(p.I);
+  T tl;
+  const uint8_t* const w = p.down.q + ((size_t)e * p.H + n0) * (size_t)p.I;
+  tl.weights(w, w, rows, p.I, wave, lane);
+  tl.rx = make_rsrc(p.hq + (size_t)first * p.I, (uint32_t)toks * (uint32_t)p.I);
+  tl.tokens(wave, lane, [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)p.I; });
+  const float* const sw = p.down.s + ((size_t)e * blocks_of(p.H) + n0 / kBlock) * (size_t)kb;
+  tl.scales(p.hs + (size_t)first * kb, (uint32_t)toks * (uint32_t)kb * 4u, sw, rows > kBlock ? sw + kb : sw, kb, wave, lane,
+            [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)kb * 4u; });
+  const int live = (toks - wt * T::JT * 16 + 15) / 16;
+  tl.template run<false>(stage_at, wave, wr, wt, lane, 0, kb, p.I, live);
+#pragma unroll
+  for (int j = 0; j < T::JT; ++j) {
+    const int r = (wt * T::JT + j) * 16 + (lane & 15);
+    if (r >= toks) continue;
+#pragma unroll
+    for (int m = 0; m < T::MT; ++m) {
+      const int n = n0 + T::row_of(wr, m) + (lane >> 4) * 4;
+      if (n < p.H) *reinterpret_cast<f32x4*>(p.o + (size_t)(first + r) * p.H + n) = tl.acc[m][j];
+    }
+  }
 }
 
+// A thread to four outputs of a token
 __global__ __launch_bounds__(kFfnThreads) void combine_kernel(FfnArgs p) {
-  const size_t at = (size_t)blockIdx.x * kFfnThreads + threadIdx.x;
-  const size_t t = at / (size_t)p.H;
-  if (t >= (size_t)p.T) return;
-  const int n = (int)(at - t * (size_t)p.H);
-  float sum = 0.0f;
+  const size_t i = (size_t)blockIdx.x * kFfnThreads + threadIdx.x;
+  const int quads = p.H / 4;
+  const int t = (int)(i / (size_t)quads), n = (int)(i - (size_t)t * quads) * 4;
+  if (t >= p.T) return;
+  float v[4] = {};
   for (int j = 0; j < p.k; ++j) {
-    const size_t route = t * p.k + j;
-    sum = fmaf(p.topk_w[route], p.o[(size_t)p.pos[route] * p.H + n], sum);
+    const size_t route = (size_t)t * p.k + j;
+    const f32x4 o = *reinterpret_cast<const f32x4*>(p.o + (size_t)p.pos[route] * p.H + n);
+    const float w = p.topk_w[route];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = fmaf(w, o[c], v[c]);
   }
-  p.y[at] = (uint16_t)to_bf16(sum);
+  *reinterpret_cast<uint2*>(p.y + (size_t)t * p.H + n) =
+      make_uint2(to_bf16(v[0]) | to_bf16(v[1]) << 16, to_bf16(v[2]) | to_bf16(v[3]) << 16);
+}
+
+// Tokens of a tile; up to that many the experts themselves are the items
+int tile_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+// Most items that R routes can make
+int most_items(size_t R, int E, int tt) {
+  const size_t experts = R < (size_t)E ? R : (size_t)E;
+  return (int)(experts + R / (size_t)tt);
+}
+
+template <int TT>
+void launch_products(const FfnArgs& p, int items, hipStream_t s) {
+  const unsigned groups = (unsigned)(items + kXcds - 1) / kXcds * kXcds;
+  const int up = blocks_of(p.I), down = (p.H + kTileRows - 1) / kTileRows;
+  gate_up_kernel<TT><<<groups * up, kTileThreads, 0, s>>>(p, up);
+  down_kernel<TT><<<groups * down, kTileThreads, 0, s>>>(p, down);
 }
 
 inline bool ffn_dims_ok(int T, int H, int I, int E, int k) {
@@ -129,7 +215,9 @@ extern "C" size_t moe_block_expert_ffn_workspace_size(int T, int H, int I, int E
   using namespace moe;
   if (T <= 0 || !ffn_dims_ok(T, H, I, E, k) || !ffn_dims_fit(T, H, I, E, k)) return 0;
   const size_t R = (size_t)T * (size_t)k;
-  return align256(R * I * 4) + align256(R * I) + align256(R * blocks_of(I) * 4) + align256(R * H * 4);
+  const int tt = tile_tokens(T);
+  return align256(R * I) + align256(R * blocks_of(I) * 4) + align256(R * H * 4) +
+         (T > tt ? align256((size_t)most_items(R, E, tt) * sizeof(int4)) + 256 : 0);
 }
 
 extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scale, const uint8_t* w_gate,
@@ -155,17 +243,25 @@ extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scal
   uint8_t* at = static_cast<uint8_t*>(workspace);
   auto take = [&](size_t n) { uint8_t* const b = at; at += align256(n); return b; };
   FfnArgs p{x, x_scale, {w_gate, s_gate}, {w_up, s_up}, {w_down, s_down}, topk_w, expert_count, expert_offset,
-            active_experts, n_active, route_src, route_pos, y, T, H, I, E, k, nullptr, nullptr, nullptr, nullptr};
-  p.h = reinterpret_cast<float*>(take(R * I * 4));
+            active_experts, n_active, route_src, route_pos, y, T, H, I, E, k, nullptr, nullptr, nullptr, nullptr, nullptr};
   p.hq = take(R * I);
   p.hs = reinterpret_cast<float*>(take(R * blocks_of(I) * 4));
   p.o = reinterpret_cast<float*>(take(R * H * 4));
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const unsigned experts = (unsigned)(R < (size_t)E ? R : (size_t)E);
-  experts_kernel<true><<<dim3(experts, (unsigned)(I + 63) / 64), kFfnThreads, 0, s>>>(p);
-  const size_t blocks = R * blocks_of(I);
-  quantize_h_kernel<<<(unsigned)((blocks + kFfnThreads / 16 - 1) / (kFfnThreads / 16)), kFfnThreads, 0, s>>>(p, blocks);
-  experts_kernel<false><<<dim3(experts, (unsigned)(H + 63) / 64), kFfnThreads, 0, s>>>(p);
-  combine_kernel<<<(unsigned)(((size_t)T * H + kFfnThreads - 1) / kFfnThreads), kFfnThreads, 0, s>>>(p);
+  const int tt = tile_tokens(T);
+  int items = (int)(R < (size_t)E ? R : (size_t)E);
+  if (T > tt) {
+    items = most_items(R, E, tt);
+    p.items = reinterpret_cast<int4*>(take((size_t)items * sizeof(int4)));
+    p.n_items = reinterpret_cast<int*>(take(4));
+    plan_kernel<<<1, kPlanThreads, 0, s>>>(p, tt);
+  }
+  switch (tt) {
+    case 16: launch_products<16>(p, items, s); break;
+    case 32: launch_products<32>(p, items, s); break;
+    case 64: launch_products<64>(p, items, s); break;
+    default: launch_products<128>(p, items, s);
+  }
+  combine_kernel<<<(unsigned)(((size_t)T * (H / 4) + kFfnThreads - 1) / kFfnThreads), kFfnThreads, 0, s>>>(p);
   return launch_status();
 }
