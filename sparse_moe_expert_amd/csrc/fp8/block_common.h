@@ -78,22 +78,30 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return max(v, rotated<1>(v));
 }
 
-// |v| as ordered bits, 0 for an infinity or NaN: such a value has no part in
-// its block's scale, and its code is NaN
-__device__ __forceinline__ bool is_finite(float v) { return (__float_as_uint(v) & 0x7FFFFFFFu) < 0x7F800000u; }
-__device__ __forceinline__ uint32_t finite_bits(float v) {
-  return is_finite(v) ? __float_as_uint(v) & 0x7FFFFFFFu : 0u;
+// The largest finite |v| of a thread's N values: an infinity or NaN has no part in
+// its block's scale, and its code is NaN.  As ordered bits.
+template <int N>
+__device__ __forceinline__ uint32_t largest(const float (&v)[N]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(v[i]));           // (NaN counts for nothing)
+  if (__builtin_expect(__any(top == __builtin_inff()), 0)) {
+    top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fabsf(v[i]) < __builtin_inff() ? fmaxf(top, fabsf(v[i])) : top;
+  }
+  return __float_as_uint(top);
 }
 
 // The scale of a block whose largest value is `amax`: the smallest that keeps
 // it within e4m3, and normal, so that its reciprocal is finite
 __device__ __forceinline__ float block_scale(float amax) { return fmaxf(amax / 448.0f, 0x1p-126f); }
 
-// Four values over the scale -> four codes, to nearest even
+// Four values over the scale -> four codes, to nearest even; beyond 464, and so
+// of an infinity, the conversion's code is NaN
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
-  auto code = [&](float v) { return is_finite(v) ? v * inv : __uint_as_float(0x7FC00000u); };
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(code(a), code(b), 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(code(c), code(d), w, true);
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
 }
 
 }  // namespace

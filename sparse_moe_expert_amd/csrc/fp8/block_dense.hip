@@ -13,18 +13,31 @@ struct LinearArgs {
   int T, N, K;
 };
 
-// y[t, n .. n+3] from their sums; outputs at or past N are left alone
-__device__ __forceinline__ void write4(const LinearArgs& p, int t, int n, f32x4 v) {
+// COUNT (a multiple of 4) outputs of a token from n on, from their sums; those
+// at or past N are left alone
+template <int COUNT>
+__device__ __forceinline__ void write(const LinearArgs& p, int t, int n, float (&v)[COUNT]) {
+  if (n >= p.N) return;
   const size_t at = (size_t)t * p.N + n;
-  uint32_t o[4];
+  if (p.bias) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = to_bf16(p.bias ? v[i] + bf16_to_f32(p.bias[min(n + i, p.N - 1)]) : v[i]);
-  if (p.N % 4 == 0) {
-    *reinterpret_cast<uint2*>(p.y + at) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+    for (int i = 0; i < COUNT; ++i) v[i] += bf16_to_f32(p.bias[min(n + i, p.N - 1)]);
+  }
+  uint32_t o[COUNT / 2];
+#pragma unroll
+  for (int i = 0; i < COUNT / 2; ++i) o[i] = to_bf16(v[2 * i]) | to_bf16(v[2 * i + 1]) << 16;
+  if (COUNT % 8 == 0 && p.N % 8 == 0 && n + COUNT <= p.N) {
+#pragma unroll
+    for (int i = 0; i < COUNT / 8; ++i)
+      *reinterpret_cast<uint4*>(p.y + at + 8 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  } else if (p.N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < COUNT / 4; ++i)
+      if (n + 4 * i < p.N) *reinterpret_cast<uint2*>(p.y + at + 4 * i) = make_uint2(o[2 * i], o[2 * i + 1]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < p.N) p.y[at + i] = (uint16_t)o[i];
+    for (int i = 0; i < COUNT; ++i)
+      if (n + i < p.N) p.y[at + i] = (uint16_t)(o[i / 2] >> (i % 2 * 16));
   }
 }
 
@@ -36,7 +49,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs
   using T = Tile<TT, false>;
   MOE_TILE_STAGES(T)
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wr = wave / T::WT, wt = wave % T::WT;
+  const int wr = wave % T::WR, wt = wave / T::WR;
   const int tiles = row_tiles * token_tiles, per = (tiles + kXcds - 1) / kXcds;
   const int part = (int)blockIdx.x / (per * kXcds), at = (int)blockIdx.x % (per * kXcds);
   const int tile = at % kXcds * per + at / kXcds;
@@ -51,29 +64,32 @@ __global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs
   const uint8_t* const w = p.w.q + (size_t)n0 * p.K;
   tl.weights(w, w, rows, p.K, wave, lane);
   tl.rx = make_rsrc(p.x + (size_t)t0 * p.K, (uint32_t)toks * (uint32_t)p.K);
-  tl.tokens(wave, lane, [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)p.K; });
+  tl.tokens(wave, lane, [&](int r) { return r < toks ? (uint32_t)r * (uint32_t)p.K : kOutside; });
   const float* const sw = p.w.s + (size_t)(n0 / kBlock) * kb;
-  tl.scales(p.sx + (size_t)t0 * kb, (uint32_t)toks * (uint32_t)kb * 4u, sw, rows > kBlock ? sw + kb : sw, kb, wave, lane,
-            [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)kb * 4u; });
-  const int live = (toks - wt * T::JT * 16 + 15) / 16;
-  tl.template run<true>(stage_at, wave, wr, wt, lane, first, steps, p.K, live);
-
+  tl.token_scales(wave, lane, [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)kb * 4u; });
+  tl.scales(p.sx + (size_t)t0 * kb, (uint32_t)toks * (uint32_t)kb * 4u, sw, rows > kBlock ? sw + kb : sw, kb, wave);
+  tl.template run<true, true>(stage_at, wave, wr, wt, lane, first, steps, 1, p.K, [](int) {}, [&](int) MOE_INLINE {
 #pragma unroll
-  for (int j = 0; j < T::JT; ++j) {
-    const int r = (wt * T::JT + j) * 16 + (lane & 15);
-    if (r >= toks) continue;
+    for (int j = 0; j < T::JT; ++j) {
+      const int r = (wt * T::JT + j) * 16 + (lane & 15);
+      if (r >= toks) continue;
 #pragma unroll
-    for (int m = 0; m < T::MT; ++m) {
-      const int n = n0 + T::row_of(wr, m) + (lane >> 4) * 4;
-      if (n >= p.N) continue;
-      if (splits > 1) {
-        const size_t np = (size_t)row_tiles * kTileRows;
-        *reinterpret_cast<f32x4*>(sums + ((size_t)part * p.T + t0 + r) * np + n) = tl.acc[m][j];
-      } else {
-        write4(p, t0 + r, n, tl.acc[m][j]);
+      for (int m = 0; m < T::MT; m += T::Q) {
+        const int n = n0 + T::group_of(wr, m) + (lane >> 4) * (4 * T::Q);
+        if (splits > 1) {
+          const size_t np = (size_t)row_tiles * kTileRows;
+          float* const to = sums + ((size_t)part * p.T + t0 + r) * np + n;
+#pragma unroll
+          for (int q = 0; q < T::Q; ++q) *reinterpret_cast<f32x4*>(to + 4 * q) = tl.acc[m + q][j];
+        } else {
+          float v[4 * T::Q];
+#pragma unroll
+          for (int i = 0; i < 4 * T::Q; ++i) v[i] = tl.acc[m + i / 4][j][i % 4];
+          write(p, t0 + r, n, v);
+        }
       }
     }
-  }
+  }, [](int) { return true; });
 }
 
 // The parts' sums, in order, to outputs: a thread to four of a token
@@ -82,13 +98,13 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs p, int np, 
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   const int t = (int)(i / (size_t)quads), n = (int)(i - (size_t)t * quads) * 4;
   if (t >= p.T) return;
-  f32x4 v{};
+  float v[4] = {};
   for (int s = 0; s < splits; ++s) {
     const f32x4 a = *reinterpret_cast<const f32x4*>(sums + ((size_t)s * p.T + t) * (size_t)np + n);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] += a[k];
   }
-  write4(p, t, n, v);
+  write(p, t, n, v);
 }
 
 struct Plan {

@@ -27,46 +27,86 @@ struct FfnArgs {
   // by bucket position
   uint8_t* hq;             // [R, I]
   float* hs;               // [R, blocks of I]
-  float* o;                // [R, H]
-  int4* items;             // {expert, first position, routes, 0}; null: each chosen expert is one item
+  uint16_t* o;             // [R, H] fp16, over
+  float* os;               // [R, blocks of H] powers of two
+  int4* items;             // {expert, first position, routes, 0}; null: a chosen expert is one item
   int* n_items;
 };
 
-// An expert's routes in pieces of up to `tt`, experts in order
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(FfnArgs p, int tt) {
-  __shared__ int s_sum[kPlanThreads / kWave];
+// An item for each piece of an expert's routes, experts in order.  Pieces hold up
+// to `size` routes, between half a tile and a whole one, chosen so that the
+// workgroups' longest run of gate/up tiles takes the least loads: `size` token
+// rows and 256 weight rows a step.  (T = 2000 4096x2048 of 16 experts: gate/up
+// 150 us with whole tiles,  so.)
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(FfnArgs p, int tt, int row_tiles, int groups) {
+  constexpr int kSizes = 9;
+  __shared__ int s_sum[kPlanThreads / kWave][kSizes];
   const int e = threadIdx.x, lane = e & (kWave - 1), wave = e >> 6;
   const int count = e < p.E ? p.count[e] : 0, first = e < p.E ? p.offset[e] : 0;
-  const int pieces = (count + tt - 1) / tt;
+  auto size_of = [&](int c) { return min(tt, tt / 2 + c * 16); };      // whole token tiles, so that no piece is empty
+  for (int c = 0; c < kSizes; ++c) {
+    const int size = size_of(c);
+    int sum = (count + size - 1) / size;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
+    if (lane == 0) s_sum[wave][c] = sum;
+  }
+  __syncthreads();
+  int size = tt;
+  long long best = 0;
+  for (int c = kSizes - 1; c >= 0; --c) {
+    int items = 0;
+    for (int w = 0; w < kPlanThreads / kWave; ++w) items += s_sum[w][c];
+    const int rows = size_of(c);
+    const long long cost = (((long long)items * row_tiles + groups - 1) / groups) * (kTileRows + rows);
+    if (c == kSizes - 1 || cost < best) best = cost, size = rows;
+  }
+  const int pieces = (count + size - 1) / size;
   int sum = pieces;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
     const int v = __shfl_up(sum, d, kWave);
     if (lane >= d) sum += v;
   }
-  if (lane == kWave - 1) s_sum[wave] = sum;
+  __syncthreads();
+  if (lane == kWave - 1) s_sum[wave][0] = sum;
   __syncthreads();
   int at = sum - pieces;
-  for (int w = 0; w < wave; ++w) at += s_sum[w];
-  for (int i = 0; i < pieces; ++i) p.items[at + i] = make_int4(e, first + i * tt, min(tt, count - i * tt), 0);
+  for (int w = 0; w < wave; ++w) at += s_sum[w][0];
+  // even pieces, of whole token tiles
+  const int even = pieces > 0 ? ((count + pieces - 1) / pieces + 15) & ~15 : 0;
+  for (int i = 0; i < pieces; ++i) {
+    const int rest = count - i * even;
+    p.items[at + i] = make_int4(e, first + i * even, min(even, rest), 0);
+  }
   if (e == kPlanThreads - 1) *p.n_items = at + pieces;
 }
 
-// The workgroup's item and row tile: the items go round the XCDs, an item's row
-// tiles stay on one, whose L2 then holds its tokens.  False: none.
-__device__ __forceinline__ bool item_of(const FfnArgs& p, int row_tiles, int4& item, int& tile) {
-  const int i = (int)blockIdx.x / kXcds / row_tiles * kXcds + (int)blockIdx.x % kXcds;
-  tile = (int)blockIdx.x / kXcds % row_tiles;
+// Up to TT routes of an expert, from a bucket position on
+struct Item {
+  int expert, first, toks;
+};
+__device__ __forceinline__ Item item_at(const FfnArgs& p, int i) {
   if (p.items) {
-    if (i >= *p.n_items) return false;
-    item = p.items[i];
-  } else {
-    if (i >= *p.n_active) return false;
-    item.x = p.active[i];
-    item.y = p.offset[item.x];
-    item.z = p.count[item.x];
+    const int4 v = p.items[i];
+    return {v.x, v.y, v.z};
   }
-  return true;
+  const int e = p.active[i];
+  return {e, p.offset[e], p.count[e]};
+}
+
+// A workgroup's tiles: a run of those of all items, an item's row tiles one
+// after another, so that its loads' addresses seldom change, and those of an XCD
+// next to each other: workgroups that read the same tokens, and pieces of an
+// expert's routes that read the same weights, share an L2.
+struct Run {
+  int first, tiles;
+};
+__device__ __forceinline__ Run run_of(const FfnArgs& p, int row_tiles) {
+  const long long all = (long long)(p.items ? *p.n_items : *p.n_active) * row_tiles;
+  const int groups = (int)gridDim.x / kXcds, at = (int)blockIdx.x % kXcds * groups + (int)blockIdx.x / kXcds;
+  const int first = (int)(all * at / (int)gridDim.x);
+  return {first, (int)(all * (at + 1) / (int)gridDim.x) - first};
 }
 
 // h of 128 rows of an item's routes, in 8 bits: the rows are one block, whose
@@ -76,60 +116,82 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
   using T = Tile<TT, true>;
   MOE_TILE_STAGES(T)
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wr = wave / T::WT, wt = wave % T::WT;
-  int4 item;
-  int tile;
-  if (!item_of(p, row_tiles, item, tile)) return;
-  const int e = item.x, first = item.y, toks = item.z;
-  const int n0 = tile * kBlock, rows = min(kBlock, p.I - n0), kb = blocks_of(p.H), ib = blocks_of(p.I);
+  const int wr = wave % T::WR, wt = wave / T::WR;
+  __shared__ uint32_t s_max[T::WR * TT];
+  const Run run = run_of(p, row_tiles);
+  if (run.tiles == 0) return;
+  const int kb = blocks_of(p.H), ib = blocks_of(p.I);
   T tl;
-  const size_t at = ((size_t)e * p.I + n0) * (size_t)p.H, at_s = ((size_t)e * ib + tile) * (size_t)kb;
-  tl.weights(p.gate.q + at, p.up.q + at, rows, p.H, wave, lane);
-  auto token = [&](int r) { return (uint32_t)(p.src[first + min(r, toks - 1)] / p.k); };
   tl.rx = make_rsrc(p.x, (uint32_t)p.T * (uint32_t)p.H);
-  tl.tokens(wave, lane, [&](int r) { return token(r) * (uint32_t)p.H; });
-  tl.scales(p.sx, (uint32_t)p.T * (uint32_t)kb * 4u, p.gate.s + at_s, p.up.s + at_s, kb, wave, lane,
-            [&](int r) { return token(r) * (uint32_t)kb * 4u; });
-  const int live = (toks - wt * T::JT * 16 + 15) / 16;
-  tl.template run<false>(stage_at, wave, wr, wt, lane, 0, kb, p.H, live);
-
-  constexpr int HT = T::MT / 2;
-  const int g = lane >> 4;
-  uint32_t* const s_max = reinterpret_cast<uint32_t*>(s_0);            // [WR][TT]
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < T::JT; ++j) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int m = 0; m < HT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float h = silu(tl.acc[m][j][i]) * tl.acc[m + HT][j][i];
-        tl.acc[m][j][i] = h;
-        top = max(top, finite_bits(h));
-      }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
-    if (g == 0) s_max[wr * TT + (wt * T::JT + j) * 16 + lane] = top;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < T::JT; ++j) {
-    const int r = (wt * T::JT + j) * 16 + (lane & 15);
-    if (r >= toks) continue;
-    uint32_t top = 0;
-#pragma unroll
-    for (int w = 0; w < T::WR; ++w) top = max(top, s_max[w * TT + r]);
-    const float s = block_scale(__uint_as_float(top)), inv = 1.0f / s;
-    const size_t row = (size_t)(first + r);
-    if (wr == 0 && g == 0) p.hs[row * ib + tile] = s;
-#pragma unroll
-    for (int m = 0; m < HT; ++m) {
-      const int n = n0 + T::row_of(wr, m) + g * 4;
-      const f32x4 v = tl.acc[m][j];
-      if (n < p.I) *reinterpret_cast<uint32_t*>(p.hq + row * p.I + n) = encode4(v[0], v[1], v[2], v[3], inv);
+  int loaded = -1;                                           // the item that the loads' addresses are of
+  Item item_in;
+  auto begin = [&](int i) MOE_INLINE {
+    const int at = run.first + i, number = at / row_tiles, tile = at - number * row_tiles;
+    if (number != loaded) {
+      loaded = number;
+      item_in = item_at(p, number);
+      auto token = [&](int r) MOE_INLINE { return (uint32_t)(p.src[item_in.first + min(r, item_in.toks - 1)] / p.k); };
+      tl.tokens(wave, lane, [&](int r) { return r < item_in.toks ? token(r) * (uint32_t)p.H : kOutside; });
+      tl.token_scales(wave, lane, [&](int r) { return token(r) * (uint32_t)kb * 4u; });
     }
-  }
+    const int n0 = tile * kBlock;
+    const size_t row = (size_t)item_in.expert * p.I + n0, scale = ((size_t)item_in.expert * ib + tile) * (size_t)kb;
+    tl.weights(p.gate.q + row * p.H, p.up.q + row * p.H, min(kBlock, p.I - n0), p.H, wave, lane);
+    tl.scales(p.sx, (uint32_t)p.T * (uint32_t)kb * 4u, p.gate.s + scale, p.up.s + scale, kb, wave);
+  };
+  begin(0);
+  int done = -1;                                             // the item whose sums are made
+  Item item;
+  auto live = [&](int i) MOE_INLINE {
+    const int number = (run.first + i) / row_tiles;
+    if (number != done) item = item_at(p, done = number);
+    return item.toks > wt * T::JT * 16;
+  };
+  auto end = [&](int i) MOE_INLINE {
+    const int tile = (run.first + i) % row_tiles, n0 = tile * kBlock, first = item.first, toks = item.toks;
+    constexpr int HT = T::HT, Q = T::Q;
+    int l = lane;
+    asm volatile("" : "+v"(l));                              // (addresses are made here, and not kept through the loop)
+    const int g = l >> 4;
+#pragma unroll
+    for (int j = 0; j < T::JT; ++j) {
+      float h[4 * HT];
+#pragma unroll
+      for (int i = 0; i < 4 * HT; ++i) {
+        const float a = tl.acc[i / 4][j][i % 4];
+        h[i] = a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)) * tl.acc[i / 4 + HT][j][i % 4];
+        tl.acc[i / 4][j][i % 4] = h[i];
+      }
+      uint32_t top = largest(h);
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
+      if (g == 0) s_max[wr * TT + (wt * T::JT + j) * 16 + l] = top;
+    }
+    wait_lds();
+    barrier();
+#pragma unroll
+    for (int j = 0; j < T::JT; ++j) {
+      const int r = (wt * T::JT + j) * 16 + (l & 15);
+      if (r >= toks) continue;
+      uint32_t top = 0;
+#pragma unroll
+      for (int w = 0; w < T::WR; ++w) top = max(top, s_max[w * TT + r]);
+      const float s = block_scale(__uint_as_float(top)), inv = 1.0f / s;
+      const size_t row = (size_t)(first + r);
+      if (wr == 0 && g == 0) p.hs[row * ib + tile] = s;
+      const int n = n0 + T::group_of(wr, 0) + g * (4 * Q);
+      uint32_t c[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) c[q] = encode4(tl.acc[q][j][0], tl.acc[q][j][1], tl.acc[q][j][2], tl.acc[q][j][3], inv);
+      static_assert(HT == Q, "a lane's values of a token are neighbours");
+      uint8_t* const to = p.hq + row * p.I + n;              // (I is a multiple of 16)
+      if (n >= p.I) continue;
+      if constexpr (Q == 4) *reinterpret_cast<uint4*>(to) = make_uint4(c[0], c[1], c[2], c[3]);
+      else if constexpr (Q == 2) *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
+      else *reinterpret_cast<uint32_t*>(to) = c[0];
+    }
+  };
+  tl.template run<false, false>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.H, begin, end, live);
 }
 
 // o of 256 rows of an item's routes
@@ -138,66 +200,149 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
   using T = Tile<TT, false>;
   MOE_TILE_STAGES(T)
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wr = wave / T::WT, wt = wave % T::WT;
-  int4 item;
-  int tile;
-  if (!item_of(p, row_tiles, item, tile)) return;
-  const int e = item.x, first = item.y, toks = item.z;
-  const int n0 = tile * kTileRows, rows = min(kTileRows, p.H - n0), kb = blocks_of(p.I);
+  const int wr = wave % T::WR, wt = wave / T::WR;
+  __shared__ uint32_t s_max[T::WR * TT];
+  const Run run = run_of(p, row_tiles);
+  if (run.tiles == 0) return;
+  const int kb = blocks_of(p.I), hb = blocks_of(p.H);
   T tl;
-  const uint8_t* const w = p.down.q + ((size_t)e * p.H + n0) * (size_t)p.I;
-  tl.weights(w, w, rows, p.I, wave, lane);
-  tl.rx = make_rsrc(p.hq + (size_t)first * p.I, (uint32_t)toks * (uint32_t)p.I);
-  tl.tokens(wave, lane, [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)p.I; });
-  const float* const sw = p.down.s + ((size_t)e * blocks_of(p.H) + n0 / kBlock) * (size_t)kb;
-  tl.scales(p.hs + (size_t)first * kb, (uint32_t)toks * (uint32_t)kb * 4u, sw, rows > kBlock ? sw + kb : sw, kb, wave, lane,
-            [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)kb * 4u; });
-  const int live = (toks - wt * T::JT * 16 + 15) / 16;
-  tl.template run<false>(stage_at, wave, wr, wt, lane, 0, kb, p.I, live);
-#pragma unroll
-  for (int j = 0; j < T::JT; ++j) {
-    const int r = (wt * T::JT + j) * 16 + (lane & 15);
-    if (r >= toks) continue;
-#pragma unroll
-    for (int m = 0; m < T::MT; ++m) {
-      const int n = n0 + T::row_of(wr, m) + (lane >> 4) * 4;
-      if (n < p.H) *reinterpret_cast<f32x4*>(p.o + (size_t)(first + r) * p.H + n) = tl.acc[m][j];
+  int loaded = -1;                                           // the item that the loads' addresses are of
+  Item item_in;
+  auto begin = [&](int i) MOE_INLINE {
+    const int at = run.first + i, number = at / row_tiles, n0 = (at - number * row_tiles) * kTileRows;
+    if (number != loaded) {
+      loaded = number;
+      item_in = item_at(p, number);
+      tl.rx = make_rsrc(p.hq + (size_t)item_in.first * p.I, (uint32_t)item_in.toks * (uint32_t)p.I);
+      tl.tokens(wave, lane, [&](int r) { return r < item_in.toks ? (uint32_t)r * (uint32_t)p.I : kOutside; });
+      tl.token_scales(wave, lane, [&](int r) { return (uint32_t)min(r, item_in.toks - 1) * (uint32_t)kb * 4u; });
     }
-  }
+    const int rows = min(kTileRows, p.H - n0);
+    const uint8_t* const w = p.down.q + ((size_t)item_in.expert * p.H + n0) * (size_t)p.I;
+    tl.weights(w, w, rows, p.I, wave, lane);
+    const float* const sw = p.down.s + ((size_t)item_in.expert * hb + n0 / kBlock) * (size_t)kb;
+    tl.scales(p.hs + (size_t)item_in.first * kb, (uint32_t)item_in.toks * (uint32_t)kb * 4u, sw,
+              rows > kBlock ? sw + kb : sw, kb, wave);
+  };
+  begin(0);
+  int done = -1;                                             // the item whose sums are made
+  Item item;
+  auto live = [&](int i) MOE_INLINE {
+    const int number = (run.first + i) / row_tiles;
+    if (number != done) item = item_at(p, done = number);
+    return item.toks > wt * T::JT * 16;
+  };
+  auto end = [&](int i) MOE_INLINE {
+    const int n0 = (run.first + i) % row_tiles * kTileRows, first = item.first, toks = item.toks;
+    // Each route's 128 outputs over the power of two that puts the largest
+    // between 2^14 and 2^15: fp16 then keeps 11 bits of every output down to 2^-28
+    // of it.  o in fp32 would be twice the bytes (T = 4096 2048x512 of 512 experts,
+    // 335 MB written and read again:  us in place of ).
+    int l = lane;
+    asm volatile("" : "+v"(l));                              // (addresses are made here, and not kept through the loop)
+    const int g = l >> 4;
+#pragma unroll
+    for (int j = 0; j < T::JT; ++j) {
+      float v[4 * T::MT];
+#pragma unroll
+      for (int i = 0; i < 4 * T::MT; ++i) v[i] = tl.acc[i / 4][j][i % 4];
+      uint32_t top = largest(v);
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
+      if (g == 0) s_max[wr * TT + (wt * T::JT + j) * 16 + l] = top;
+    }
+    wait_lds();
+    barrier();
+    constexpr int kShare = T::WR / 2;                        // waves of a block of rows
+    const int block = n0 / kBlock + wr / kShare;
+#pragma unroll
+    for (int j = 0; j < T::JT; ++j) {
+      const int r = (wt * T::JT + j) * 16 + (l & 15);
+      if (r >= toks || block >= hb) continue;
+      uint32_t top = 0;
+#pragma unroll
+      for (int w = 0; w < kShare; ++w) top = max(top, s_max[(wr / kShare * kShare + w) * TT + r]);
+      const uint32_t ex = max(top >> 23, 15u);
+      const float inv = __uint_as_float((268u - ex) << 23);
+      const size_t row = (size_t)(first + r);
+      if (wr % kShare == 0 && g == 0) p.os[row * hb + block] = __uint_as_float((ex - 14u) << 23);
+#pragma unroll
+      for (int m = 0; m < T::MT; m += T::Q) {
+        const int n = n0 + T::group_of(wr, m) + g * (4 * T::Q);
+        if (n >= p.H) continue;                              // (H is a multiple of 16)
+        uint32_t c[2 * T::Q];
+#pragma unroll
+        for (int q = 0; q < T::Q; ++q) {
+          const f32x4 v = tl.acc[m + q][j];
+          c[2 * q] = f32_to_f16_bits(v[0] * inv) | f32_to_f16_bits(v[1] * inv) << 16;
+          c[2 * q + 1] = f32_to_f16_bits(v[2] * inv) | f32_to_f16_bits(v[3] * inv) << 16;
+        }
+        uint4* const to = reinterpret_cast<uint4*>(p.o + row * p.H + n);
+#pragma unroll
+        for (int q = 0; q < T::Q / 2; ++q) to[q] = make_uint4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]);
+      }
+    }
+  };
+  tl.template run<false, false>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.I, begin, end, live);
 }
 
-// A thread to four outputs of a token
+// A thread to eight outputs of a token
 __global__ __launch_bounds__(kFfnThreads) void combine_kernel(FfnArgs p) {
   const size_t i = (size_t)blockIdx.x * kFfnThreads + threadIdx.x;
-  const int quads = p.H / 4;
-  const int t = (int)(i / (size_t)quads), n = (int)(i - (size_t)t * quads) * 4;
+  const int pieces = p.H / 8, hb = blocks_of(p.H);
+  const int t = (int)(i / (size_t)pieces), n = (int)(i - (size_t)t * pieces) * 8;
   if (t >= p.T) return;
-  float v[4] = {};
-  for (int j = 0; j < p.k; ++j) {
-    const size_t route = (size_t)t * p.k + j;
-    const f32x4 o = *reinterpret_cast<const f32x4*>(p.o + (size_t)p.pos[route] * p.H + n);
-    const float w = p.topk_w[route];
+  float v[8] = {};
+  const int32_t* const pos = p.pos + (size_t)t * p.k;
+  const float* const weight = p.topk_w + (size_t)t * p.k;
+  constexpr int kAhead = 4;                                  // routes whose loads are in flight together
+  for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+    uint4 o[kAhead];
+    float w[kAhead];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = fmaf(w, o[c], v[c]);
+    for (int a = 0; a < kAhead; ++a) {
+      const int j = min(j0 + a, p.k - 1);
+      const size_t row = (size_t)pos[j];
+      o[a] = *reinterpret_cast<const uint4*>(p.o + row * p.H + n);
+      w[a] = weight[j] * p.os[row * hb + n / kBlock];
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (j0 + a >= p.k) break;
+      const uint32_t u[4] = {o[a].x, o[a].y, o[a].z, o[a].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        v[2 * c] = fmaf(w[a], f16_bits_to_f32(u[c] & 0xFFFFu), v[2 * c]);
+        v[2 * c + 1] = fmaf(w[a], f16_bits_to_f32(u[c] >> 16), v[2 * c + 1]);
+      }
+    }
   }
-  *reinterpret_cast<uint2*>(p.y + (size_t)t * p.H + n) =
-      make_uint2(to_bf16(v[0]) | to_bf16(v[1]) << 16, to_bf16(v[2]) | to_bf16(v[3]) << 16);
+  *reinterpret_cast<uint4*>(p.y + (size_t)t * p.H + n) =
+      make_uint4(to_bf16(v[0]) | to_bf16(v[1]) << 16, to_bf16(v[2]) | to_bf16(v[3]) << 16,
+                 to_bf16(v[4]) | to_bf16(v[5]) << 16, to_bf16(v[6]) | to_bf16(v[7]) << 16);
 }
 
 // Tokens of a tile; up to that many the experts themselves are the items
-int tile_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
-// Most items that R routes can make
+int tile_tokens(int T, int E, int k) {
+  if (T <= 128) return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  return (long long)T * k >= 128ll * E ? 256 : 128;
+}
+// Most items that R routes can make, in pieces of half a tile or more
 int most_items(size_t R, int E, int tt) {
   const size_t experts = R < (size_t)E ? R : (size_t)E;
-  return (int)(experts + R / (size_t)tt);
+  return (int)(experts + 2 * R / (size_t)tt);
 }
 
 template <int TT>
 void launch_products(const FfnArgs& p, int items, hipStream_t s) {
-  const unsigned groups = (unsigned)(items + kXcds - 1) / kXcds * kXcds;
   const int up = blocks_of(p.I), down = (p.H + kTileRows - 1) / kTileRows;
-  gate_up_kernel<TT><<<groups * up, kTileThreads, 0, s>>>(p, up);
-  down_kernel<TT><<<groups * down, kTileThreads, 0, s>>>(p, down);
+  const int most = (device_cu_count() + kXcds - 1) / kXcds * kXcds;    // a workgroup takes a compute unit's LDS
+  auto grid = [&](int row_tiles) {
+    const long long tiles = ((long long)items * row_tiles + kXcds - 1) / kXcds * kXcds;
+    return (unsigned)(tiles < most ? tiles : most);
+  };
+  gate_up_kernel<TT><<<grid(up), kTileThreads, 0, s>>>(p, up);
+  down_kernel<TT><<<grid(down), kTileThreads, 0, s>>>(p, down);
 }
 
 inline bool ffn_dims_ok(int T, int H, int I, int E, int k) {
@@ -215,9 +360,8 @@ extern "C" size_t moe_block_expert_ffn_workspace_size(int T, int H, int I, int E
   using namespace moe;
   if (T <= 0 || !ffn_dims_ok(T, H, I, E, k) || !ffn_dims_fit(T, H, I, E, k)) return 0;
   const size_t R = (size_t)T * (size_t)k;
-  const int tt = tile_tokens(T);
-  return align256(R * I) + align256(R * blocks_of(I) * 4) + align256(R * H * 4) +
-         (T > tt ? align256((size_t)most_items(R, E, tt) * sizeof(int4)) + 256 : 0);
+  return align256(R * I) + align256(R * blocks_of(I) * 4) + align256(R * H * 2) + align256(R * blocks_of(H) * 4) +
+         (T > 128 ? align256((size_t)most_items(R, E, 128) * sizeof(int4)) + 256 : 0);
 }
 
 extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scale, const uint8_t* w_gate,
@@ -243,25 +387,27 @@ extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scal
   uint8_t* at = static_cast<uint8_t*>(workspace);
   auto take = [&](size_t n) { uint8_t* const b = at; at += align256(n); return b; };
   FfnArgs p{x, x_scale, {w_gate, s_gate}, {w_up, s_up}, {w_down, s_down}, topk_w, expert_count, expert_offset,
-            active_experts, n_active, route_src, route_pos, y, T, H, I, E, k, nullptr, nullptr, nullptr, nullptr, nullptr};
+            active_experts, n_active, route_src, route_pos, y, T, H, I, E, k, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   p.hq = take(R * I);
   p.hs = reinterpret_cast<float*>(take(R * blocks_of(I) * 4));
-  p.o = reinterpret_cast<float*>(take(R * H * 4));
+  p.o = reinterpret_cast<uint16_t*>(take(R * H * 2));
+  p.os = reinterpret_cast<float*>(take(R * blocks_of(H) * 4));
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int tt = tile_tokens(T);
+  const int tt = tile_tokens(T, E, k);
   int items = (int)(R < (size_t)E ? R : (size_t)E);
   if (T > tt) {
     items = most_items(R, E, tt);
     p.items = reinterpret_cast<int4*>(take((size_t)items * sizeof(int4)));
     p.n_items = reinterpret_cast<int*>(take(4));
-    plan_kernel<<<1, kPlanThreads, 0, s>>>(p, tt);
+    plan_kernel<<<1, kPlanThreads, 0, s>>>(p, tt, blocks_of(I), device_cu_count());
   }
   switch (tt) {
     case 16: launch_products<16>(p, items, s); break;
     case 32: launch_products<32>(p, items, s); break;
     case 64: launch_products<64>(p, items, s); break;
-    default: launch_products<128>(p, items, s);
+    case 128: launch_products<128>(p, items, s); break;
+    default: launch_products<256>(p, items, s);
   }
-  combine_kernel<<<(unsigned)(((size_t)T * (H / 4) + kFfnThreads - 1) / kFfnThreads), kFfnThreads, 0, s>>>(p);
+  combine_kernel<<<(unsigned)(((size_t)T * (H / 8) + kFfnThreads - 1) / kFfnThreads), kFfnThreads, 0, s>>>(p);
   return launch_status();
 }

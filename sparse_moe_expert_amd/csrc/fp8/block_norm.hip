@@ -44,10 +44,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // Eight values of a block that 16 lanes hold (those past the row: zero) to
 // codes at q and, from its first lane, the scale
 __device__ __forceinline__ void encode8(const float (&v)[8], bool here, uint8_t* q, float* scale) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, finite_bits(v[i]));
-  const float s = block_scale(__uint_as_float(max16(m)));
+  const float s = block_scale(__uint_as_float(max16(largest(v))));
   const float inv = 1.0f / s;
   if (!here) return;
   *reinterpret_cast<uint2*>(q) = make_uint2(encode4(v[0], v[1], v[2], v[3], inv), encode4(v[4], v[5], v[6], v[7], inv));

@@ -3,8 +3,10 @@
 //
 // Tokens, weights and scales go straight to LDS (buffer_load ... lds), a block
 // of 128 of the reduction a step, in a ring of NS stages.  A row's step is 128
-// bytes, chunk c of 16 at c ^ ((r >> 1) & 7): the reads of 16 lanes, one chunk of
-// 16 rows, hit all banks.  The waves stand WR x WT over the tile; a wave holds
+// bytes, its 16-byte chunks permuted so that the reads of 16 lanes, one chunk of
+// the 16 rows of a product, hit all banks.  The rows of Q products are
+// interleaved by fours, so that a lane's sums of them are 4Q neighbouring outputs
+// of a token.  The waves stand WR x WT over the tile; a wave holds
 // the step's fragments of its JT token tiles and goes through its MT row tiles,
 // each product followed, three products later, by the four multiply-adds that
 // scale it onto the sums: the matrix pipe and the vector pipe then work side by
@@ -14,6 +16,9 @@
 #include "block_common.h"
 
 #include <type_traits>
+
+// of a lambda: its captures stay in registers
+#define MOE_INLINE __attribute__((always_inline))
 
 namespace moe {
 namespace {
@@ -52,29 +57,45 @@ __device__ __forceinline__ void for_each(F&& f) {
   }
 }
 
+// A stage: the weights of a step with all its scales, and the tokens
+struct Stage {
+  uint8_t* w;
+  uint8_t* x;
+};
+
 template <int TT, bool PAIR>
 struct Tile {
   static constexpr int WR = TT == 256 ? 2 : TT == 16 ? 8 : 4, WT = 8 / WR;
   static constexpr int MT = kTileRows / WR / 16, JT = TT / WT / 16;        // row tiles, token tiles a wave
+  static constexpr int HT = PAIR ? MT / 2 : MT, Q = HT < 4 ? HT : 4;       // row tiles of one matrix, interleaved ones
   static constexpr int kWeightBytes = kTileRows * kBlock, kTokenBytes = TT * kBlock;
   static constexpr int kScaleGroups = (TT + 63) / 64 + 2;                  // 64 of the tokens' scales each, and the weights'
-  static constexpr int kStageBytes = kWeightBytes + kTokenBytes + kScaleGroups * 256;
-  static constexpr int kFit = 160 * 1024 / kStageBytes, NS = kFit < 4 ? kFit : 4, kLead = NS - 1;
+  static constexpr int kScaledBytes = kWeightBytes + kScaleGroups * 256;   // the weights and all scales
+  static constexpr int kFit = 160 * 1024 / (kScaledBytes + kTokenBytes), NS = kFit < 4 ? kFit : 4, kLead = NS - 1;
   static constexpr int XL = TT < 64 ? 1 : TT / 64;                         // a wave's token loads a step
-  static constexpr int kLoads = 4 + XL + 1;
+  static constexpr int kLoads = 4 + 1 + XL;
   static_assert(NS >= 2 && (kLead - 1) * kLoads < 64, "two stages or more");
 
   __amdgpu_buffer_rsrc_t rw, rx, rs;         // the wave's weight rows, the tokens, the wave's scales
   uint32_t w_off[4], x_off[XL], s_off;
-  uint32_t token_at, scale_at;               // where a wave's first token piece and its scales go in a stage
+  uint32_t token_at, scale_at;               // where a wave's first token piece and its scales go
   f32x4 acc[MT][JT];
 
-  // Row of the tile where a wave's row tile m starts (of a pair: in the 128 of
-  // either matrix, the second's from 128 on)
-  static __device__ __forceinline__ int row_of(int wr, int m) {
-    if constexpr (PAIR) return (m < MT / 2 ? 0 : 128) + wr * (MT / 2 * 16) + m % (MT / 2) * 16;
-    return (wr * MT + m) * 16;
+  // Row of the tile (of a pair: in the 128 of either matrix, the second's from
+  // 128 on) where the interleaved tiles that row tile m is one of start
+  static __device__ __forceinline__ int group_of(int wr, int m) {
+    if constexpr (PAIR) return (m < HT ? 0 : 128) + (wr * HT + m % HT / Q * Q) * 16;
+    return (wr * MT + m / Q * Q) * 16;
   }
+  // Row of the product's row l16 of row tile m; D's register i, lane group g: row
+  // group_of + g * 4Q + m % Q * 4 + i
+  static __device__ __forceinline__ int row_of(int wr, int m, int l16) {
+    return group_of(wr, m) + (l16 >> 2) * (4 * Q) + m % Q * 4 + (l16 & 3);
+  }
+  // What a row's chunks are permuted by (XOR): different for the 16 rows of a
+  // product, but for pairs of neighbours, which lie in different halves of the banks
+  static __device__ __forceinline__ int mix(int r) { return ((r >> 1) & 1) | (r / (4 * Q) & 3) << 1; }
+  static __device__ __forceinline__ int token_mix(int r) { return (r >> 1) & 7; }
 
   // The wave's loads.  Weight piece i: 8 rows from (wave * 4 + i) * 8 on.
   // `first`, `second`: a pair's matrices from the tile's first row on, of which
@@ -84,7 +105,7 @@ struct Tile {
     rw = make_rsrc(other ? second : first, (uint32_t)rows * (uint32_t)K);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = (wave * 4 + i) * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+      const int r = (wave * 4 + i) * 8 + (lane >> 3), c = (lane & 7) ^ mix(r);
       const int in = PAIR ? r & 127 : r;
       w_off[i] = (uint32_t)min(in, rows - 1) * (uint32_t)K + (uint32_t)c * 16u;
     }
@@ -95,156 +116,184 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
       const int piece = TT < 64 ? wave % (TT / 8) : i * 8 + wave;          // 8 rows each
-      const int r = piece * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+      const int r = piece * 8 + (lane >> 3), c = (lane & 7) ^ token_mix(r);
       x_off[i] = f(r) + (uint32_t)c * 16u;
     }
-    token_at = kWeightBytes + (TT < 64 ? wave % (TT / 8) : wave) * 1024u;
+    token_at = (TT < 64 ? wave % (TT / 8) : wave) * 1024u;
   }
 
   // A wave's 64 scales: of tokens, f(r) the offset of row r's in sx; else one of
   // the weights', of the first matrix or rows, or of the second
   template <class F>
-  __device__ __forceinline__ void scales(const float* sx, uint32_t bytes, const float* first, const float* second, int kb,
-                                         int wave, int lane, F&& f) {
+  __device__ __forceinline__ void token_scales(int wave, int lane, F&& f) {
     const int group = wave % kScaleGroups;
-    scale_at = kWeightBytes + kTokenBytes + group * 256u;
-    if (group < kScaleGroups - 2) {
-      rs = make_rsrc(sx, bytes);
-      s_off = f(min(group * 64 + lane, TT - 1));
-    } else {
-      rs = make_rsrc(group == kScaleGroups - 2 ? first : second, (uint32_t)kb * 4u);
-      s_off = 0;
-    }
+    scale_at = kWeightBytes + group * 256u;
+    s_off = group < kScaleGroups - 2 ? f(min(group * 64 + lane, TT - 1)) : 0;
+  }
+  __device__ __forceinline__ void scales(const float* sx, uint32_t bytes, const float* first, const float* second, int kb, int wave) {
+    const int group = wave % kScaleGroups;
+    if (group < kScaleGroups - 2) rs = make_rsrc(sx, bytes);
+    else rs = make_rsrc(group == kScaleGroups - 2 ? first : second, (uint32_t)kb * 4u);
   }
 
-  __device__ __forceinline__ void issue(uint8_t* stage, int wave, uint32_t step) {
+  // Load i (a constant) of a step: its weights, scales, then tokens
+  __device__ __forceinline__ void issue_scaled(int i, uint8_t* w, int wave, uint32_t step) {
+    if (i < 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, w + (wave * 4 + i) * 1024, 16, w_off[i] + step * kBlock, 0, 0, 0);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, w + scale_at, 4, s_off + step * 4u, 0, 0, 0);
+  }
+  __device__ __forceinline__ void issue_token(int i, uint8_t* x, uint32_t step) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, x + token_at + i * 8192, 16, x_off[i] + step * kBlock, 0, 0, 0);
+  }
+  __device__ __forceinline__ void issue_weights(uint8_t* w, int wave, uint32_t step) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, stage + (wave * 4 + i) * 1024, 16, w_off[i] + step * kBlock, 0, 0, 0);
+    for (int i = 0; i < 5; ++i) issue_scaled(i, w, wave, step);
+    fence();
+  }
+  __device__ __forceinline__ void issue_tokens(uint8_t* x, uint32_t step) {
 #pragma unroll
-    for (int i = 0; i < XL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, stage + token_at + i * 8192, 16, x_off[i] + step * kBlock, 0, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, stage + scale_at, 4, s_off + step * 4u, 0, 0, 0);
+    for (int i = 0; i < XL; ++i) issue_token(i, x, step);
+    fence();
   }
 
   // What follows a row's last value in its last step is not its: zero, in the
   // pieces that this wave loaded (chunks from `from` on)
-  __device__ __forceinline__ void clear_tail(uint8_t* stage, int wave, int lane, int from) {
-    auto clear = [&](uint32_t at, int r) {
-      if (((lane & 7) ^ ((r >> 1) & 7)) >= from) *reinterpret_cast<uint4*>(stage + at + lane * 16) = make_uint4(0, 0, 0, 0);
+  __device__ __forceinline__ void clear_tail(const Stage& stage, int wave, int lane, int from) {
+    auto clear = [&](uint8_t* piece, int by) {
+      if (((lane & 7) ^ by) >= from) *reinterpret_cast<uint4*>(piece + lane * 16) = make_uint4(0, 0, 0, 0);
     };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) clear((wave * 4 + i) * 1024, (wave * 4 + i) * 8 + (lane >> 3));
+    for (int i = 0; i < 4; ++i) clear(stage.w + (wave * 4 + i) * 1024, mix((wave * 4 + i) * 8 + (lane >> 3)));
 #pragma unroll
-    for (int i = 0; i < XL; ++i) clear(token_at + i * 8192, (TT < 64 ? wave % (TT / 8) : i * 8 + wave) * 8 + (lane >> 3));
+    for (int i = 0; i < XL; ++i)
+      clear(stage.x + token_at + i * 8192, token_mix((TT < 64 ? wave % (TT / 8) : i * 8 + wave) * 8 + (lane >> 3)));
   }
 
-  static __device__ __forceinline__ i32x8 read(const uint8_t* rows, int r, int g) {
+  static __device__ __forceinline__ i32x8 read(const uint8_t* rows, int r, int x, int g) {
     const uint8_t* const row = rows + r * kBlock;
-    const int x = (r >> 1) & 7;
     return fragment(*reinterpret_cast<const i32x4*>(row + ((g ^ x) << 4)),
                     *reinterpret_cast<const i32x4*>(row + (((g + 4) ^ x) << 4)));
   }
 
-  // One step's products of the first JL token tiles
-  template <int JL>
-  __device__ __forceinline__ void products(const uint8_t* stage, int wr, int wt, int lane) {
+  // One step's products
+  __device__ __forceinline__ void products(const Stage& stage, int wr, int wt, int lane) {
     const int l16 = lane & 15, g = lane >> 4;
-    const float* const scales = reinterpret_cast<const float*>(stage + kWeightBytes + kTokenBytes);
+    const float* const scales = reinterpret_cast<const float*>(stage.w + kWeightBytes);
     const float* const sw = scales + (kScaleGroups - 2) * 64;
     const float s0 = PAIR || wr * MT < 8 ? sw[0] : sw[64], s1 = PAIR ? sw[64] : s0;
-    i32x8 b[JL], a[2];
-    float s[2][JL];
-    a[0] = read(stage, row_of(wr, 0) + l16, g);
+    i32x8 b[JT], a[2];
+    float s[2][JT];
+    const int by = (l16 >> 1 & 1) | (l16 >> 2) << 1;         // mix(row_of(...))
+    a[0] = read(stage.w, row_of(wr, 0, l16), by, g);
 #pragma unroll
-    for (int j = 0; j < JL; ++j) {
+    for (int j = 0; j < JT; ++j) {
       const int r = (wt * JT + j) * 16 + l16;
-      b[j] = read(stage + kWeightBytes, r, g);
+      b[j] = read(stage.x, r, token_mix(r), g);
       s[0][j] = scales[r];
     }
 #pragma unroll
-    for (int j = 0; j < JL; ++j) {
+    for (int j = 0; j < JT; ++j) {
       if constexpr (PAIR) s[1][j] = s[0][j] * s1;
       s[0][j] *= s0;
     }
-    constexpr int kDelay = 3, kAll = MT * JL;
+    constexpr int kDelay = 3, kAll = MT * JT;
     f32x4 d[kDelay + 1];
-    for_each<kAll + kDelay>([&](auto n_c) {
+    for_each<kAll + kDelay>([&](auto n_c) MOE_INLINE {
       constexpr int n = decltype(n_c)::value, q = n - kDelay;
       if constexpr (n < kAll) {
-        if constexpr (n % JL == 0 && n / JL + 1 < MT) a[(n / JL + 1) % 2] = read(stage, row_of(wr, n / JL + 1) + l16, g);
-        d[n % (kDelay + 1)] = block_product(a[n / JL % 2], b[n % JL]);
+        if constexpr (n % JT == 0 && n / JT + 1 < MT) a[(n / JT + 1) % 2] = read(stage.w, row_of(wr, n / JT + 1, l16), by, g);
+        d[n % (kDelay + 1)] = block_product(a[n / JT % 2], b[n % JT]);
       }
       if constexpr (q >= 0) {
-        const float scale = s[PAIR && q / JL >= MT / 2][q % JL];
+        const float scale = s[PAIR && q / JT >= HT][q % JT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[q / JL][q % JL][i] = fmaf(d[q % (kDelay + 1)][i], scale, acc[q / JL][q % JL][i]);
-        asm volatile("" : "+v"(acc[q / JL][q % JL]));         // here, and not where the sums are used next
+        for (int i = 0; i < 4; ++i) acc[q / JT][q % JT][i] = fmaf(d[q % (kDelay + 1)][i], scale, acc[q / JT][q % JT][i]);
+        asm volatile("" : "+v"(acc[q / JT][q % JT]));         // here, and not where the sums are used next
       }
       __builtin_amdgcn_sched_barrier(0);
     });
   }
-  // Of those below `live`, or of all
-  template <bool ALL>
-  __device__ __forceinline__ void step(const uint8_t* stage, int wr, int wt, int lane, int live) {
-    if constexpr (ALL) {
-      products<JT>(stage, wr, wt, lane);
-    } else {
-      for_each<JT>([&](auto j) {
-        constexpr int JL = decltype(j)::value + 1;
-        if (live == JL || (JL == JT && live > JT)) products<JL>(stage, wr, wt, lane);
-      });
-    }
-  }
 
-  // All steps first .. first + steps; stages: NS arrays, so that reads of one
-  // are seen not to alias the loads in flight to the others
-  template <bool ALL, class Stage>
-  __device__ __forceinline__ void run(Stage&& stage_at, int wave, int wr, int wt, int lane, int first, int steps, int K, int live) {
+  __device__ __forceinline__ void clear_sums() {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < JT; ++j) acc[m][j] = f32x4{};
-    // a step past the last is issued out of range: it reads nothing
-    auto at = [&](int s) { return s < steps ? (uint32_t)(first + s) : kOutside / kBlock; };
-    for_each<kLead>([&](auto s) {
-      issue(stage_at(s), wave, at(decltype(s)::value));
-      fence();
-    });
-    auto body = [&](auto stage_c, int s) {
-      constexpr int S = decltype(stage_c)::value;
-      uint8_t* const stage = stage_at(stage_c);
-      wait_loads<(kLead - 1) * kLoads>();                    // this wave's loads of step s have landed
-      const int rest = K - (first + s) * kBlock;
-      if (rest < kBlock) clear_tail(stage, wave, lane, rest / 16);
-      wait_lds();                                            // and its reads of step s-1 returned
-      barrier();
-      issue(stage_at(std::integral_constant<int, (S + kLead) % NS>{}), wave, at(s + kLead));
-      fence();
-      step<ALL>(stage, wr, wt, lane, live);
+  }
+
+  // `tiles` tiles of `steps` steps each, from block `first` of the reduction on,
+  // as one stream: while a tile's last steps are multiplied the next one's first
+  // are on their way.  begin(i) sets the loads to tile i (0 is set before);
+  // end(i) finishes tile i's sums; live(i): whether this wave has any of its tokens
+  // (ALL: not asked).  ONE: one tile only.
+  template <bool ALL, bool ONE, class At, class Begin, class End, class Live>
+  __device__ __forceinline__ void run(At&& stage_at, int wave, int wr, int wt, int lane, int first, int steps, int tiles, int K,
+                                      Begin&& begin, End&& end, Live&& live) {
+    int in = 0, tile_in = 0;                                 // the next loads' step and tile
+    // past the last tile they are issued out of range: they read nothing
+    auto issue = [&](const Stage& stage) MOE_INLINE {
+      const uint32_t at = tile_in < tiles ? (uint32_t)(first + in) : kOutside / kBlock;
+      issue_tokens(stage.x, at);
+      issue_weights(stage.w, wave, at);
+      ++in;
+      if (ONE) {
+        if (in == steps) tile_in = 1;
+      } else if (in == steps) {
+        in = 0;
+        if (++tile_in < tiles) begin(tile_in);
+      }
     };
-    int s0 = 0;
-    for (; s0 + NS <= steps; s0 += NS)
-      for_each<NS>([&](auto i) { body(i, s0 + decltype(i)::value); });
-    for_each<NS - 1>([&](auto i) {
-      if (s0 + decltype(i)::value < steps) body(i, s0 + decltype(i)::value);
+    for_each<kLead>([&](auto s) MOE_INLINE { issue(stage_at(s)); });
+    clear_sums();
+    int out = 0, tile_out = 0;
+    bool here = ALL || live(0);
+    auto body = [&](auto stage_c) MOE_INLINE {
+      constexpr int S = decltype(stage_c)::value;
+      const Stage stage = stage_at(stage_c);
+      wait_loads<(kLead - 1) * kLoads>();                    // this wave's loads of the step have landed
+      const int rest = K - (first + out) * kBlock;
+      if (rest < kBlock) clear_tail(stage, wave, lane, rest / 16);
+      wait_lds();                                            // and its reads of the step before returned
+      barrier();
+      // (spread between the products instead, they end later: 4096^3 65.0 us, and 66.5)
+      issue(stage_at(std::integral_constant<int, (S + kLead) % NS>{}));
+      if (ALL || here) products(stage, wr, wt, lane);
+      ++out;
+      if (!ONE && out == steps) {
+        out = 0;
+        end(tile_out);
+        if (++tile_out < tiles) {
+          clear_sums();
+          if constexpr (!ALL) here = live(tile_out);
+        }
+      }
+    };
+    int left = tiles * steps;
+    for (; left >= NS; left -= NS) for_each<NS>([&](auto i) MOE_INLINE { body(i); });
+    for_each<NS - 1>([&](auto i) MOE_INLINE {
+      if (decltype(i)::value < left) body(i);
     });
     wait_loads<0>();                                         // the loads past the last step have landed
+    if (ONE) end(0);
   }
 };
 
-// The stages' memory, and stage_at of Tile::run
+// The stages' memory, one array each, so that reads of one are seen not to
+// alias the loads in flight to the others; and stage_at of Tile::run
 #define MOE_TILE_STAGES(TILE)                                                          \
-  __shared__ __align__(16) uint8_t s_0[TILE::kStageBytes];                             \
-  __shared__ __align__(16) uint8_t s_1[TILE::kStageBytes];                             \
-  __shared__ __align__(16) uint8_t s_2[TILE::NS > 2 ? TILE::kStageBytes : 16];         \
-  __shared__ __align__(16) uint8_t s_3[TILE::NS > 3 ? TILE::kStageBytes : 16];         \
-  auto stage_at = [&](auto i) -> uint8_t* {                                            \
+  __shared__ __align__(16) uint8_t s_w0[TILE::kScaledBytes];                           \
+  __shared__ __align__(16) uint8_t s_w1[TILE::kScaledBytes];                           \
+  __shared__ __align__(16) uint8_t s_w2[TILE::NS > 2 ? TILE::kScaledBytes : 16];       \
+  __shared__ __align__(16) uint8_t s_w3[TILE::NS > 3 ? TILE::kScaledBytes : 16];       \
+  __shared__ __align__(16) uint8_t s_x0[TILE::kTokenBytes];                            \
+  __shared__ __align__(16) uint8_t s_x1[TILE::kTokenBytes];                            \
+  __shared__ __align__(16) uint8_t s_x2[TILE::NS > 2 ? TILE::kTokenBytes : 16];        \
+  __shared__ __align__(16) uint8_t s_x3[TILE::NS > 3 ? TILE::kTokenBytes : 16];        \
+  auto stage_at = [&](auto i) -> Stage {                                               \
     constexpr int I = decltype(i)::value;                                              \
-    if constexpr (I == 0) return s_0;                                                  \
-    else if constexpr (I == 1) return s_1;                                             \
-    else if constexpr (I == 2) return s_2;                                             \
-    else return s_3;                                                                   \
+    if constexpr (I == 0) return {s_w0, s_x0};                                         \
+    else if constexpr (I == 1) return {s_w1, s_x1};                                    \
+    else if constexpr (I == 2) return {s_w2, s_x2};                                    \
+    else return {s_w3, s_x3};                                                          \
   };
 
 }  // namespace
