@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs
   const float* const sw = p.w.s + (size_t)(n0 / kBlock) * kb;
   tl.token_scales(wave, lane, [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)kb * 4u; });
   tl.scales(p.sx + (size_t)t0 * kb, (uint32_t)toks * (uint32_t)kb * 4u, sw, rows > kBlock ? sw + kb : sw, kb, wave);
-  tl.template run<true, true>(stage_at, wave, wr, wt, lane, first, steps, 1, p.K, [](int) {}, [&](int) MOE_INLINE {
+  tl.template run<true, true, 0>(stage_at, wave, wr, wt, lane, first, steps, 1, p.K, [](int) {}, [&](int) MOE_INLINE {
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {
       const int r = (wt * T::JT + j) * 16 + (lane & 15);

@@ -33,52 +33,59 @@ struct FfnArgs {
   int* n_items;
 };
 
+// Sum over the lanes up to this one
+__device__ __forceinline__ int wave_scan(int v) {
+  auto from = [&](auto ctrl, auto rows) {
+    return __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+  };
+  using std::integral_constant;
+  v += from(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});       // within rows of 16: from 1, 2, 4, 8 lanes below
+  v += from(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+  v += from(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+  v += from(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+  v += from(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});       // row 0's last to row 1, 2's to 3
+  v += from(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});       // lane 31 to rows 2 and 3
+  return v;
+}
+
 // An item for each piece of an expert's routes, experts in order.  Pieces hold up
 // to `size` routes, between half a tile and a whole one, chosen so that the
 // workgroups' longest run of gate/up tiles takes the least loads: `size` token
 // rows and 256 weight rows a step.  (T = 2000 4096x2048 of 16 experts: gate/up
 // 150 us with whole tiles,  so.)
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(FfnArgs p, int tt, int row_tiles, int groups) {
-  constexpr int kSizes = 9;
-  __shared__ int s_sum[kPlanThreads / kWave][kSizes];
+template <int TT>
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(FfnArgs p, int row_tiles, int groups) {
+  // whole token tiles, so that no piece is empty
+  constexpr int kSizes = TT / 32 + 1, kWaves = kPlanThreads / kWave;
+  __shared__ int s_sum[kSizes][kWaves];
+  __shared__ int s_before[kWaves];
   const int e = threadIdx.x, lane = e & (kWave - 1), wave = e >> 6;
   const int count = e < p.E ? p.count[e] : 0, first = e < p.E ? p.offset[e] : 0;
-  auto size_of = [&](int c) { return min(tt, tt / 2 + c * 16); };      // whole token tiles, so that no piece is empty
-  for (int c = 0; c < kSizes; ++c) {
-    const int size = size_of(c);
-    int sum = (count + size - 1) / size;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
-    if (lane == 0) s_sum[wave][c] = sum;
-  }
+  for_each<kSizes>([&](auto c) MOE_INLINE {
+    constexpr int C = decltype(c)::value, kSize = TT / 2 + 16 * C;
+    const int sum = wave_scan((count + kSize - 1) / kSize);
+    if (lane == kWave - 1) s_sum[C][wave] = sum;
+  });
   __syncthreads();
-  int size = tt;
-  long long best = 0;
-  for (int c = kSizes - 1; c >= 0; --c) {
-    int items = 0;
-    for (int w = 0; w < kPlanThreads / kWave; ++w) items += s_sum[w][c];
-    const int rows = size_of(c);
-    const long long cost = (((long long)items * row_tiles + groups - 1) / groups) * (kTileRows + rows);
-    if (c == kSizes - 1 || cost < best) best = cost, size = rows;
+  int items = 0;
+  const int mine = min(lane, kSizes - 1);                    // a lane to a size
+  for (int w = 0; w < kWaves; ++w) items += s_sum[mine][w];
+  const long long cost = (((long long)items * row_tiles + groups - 1) / groups) * (kTileRows + TT / 2 + 16 * mine);
+  int size = TT;
+  long long best = __shfl(cost, kSizes - 1, kWave);
+  for (int c = kSizes - 2; c >= 0; --c) {
+    const long long other = __shfl(cost, c, kWave);
+    if (other < best) best = other, size = TT / 2 + 16 * c;
   }
   const int pieces = (count + size - 1) / size;
-  int sum = pieces;
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int v = __shfl_up(sum, d, kWave);
-    if (lane >= d) sum += v;
-  }
-  __syncthreads();
-  if (lane == kWave - 1) s_sum[wave][0] = sum;
+  const int sum = wave_scan(pieces);
+  if (lane == kWave - 1) s_before[wave] = sum;
   __syncthreads();
   int at = sum - pieces;
-  for (int w = 0; w < wave; ++w) at += s_sum[w][0];
+  for (int w = 0; w < wave; ++w) at += s_before[w];
   // even pieces, of whole token tiles
   const int even = pieces > 0 ? ((count + pieces - 1) / pieces + 15) & ~15 : 0;
-  for (int i = 0; i < pieces; ++i) {
-    const int rest = count - i * even;
-    p.items[at + i] = make_int4(e, first + i * even, min(even, rest), 0);
-  }
+  for (int i = 0; i < pieces; ++i) p.items[at + i] = make_int4(e, first + i * even, min(even, count - i * even), 0);
   if (e == kPlanThreads - 1) *p.n_items = at + pieces;
 }
 
@@ -86,13 +93,18 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(FfnArgs p, int tt, i
 struct Item {
   int expert, first, toks;
 };
+// (through the scalar cache: a vector load would wait for the loads in flight)
+template <class V>
+__device__ __forceinline__ V scalar_load(const V* at) {
+  return *(const __attribute__((address_space(4))) V*)(uintptr_t)at;
+}
 __device__ __forceinline__ Item item_at(const FfnArgs& p, int i) {
   if (p.items) {
-    const int4 v = p.items[i];
-    return {v.x, v.y, v.z};
+    const i32x4 v = scalar_load(reinterpret_cast<const i32x4*>(p.items) + i);
+    return {v[0], v[1], v[2]};
   }
-  const int e = p.active[i];
-  return {e, p.offset[e], p.count[e]};
+  const int e = scalar_load(p.active + i);
+  return {e, scalar_load(p.offset + e), scalar_load(p.count + e)};
 }
 
 // A workgroup's tiles: a run of those of all items, an item's row tiles one
@@ -103,7 +115,7 @@ struct Run {
   int first, tiles;
 };
 __device__ __forceinline__ Run run_of(const FfnArgs& p, int row_tiles) {
-  const long long all = (long long)(p.items ? *p.n_items : *p.n_active) * row_tiles;
+  const long long all = (long long)scalar_load(p.items ? p.n_items : p.n_active) * row_tiles;
   const int groups = (int)gridDim.x / kXcds, at = (int)blockIdx.x % kXcds * groups + (int)blockIdx.x / kXcds;
   const int first = (int)(all * at / (int)gridDim.x);
   return {first, (int)(all * (at + 1) / (int)gridDim.x) - first};
@@ -131,7 +143,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
       loaded = number;
       item_in = item_at(p, number);
       auto token = [&](int r) MOE_INLINE { return (uint32_t)(p.src[item_in.first + min(r, item_in.toks - 1)] / p.k); };
-      tl.tokens(wave, lane, [&](int r) { return r < item_in.toks ? token(r) * (uint32_t)p.H : kOutside; });
+      tl.tokens(wave, lane, [&](int r) MOE_INLINE {
+        const uint32_t at = token(r) * (uint32_t)p.H;
+        return r < item_in.toks ? at : kOutside;
+      });
       tl.token_scales(wave, lane, [&](int r) { return token(r) * (uint32_t)kb * 4u; });
     }
     const int n0 = tile * kBlock;
@@ -140,11 +155,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
     tl.scales(p.sx, (uint32_t)p.T * (uint32_t)kb * 4u, p.gate.s + scale, p.up.s + scale, kb, wave);
   };
   begin(0);
-  int done = -1;                                             // the item whose sums are made
-  Item item;
+  // The item whose sums are made.  When a tile's last step is done, the next one's
+  // first kLead are issued: with more steps than that a tile, the loads are still at
+  // it, and its item is theirs.
+  Item item = item_in;
+  int done = loaded;
   auto live = [&](int i) MOE_INLINE {
     const int number = (run.first + i) / row_tiles;
-    if (number != done) item = item_at(p, done = number);
+    if (number != done) {
+      done = number;
+      item = kb > T::kLead ? item_in : item_at(p, number);
+    }
     return item.toks > wt * T::JT * 16;
   };
   auto end = [&](int i) MOE_INLINE {
@@ -169,29 +190,30 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
     }
     wait_lds();
     barrier();
+    // every lane stores, those past the item's routes or I out of range
+    const __amdgpu_buffer_rsrc_t to_q = make_rsrc(p.hq + (size_t)first * p.I, (uint32_t)toks * (uint32_t)p.I);
+    const __amdgpu_buffer_rsrc_t to_s = make_rsrc(p.hs + (size_t)first * ib, (uint32_t)toks * (uint32_t)ib * 4u);
+    const int n = n0 + T::group_of(wr, 0) + g * (4 * Q);
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {
       const int r = (wt * T::JT + j) * 16 + (l & 15);
-      if (r >= toks) continue;
       uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < T::WR; ++w) top = max(top, s_max[w * TT + r]);
       const float s = block_scale(__uint_as_float(top)), inv = 1.0f / s;
-      const size_t row = (size_t)(first + r);
-      if (wr == 0 && g == 0) p.hs[row * ib + tile] = s;
-      const int n = n0 + T::group_of(wr, 0) + g * (4 * Q);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), to_s,
+                                            wr == 0 && g == 0 && r < toks ? (uint32_t)(r * ib + tile) * 4u : kOutside, 0, 0);
       uint32_t c[Q];
 #pragma unroll
       for (int q = 0; q < Q; ++q) c[q] = encode4(tl.acc[q][j][0], tl.acc[q][j][1], tl.acc[q][j][2], tl.acc[q][j][3], inv);
       static_assert(HT == Q, "a lane's values of a token are neighbours");
-      uint8_t* const to = p.hq + row * p.I + n;              // (I is a multiple of 16)
-      if (n >= p.I) continue;
-      if constexpr (Q == 4) *reinterpret_cast<uint4*>(to) = make_uint4(c[0], c[1], c[2], c[3]);
-      else if constexpr (Q == 2) *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
-      else *reinterpret_cast<uint32_t*>(to) = c[0];
+      const uint32_t at = n < p.I && r < toks ? (uint32_t)r * (uint32_t)p.I + (uint32_t)n : kOutside;      // (I is a multiple of 16)
+      if constexpr (Q == 4) __builtin_amdgcn_raw_buffer_store_b128(u32x4{c[0], c[1], c[2], c[3]}, to_q, at, 0, 0);
+      else if constexpr (Q == 2) __builtin_amdgcn_raw_buffer_store_b64(u32x2{c[0], c[1]}, to_q, at, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b32(c[0], to_q, at, 0, 0);
     }
   };
-  tl.template run<false, false>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.H, begin, end, live);
+  tl.template run<false, false, 2 * T::JT>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.H, begin, end, live);
 }
 
 // o of 256 rows of an item's routes
@@ -225,11 +247,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
               rows > kBlock ? sw + kb : sw, kb, wave);
   };
   begin(0);
-  int done = -1;                                             // the item whose sums are made
-  Item item;
+  // The item whose sums are made.  When a tile's last step is done, the next one's
+  // first kLead are issued: with more steps than that a tile, the loads are still at
+  // it, and its item is theirs.
+  Item item = item_in;
+  int done = loaded;
   auto live = [&](int i) MOE_INLINE {
     const int number = (run.first + i) / row_tiles;
-    if (number != done) item = item_at(p, done = number);
+    if (number != done) {
+      done = number;
+      item = kb > T::kLead ? item_in : item_at(p, number);
+    }
     return item.toks > wt * T::JT * 16;
   };
   auto end = [&](int i) MOE_INLINE {
@@ -255,21 +283,22 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
     barrier();
     constexpr int kShare = T::WR / 2;                        // waves of a block of rows
     const int block = n0 / kBlock + wr / kShare;
+    // every lane stores, those past the item's routes or H out of range
+    const __amdgpu_buffer_rsrc_t to_o = make_rsrc(p.o + (size_t)first * p.H, (uint32_t)toks * (uint32_t)p.H * 2u);
+    const __amdgpu_buffer_rsrc_t to_s = make_rsrc(p.os + (size_t)first * hb, (uint32_t)toks * (uint32_t)hb * 4u);
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {
       const int r = (wt * T::JT + j) * 16 + (l & 15);
-      if (r >= toks || block >= hb) continue;
       uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < kShare; ++w) top = max(top, s_max[(wr / kShare * kShare + w) * TT + r]);
       const uint32_t ex = max(top >> 23, 15u);
       const float inv = __uint_as_float((268u - ex) << 23);
-      const size_t row = (size_t)(first + r);
-      if (wr % kShare == 0 && g == 0) p.os[row * hb + block] = __uint_as_float((ex - 14u) << 23);
+      const bool whose = wr % kShare == 0 && g == 0 && r < toks && block < hb;
+      __builtin_amdgcn_raw_buffer_store_b32((ex - 14u) << 23, to_s, whose ? (uint32_t)(r * hb + block) * 4u : kOutside, 0, 0);
 #pragma unroll
       for (int m = 0; m < T::MT; m += T::Q) {
         const int n = n0 + T::group_of(wr, m) + g * (4 * T::Q);
-        if (n >= p.H) continue;                              // (H is a multiple of 16)
         uint32_t c[2 * T::Q];
 #pragma unroll
         for (int q = 0; q < T::Q; ++q) {
@@ -277,13 +306,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
           c[2 * q] = f32_to_f16_bits(v[0] * inv) | f32_to_f16_bits(v[1] * inv) << 16;
           c[2 * q + 1] = f32_to_f16_bits(v[2] * inv) | f32_to_f16_bits(v[3] * inv) << 16;
         }
-        uint4* const to = reinterpret_cast<uint4*>(p.o + row * p.H + n);
+        const uint32_t at = n < p.H && r < toks ? ((uint32_t)r * (uint32_t)p.H + (uint32_t)n) * 2u : kOutside;       // (H is a multiple of 16)
 #pragma unroll
-        for (int q = 0; q < T::Q / 2; ++q) to[q] = make_uint4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]);
+        for (int q = 0; q < T::Q / 2; ++q)
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]}, to_o, at + 16 * q, 0, 0);
       }
     }
   };
-  tl.template run<false, false>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.I, begin, end, live);
+  tl.template run<false, false, (1 + T::MT / 2) * T::JT>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.I, begin, end, live);
 }
 
 // A thread to eight outputs of a token
@@ -399,7 +429,8 @@ extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scal
     items = most_items(R, E, tt);
     p.items = reinterpret_cast<int4*>(take((size_t)items * sizeof(int4)));
     p.n_items = reinterpret_cast<int*>(take(4));
-    plan_kernel<<<1, kPlanThreads, 0, s>>>(p, tt, blocks_of(I), device_cu_count());
+    if (tt == 128) plan_kernel<128><<<1, kPlanThreads, 0, s>>>(p, blocks_of(I), device_cu_count());
+    else plan_kernel<256><<<1, kPlanThreads, 0, s>>>(p, blocks_of(I), device_cu_count());
   }
   switch (tt) {
     case 16: launch_products<16>(p, items, s); break;

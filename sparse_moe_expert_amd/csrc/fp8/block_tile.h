@@ -224,8 +224,9 @@ struct Tile {
   // as one stream: while a tile's last steps are multiplied the next one's first
   // are on their way.  begin(i) sets the loads to tile i (0 is set before);
   // end(i) finishes tile i's sums; live(i): whether this wave has any of its tokens
-  // (ALL: not asked).  ONE: one tile only.
-  template <bool ALL, bool ONE, class At, class Begin, class End, class Live>
+  // (ALL: not asked).  ONE: one tile only; else end(i) stores STORES times, whatever
+  // the tile, and the next step need not wait for that.
+  template <bool ALL, bool ONE, int STORES, class At, class Begin, class End, class Live>
   __device__ __forceinline__ void run(At&& stage_at, int wave, int wr, int wt, int lane, int first, int steps, int tiles, int K,
                                       Begin&& begin, End&& end, Live&& live) {
     int in = 0, tile_in = 0;                                 // the next loads' step and tile
@@ -249,7 +250,9 @@ struct Tile {
     auto body = [&](auto stage_c) MOE_INLINE {
       constexpr int S = decltype(stage_c)::value;
       const Stage stage = stage_at(stage_c);
-      wait_loads<(kLead - 1) * kLoads>();                    // this wave's loads of the step have landed
+      // this wave's loads of the step have landed (loads and stores end in order)
+      if (!ONE && out == 0 && tile_out > 0) wait_loads<(kLead - 1) * kLoads + STORES>();
+      else wait_loads<(kLead - 1) * kLoads>();
       const int rest = K - (first + out) * kBlock;
       if (rest < kBlock) clear_tail(stage, wave, lane, rest / 16);
       wait_lds();                                            // and its reads of the step before returned
