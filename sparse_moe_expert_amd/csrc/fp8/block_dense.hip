@@ -66,8 +66,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs
   tl.rx = make_rsrc(p.x + (size_t)t0 * p.K, (uint32_t)toks * (uint32_t)p.K);
   tl.tokens(wave, lane, [&](int r) { return r < toks ? (uint32_t)r * (uint32_t)p.K : kOutside; });
   const float* const sw = p.w.s + (size_t)(n0 / kBlock) * kb;
-  tl.token_scales(wave, lane, [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)kb * 4u; });
-  tl.scales(p.sx + (size_t)t0 * kb, (uint32_t)toks * (uint32_t)kb * 4u, sw, rows > kBlock ? sw + kb : sw, kb, wave);
+  tl.token_scales(p.sx + (size_t)t0 * kb, (uint32_t)toks * (uint32_t)kb * 4u, 4, wave, lane,
+                  [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)kb * 4u; });
+  tl.weight_scales(sw, rows > kBlock ? sw + kb : sw, kb, wave);
   tl.template run<true, true, 0>(stage_at, wave, wr, wt, lane, first, steps, 1, p.K, [](int) {}, [&](int) MOE_INLINE {
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {

@@ -25,8 +25,9 @@ struct FfnArgs {
   uint16_t* y;
   int T, H, I, E, k;
   // by bucket position
+  float* xs;               // [blocks of H, R] the tokens' scales; null: taken from sx
   uint8_t* hq;             // [R, I]
-  float* hs;               // [R, blocks of I]
+  float* hs;               // [blocks of I, R]
   uint16_t* o;             // [R, H] fp16, over
   float* os;               // [R, blocks of H] powers of two
   int4* items;             // {expert, first position, routes, 0}; null: a chosen expert is one item
@@ -53,8 +54,21 @@ __device__ __forceinline__ int wave_scan(int v) {
 // workgroups' longest run of gate/up tiles takes the least loads: `size` token
 // rows and 256 weight rows a step.  (T = 2000 4096x2048 of 16 experts: gate/up
 // 150 us with whole tiles,  so.)
+//
+// The other workgroups copy the tokens' scales to bucket positions, a block of H
+// together: of [T, blocks] the tiles would fetch a cache line for each four
+// bytes (T = 4096 2048x512 of 512 experts: gate/up 257 us, and  so).
+constexpr int kScaleRows = 64;               // positions a workgroup
+
 template <int TT>
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(FfnArgs p, int row_tiles, int groups) {
+  if (blockIdx.x > 0) {
+    const int R = p.T * p.k, kb = blocks_of(p.H), r = ((int)blockIdx.x - 1) * kScaleRows + (int)threadIdx.x % kScaleRows;
+    if (r >= R) return;
+    const float* const from = p.sx + (size_t)(p.src[r] / p.k) * kb;
+    for (int b = (int)threadIdx.x / kScaleRows; b < kb; b += kPlanThreads / kScaleRows) p.xs[(size_t)b * R + r] = from[b];
+    return;
+  }
   // whole token tiles, so that no piece is empty
   constexpr int kSizes = TT / 32 + 1, kWaves = kPlanThreads / kWave;
   __shared__ int s_sum[kSizes][kWaves];
@@ -147,12 +161,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
         const uint32_t at = token(r) * (uint32_t)p.H;
         return r < item_in.toks ? at : kOutside;
       });
-      tl.token_scales(wave, lane, [&](int r) { return token(r) * (uint32_t)kb * 4u; });
+      if (p.xs)
+        tl.token_scales(p.xs + item_in.first, (uint32_t)item_in.toks * 4u, (size_t)p.T * p.k * 4, wave, lane,
+                        [](int r) { return (uint32_t)r * 4u; });
+      else
+        tl.token_scales(p.sx, (uint32_t)p.T * (uint32_t)kb * 4u, 4, wave, lane,
+                        [&](int r) { return token(r) * (uint32_t)kb * 4u; });
     }
     const int n0 = tile * kBlock;
     const size_t row = (size_t)item_in.expert * p.I + n0, scale = ((size_t)item_in.expert * ib + tile) * (size_t)kb;
     tl.weights(p.gate.q + row * p.H, p.up.q + row * p.H, min(kBlock, p.I - n0), p.H, wave, lane);
-    tl.scales(p.sx, (uint32_t)p.T * (uint32_t)kb * 4u, p.gate.s + scale, p.up.s + scale, kb, wave);
+    tl.weight_scales(p.gate.s + scale, p.up.s + scale, kb, wave);
   };
   begin(0);
   // The item whose sums are made.  When a tile's last step is done, the next one's
@@ -192,7 +211,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
     barrier();
     // every lane stores, those past the item's routes or I out of range
     const __amdgpu_buffer_rsrc_t to_q = make_rsrc(p.hq + (size_t)first * p.I, (uint32_t)toks * (uint32_t)p.I);
-    const __amdgpu_buffer_rsrc_t to_s = make_rsrc(p.hs + (size_t)first * ib, (uint32_t)toks * (uint32_t)ib * 4u);
+    const __amdgpu_buffer_rsrc_t to_s = make_rsrc(p.hs + (size_t)tile * p.T * p.k + first, (uint32_t)toks * 4u);
     const int n = n0 + T::group_of(wr, 0) + g * (4 * Q);
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {
@@ -202,7 +221,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
       for (int w = 0; w < T::WR; ++w) top = max(top, s_max[w * TT + r]);
       const float s = block_scale(__uint_as_float(top)), inv = 1.0f / s;
       __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), to_s,
-                                            wr == 0 && g == 0 && r < toks ? (uint32_t)(r * ib + tile) * 4u : kOutside, 0, 0);
+                                            wr == 0 && g == 0 ? (uint32_t)r * 4u : kOutside, 0, 0);
       uint32_t c[Q];
 #pragma unroll
       for (int q = 0; q < Q; ++q) c[q] = encode4(tl.acc[q][j][0], tl.acc[q][j][1], tl.acc[q][j][2], tl.acc[q][j][3], inv);
@@ -237,14 +256,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
       item_in = item_at(p, number);
       tl.rx = make_rsrc(p.hq + (size_t)item_in.first * p.I, (uint32_t)item_in.toks * (uint32_t)p.I);
       tl.tokens(wave, lane, [&](int r) { return r < item_in.toks ? (uint32_t)r * (uint32_t)p.I : kOutside; });
-      tl.token_scales(wave, lane, [&](int r) { return (uint32_t)min(r, item_in.toks - 1) * (uint32_t)kb * 4u; });
+      tl.token_scales(p.hs + item_in.first, (uint32_t)item_in.toks * 4u, (size_t)p.T * p.k * 4, wave, lane,
+                      [](int r) { return (uint32_t)r * 4u; });
     }
     const int rows = min(kTileRows, p.H - n0);
     const uint8_t* const w = p.down.q + ((size_t)item_in.expert * p.H + n0) * (size_t)p.I;
     tl.weights(w, w, rows, p.I, wave, lane);
     const float* const sw = p.down.s + ((size_t)item_in.expert * hb + n0 / kBlock) * (size_t)kb;
-    tl.scales(p.hs + (size_t)item_in.first * kb, (uint32_t)item_in.toks * (uint32_t)kb * 4u, sw,
-              rows > kBlock ? sw + kb : sw, kb, wave);
+    tl.weight_scales(sw, rows > kBlock ? sw + kb : sw, kb, wave);
   };
   begin(0);
   // The item whose sums are made.  When a tile's last step is done, the next one's
@@ -391,7 +410,7 @@ extern "C" size_t moe_block_expert_ffn_workspace_size(int T, int H, int I, int E
   if (T <= 0 || !ffn_dims_ok(T, H, I, E, k) || !ffn_dims_fit(T, H, I, E, k)) return 0;
   const size_t R = (size_t)T * (size_t)k;
   return align256(R * I) + align256(R * blocks_of(I) * 4) + align256(R * H * 2) + align256(R * blocks_of(H) * 4) +
-         (T > 128 ? align256((size_t)most_items(R, E, 128) * sizeof(int4)) + 256 : 0);
+         (T > 128 ? align256((size_t)most_items(R, E, 128) * sizeof(int4)) + 256 + align256(R * blocks_of(H) * 4) : 0);
 }
 
 extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scale, const uint8_t* w_gate,
@@ -417,7 +436,7 @@ extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scal
   uint8_t* at = static_cast<uint8_t*>(workspace);
   auto take = [&](size_t n) { uint8_t* const b = at; at += align256(n); return b; };
   FfnArgs p{x, x_scale, {w_gate, s_gate}, {w_up, s_up}, {w_down, s_down}, topk_w, expert_count, expert_offset,
-            active_experts, n_active, route_src, route_pos, y, T, H, I, E, k, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+            active_experts, n_active, route_src, route_pos, y, T, H, I, E, k, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   p.hq = take(R * I);
   p.hs = reinterpret_cast<float*>(take(R * blocks_of(I) * 4));
   p.o = reinterpret_cast<uint16_t*>(take(R * H * 2));
@@ -429,8 +448,10 @@ extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scal
     items = most_items(R, E, tt);
     p.items = reinterpret_cast<int4*>(take((size_t)items * sizeof(int4)));
     p.n_items = reinterpret_cast<int*>(take(4));
-    if (tt == 128) plan_kernel<128><<<1, kPlanThreads, 0, s>>>(p, blocks_of(I), device_cu_count());
-    else plan_kernel<256><<<1, kPlanThreads, 0, s>>>(p, blocks_of(I), device_cu_count());
+    p.xs = reinterpret_cast<float*>(take(R * blocks_of(H) * 4));
+    const unsigned grid = 1 + (unsigned)((R + kScaleRows - 1) / kScaleRows);
+    if (tt == 128) plan_kernel<128><<<grid, kPlanThreads, 0, s>>>(p, blocks_of(I), device_cu_count());
+    else plan_kernel<256><<<grid, kPlanThreads, 0, s>>>(p, blocks_of(I), device_cu_count());
   }
   switch (tt) {
     case 16: launch_products<16>(p, items, s); break;

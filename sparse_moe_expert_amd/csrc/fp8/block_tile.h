@@ -76,7 +76,10 @@ struct Tile {
   static constexpr int kLoads = 4 + 1 + XL;
   static_assert(NS >= 2 && (kLead - 1) * kLoads < 64, "two stages or more");
 
-  __amdgpu_buffer_rsrc_t rw, rx, rs;         // the wave's weight rows, the tokens, the wave's scales
+  __amdgpu_buffer_rsrc_t rw, rx;             // the wave's weight rows, the tokens
+  const float* s_from;                       // the wave's scales
+  uint32_t s_bytes;
+  size_t s_stride;
   uint32_t w_off[4], x_off[XL], s_off;
   uint32_t token_at, scale_at;               // where a wave's first token piece and its scales go
   f32x4 acc[MT][JT];
@@ -122,24 +125,33 @@ struct Tile {
     token_at = (TT < 64 ? wave % (TT / 8) : wave) * 1024u;
   }
 
-  // A wave's 64 scales: of tokens, f(r) the offset of row r's in sx; else one of
-  // the weights', of the first matrix or rows, or of the second
+  // A wave's 64 scales of a step: of tokens, at `first` + step * stride bytes, f(r)
+  // the offset of row r's; else one of the weights', of the first matrix or rows,
+  // or of the second.
   template <class F>
-  __device__ __forceinline__ void token_scales(int wave, int lane, F&& f) {
+  __device__ __forceinline__ void token_scales(const float* first, uint32_t bytes, size_t stride, int wave, int lane, F&& f) {
     const int group = wave % kScaleGroups;
     scale_at = kWeightBytes + group * 256u;
-    s_off = group < kScaleGroups - 2 ? f(min(group * 64 + lane, TT - 1)) : 0;
+    s_off = 0;
+    if (group < kScaleGroups - 2) {
+      s_from = first, s_bytes = bytes, s_stride = stride;
+      s_off = f(min(group * 64 + lane, TT - 1));
+    }
   }
-  __device__ __forceinline__ void scales(const float* sx, uint32_t bytes, const float* first, const float* second, int kb, int wave) {
+  __device__ __forceinline__ void weight_scales(const float* first, const float* second, int kb, int wave) {
     const int group = wave % kScaleGroups;
-    if (group < kScaleGroups - 2) rs = make_rsrc(sx, bytes);
-    else rs = make_rsrc(group == kScaleGroups - 2 ? first : second, (uint32_t)kb * 4u);
+    if (group >= kScaleGroups - 2)
+      s_from = group == kScaleGroups - 2 ? first : second, s_bytes = (uint32_t)kb * 4u, s_stride = 4;
   }
 
   // Load i (a constant) of a step: its weights, scales, then tokens
   __device__ __forceinline__ void issue_scaled(int i, uint8_t* w, int wave, uint32_t step) {
     if (i < 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, w + (wave * 4 + i) * 1024, 16, w_off[i] + step * kBlock, 0, 0, 0);
-    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, w + scale_at, 4, s_off + step * 4u, 0, 0, 0);
+    else {
+      const bool none = step >= kOutside / kBlock;
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<const uint8_t*>(s_from) + (none ? 0 : step * s_stride), s_bytes);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, w + scale_at, 4, none ? kOutside : s_off, 0, 0, 0);
+    }
   }
   __device__ __forceinline__ void issue_token(int i, uint8_t* x, uint32_t step) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, x + token_at + i * 8192, 16, x_off[i] + step * kBlock, 0, 0, 0);
