@@ -1,52 +1,16 @@
 // A dense layer in 8 bits: moe_block_linear.
+#include "block_linear.h"
 #include "block_tile.h"
 
 namespace moe {
 namespace {
 
-struct LinearArgs {
-  const uint8_t* x;
-  const float* sx;
-  BlockMat w;
-  const uint16_t* bias;
-  uint16_t* y;
-  int T, N, K;
-};
-
-// COUNT (a multiple of 4) outputs of a token from n on, from their sums; those
-// at or past N are left alone
-template <int COUNT>
-__device__ __forceinline__ void write(const LinearArgs& p, int t, int n, float (&v)[COUNT]) {
-  if (n >= p.N) return;
-  const size_t at = (size_t)t * p.N + n;
-  if (p.bias) {
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) v[i] += bf16_to_f32(p.bias[min(n + i, p.N - 1)]);
-  }
-  uint32_t o[COUNT / 2];
-#pragma unroll
-  for (int i = 0; i < COUNT / 2; ++i) o[i] = to_bf16(v[2 * i]) | to_bf16(v[2 * i + 1]) << 16;
-  if (COUNT % 8 == 0 && p.N % 8 == 0 && n + COUNT <= p.N) {
-#pragma unroll
-    for (int i = 0; i < COUNT / 8; ++i)
-      *reinterpret_cast<uint4*>(p.y + at + 8 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-  } else if (p.N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < COUNT / 4; ++i)
-      if (n + 4 * i < p.N) *reinterpret_cast<uint2*>(p.y + at + 4 * i) = make_uint2(o[2 * i], o[2 * i + 1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i)
-      if (n + i < p.N) p.y[at + i] = (uint16_t)(o[i / 2] >> (i % 2 * 16));
-  }
-}
-
-// Tiles of 256 rows by TT tokens; with more than one part of the reduction
+// Tiles of ROWS rows by TT tokens; with more than one part of the reduction
 // (`splits`) fp32 sums go to [part][T][Np], Np rows of whole tiles.
-template <int TT>
+template <int TT, int ROWS, int U>
 __global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs p, int row_tiles, int token_tiles, int splits,
                                                                       float* __restrict__ sums) {
-  using T = Tile<TT, false>;
+  using T = Tile<TT, false, ROWS, U>;
   MOE_TILE_STAGES(T)
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave % T::WR, wt = wave / T::WR;
@@ -56,15 +20,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs
   if (tile >= tiles) return;
   // groups of four token tiles, row tile by row tile
   const int group = tile / (4 * row_tiles), in = tile % (4 * row_tiles), width = min(4, token_tiles - group * 4);
-  const int n0 = in / width * kTileRows, t0 = (group * 4 + in % width) * TT;
-  const int rows = min(kTileRows, p.N - n0), toks = min(TT, p.T - t0), kb = blocks_of(p.K);
-  const int first = (int)((long long)kb * part / splits), steps = (int)((long long)kb * (part + 1) / splits) - first;
+  const int n0 = in / width * ROWS, t0 = (group * 4 + in % width) * TT;
+  const int rows = min(ROWS, p.N - n0), toks = min(TT, p.T - t0), kb = blocks_of(p.K);
+  const int all = (kb + U - 1) / U, first = (int)((long long)all * part / splits);
+  const int steps = (int)((long long)all * (part + 1) / splits) - first;
 
   T tl;
   const uint8_t* const w = p.w.q + (size_t)n0 * p.K;
   tl.weights(w, w, rows, p.K, wave, lane);
   tl.rx = make_rsrc(p.x + (size_t)t0 * p.K, (uint32_t)toks * (uint32_t)p.K);
-  tl.tokens(wave, lane, [&](int r) { return r < toks ? (uint32_t)r * (uint32_t)p.K : kOutside; });
+  tl.tokens(p.K, wave, lane);
   const float* const sw = p.w.s + (size_t)(n0 / kBlock) * kb;
   tl.token_scales(p.sx + (size_t)t0 * kb, (uint32_t)toks * (uint32_t)kb * 4u, 4, wave, lane,
                   [&](int r) { return (uint32_t)min(r, toks - 1) * (uint32_t)kb * 4u; });
@@ -78,7 +43,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs
       for (int m = 0; m < T::MT; m += T::Q) {
         const int n = n0 + T::group_of(wr, m) + (lane >> 4) * (4 * T::Q);
         if (splits > 1) {
-          const size_t np = (size_t)row_tiles * kTileRows;
+          const size_t np = (size_t)row_tiles * ROWS;
           float* const to = sums + ((size_t)part * p.T + t0 + r) * np + n;
 #pragma unroll
           for (int q = 0; q < T::Q; ++q) *reinterpret_cast<f32x4*>(to + 4 * q) = tl.acc[m + q][j];
@@ -108,30 +73,56 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs p, int np, 
   write(p, t, n, v);
 }
 
+// (the size of a workspace does not go by the device that asks)
+constexpr int kComputeUnits = 256;
+
+// A kernel of tiles: its tokens, rows, blocks a step; about what a workgroup's
+// start and end take and a block of its reduction, in ns.  (Measured with up to
+// 256 tiles: T = 333 2560x5200 18.7 us with 64x64 tiles, 21.8 with 128x64 in two
+// parts, 27.4 with 256x128 in six; T = 500 2048x2048 8.7, 10.1 with 128x64, 13.1
+// with 128x128; T = 1000 4096x4096 25.6 with 128x128, 31.1 with 128x64, 36.2 with
+// 256x128; T = 2000 2560x2560 25.7 with 256x128, 30.6 with 128x128.)
+struct Kind {
+  int tt, rows, unit;
+  float start_ns, block_ns;
+};
+constexpr Kind kKinds[] = {{256, 256, 1, 9000.0f, 1650.0f}, {128, 256, 1, 5500.0f, 1080.0f}, {128, 128, 1, 3400.0f, 670.0f},
+                           {64, 128, 1, 2400.0f, 430.0f},   {64, 64, 2, 1900.0f, 330.0f},    {32, 64, 2, 1500.0f, 210.0f}};
+
 struct Plan {
-  int tt, row_tiles, token_tiles, splits;
-  size_t sums() const { return splits > 1 ? (size_t)splits * row_tiles * kTileRows * 4 : 0; }      // a token
+  int kind, row_tiles, token_tiles, splits;
+  size_t sums() const { return splits > 1 ? (size_t)splits * row_tiles * kKinds[kind].rows * 4 : 0; }       // a token
 };
 
+// The kind and number of parts that should take least: rounds of workgroups, one
+// on a compute unit, and where there are parts (few tiles, a long reduction) their
+// sums written and joined.
 Plan plan_of(int T, int N, int K) {
-  Plan pl;
-  pl.row_tiles = (N + kTileRows - 1) / kTileRows;
-  pl.tt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-  if (pl.tt == 256 && (long long)pl.row_tiles * ((T + 255) / 256) < 160) pl.tt = 128;
-  pl.token_tiles = (T + pl.tt - 1) / pl.tt;
-  const int tiles = pl.row_tiles * pl.token_tiles, kb = blocks_of(K);
-  pl.splits = tiles >= 128 ? 1 : 256 / tiles;
-  if (pl.splits > kb) pl.splits = kb;
-  if (pl.splits > 16) pl.splits = 16;
-  while (pl.splits > 1 && pl.sums() * T > MOE_BLOCK_SUMS_BYTES) --pl.splits;
-  return pl;
+  Plan best{};
+  float least = 0.0f;
+  const int kb = blocks_of(K), units = kComputeUnits;
+  for (int kind = 0; kind < (int)(sizeof(kKinds) / sizeof(kKinds[0])); ++kind) {
+    const Kind& c = kKinds[kind];
+    Plan pl{kind, (N + c.rows - 1) / c.rows, (T + c.tt - 1) / c.tt, 1};
+    const long long tiles = (long long)pl.row_tiles * pl.token_tiles;
+    const int steps = (kb + c.unit - 1) / c.unit;
+    for (pl.splits = 1; pl.splits <= 16 && pl.splits <= steps; ++pl.splits) {
+      if (pl.splits > 1 && (tiles * pl.splits > units || pl.sums() * T > MOE_BLOCK_SUMS_BYTES)) break;
+      const long long rounds = (tiles * pl.splits + units - 1) / units;
+      float ns = (float)rounds * (c.start_ns + (float)((steps + pl.splits - 1) / pl.splits * c.unit) * c.block_ns);
+      if (pl.splits > 1) ns += 4000.0f + (float)(pl.sums() * T) / 3000.0f;
+      if (least == 0.0f || ns < least) least = ns, best = pl;
+    }
+  }
+  return best;
 }
 
-template <int TT>
+template <int KIND>
 void launch_tiles(const LinearArgs& p, const Plan& pl, float* sums, hipStream_t s) {
+  constexpr Kind c = kKinds[KIND];
   const int tiles = pl.row_tiles * pl.token_tiles;
   const unsigned grid = (unsigned)((tiles + kXcds - 1) / kXcds * kXcds) * (unsigned)pl.splits;
-  linear_tile_kernel<TT><<<grid, kTileThreads, 0, s>>>(p, pl.row_tiles, pl.token_tiles, pl.splits, sums);
+  linear_tile_kernel<c.tt, c.rows, c.unit><<<grid, kTileThreads, 0, s>>>(p, pl.row_tiles, pl.token_tiles, pl.splits, sums);
 }
 
 inline bool linear_dims_ok(int N, int K) { return N >= 1 && K >= 16 && K % 16 == 0; }
@@ -142,7 +133,7 @@ inline bool linear_dims_fit(int N, int K) { return N <= (1 << 20) && K <= kBlock
 
 extern "C" size_t moe_block_linear_workspace_size(int T, int N, int K) {
   using namespace moe;
-  if (T <= 0 || T > kBlockMaxTokens || !linear_dims_ok(N, K) || !linear_dims_fit(N, K)) return 0;
+  if (T <= 0 || T > kBlockMaxTokens || !linear_dims_ok(N, K) || !linear_dims_fit(N, K) || linear_few_ok(T, N, K)) return 0;
   return align256(plan_of(T, N, K).sums() * T);
 }
 
@@ -162,19 +153,21 @@ extern "C" moe_status moe_block_linear(const uint8_t* x, const float* x_scale, c
   if (need > 0 && !aligned16(workspace)) return MOE_ERR_MISALIGNED;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const LinearArgs p{x, x_scale, {w, w_scale}, bias, y, T, N, K};
+  if (linear_few_ok(T, N, K)) return linear_few(p, static_cast<hipStream_t>(stream));
   const Plan pl = plan_of(T, N, K);
   float* const sums = static_cast<float*>(workspace);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  switch (pl.tt) {
-    case 16: launch_tiles<16>(p, pl, sums, s); break;
-    case 32: launch_tiles<32>(p, pl, sums, s); break;
-    case 64: launch_tiles<64>(p, pl, sums, s); break;
-    case 128: launch_tiles<128>(p, pl, sums, s); break;
-    default: launch_tiles<256>(p, pl, sums, s);
+  switch (pl.kind) {
+    case 0: launch_tiles<0>(p, pl, sums, s); break;
+    case 1: launch_tiles<1>(p, pl, sums, s); break;
+    case 2: launch_tiles<2>(p, pl, sums, s); break;
+    case 3: launch_tiles<3>(p, pl, sums, s); break;
+    case 4: launch_tiles<4>(p, pl, sums, s); break;
+    default: launch_tiles<5>(p, pl, sums, s);
   }
   if (pl.splits > 1) {
     const size_t quads = (size_t)T * ((N + 3) / 4);
-    linear_join_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(p, pl.row_tiles * kTileRows, pl.splits, sums);
+    linear_join_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(p, pl.row_tiles * kKinds[pl.kind].rows, pl.splits, sums);
   }
   return launch_status();
 }

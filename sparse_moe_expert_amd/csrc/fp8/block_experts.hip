@@ -3,6 +3,7 @@
 //   h_r = SiLU(Wg_e x_t) * (Wu_e x_t) in fp32, then in 8 bits by blocks of 128
 //   o_r = Wd_e h_r
 //   y_t = bf16( sum_j w[t,j] o_(t,j) ), in slot order
+#include "block_few.h"
 #include "block_tile.h"
 
 namespace moe {
@@ -10,6 +11,9 @@ namespace {
 
 constexpr int kFfnThreads = 256;
 constexpr int kPlanThreads = 1024;
+
+// Up to so many tokens there is no plan: the chosen experts are the items
+constexpr int kUnplanned = 128;
 
 struct FfnArgs {
   const uint8_t* x;
@@ -53,11 +57,11 @@ __device__ __forceinline__ int wave_scan(int v) {
 // to `size` routes, between half a tile and a whole one, chosen so that the
 // workgroups' longest run of gate/up tiles takes the least loads: `size` token
 // rows and 256 weight rows a step.  (T = 2000 4096x2048 of 16 experts: gate/up
-// 150 us with whole tiles,  so.)
+// 127 us with whole tiles, 123 so, down 76 and 71.)
 //
 // The other workgroups copy the tokens' scales to bucket positions, a block of H
 // together: of [T, blocks] the tiles would fetch a cache line for each four
-// bytes (T = 4096 2048x512 of 512 experts: gate/up 257 us, and  so).
+// bytes (T = 4096 2048x512 of 512 experts: gate/up 257 us, and 231 so).
 constexpr int kScaleRows = 64;               // positions a workgroup
 
 template <int TT>
@@ -107,18 +111,27 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(FfnArgs p, int row_t
 struct Item {
   int expert, first, toks;
 };
-// (through the scalar cache: a vector load would wait for the loads in flight)
-template <class V>
-__device__ __forceinline__ V scalar_load(const V* at) {
-  return *(const __attribute__((address_space(4))) V*)(uintptr_t)at;
-}
-__device__ __forceinline__ Item item_at(const FfnArgs& p, int i) {
-  if (p.items) {
+// (through the scalar cache: vector loads would wait for the loads in flight)
+template <int TT>
+__device__ __forceinline__ Item item_at(const FfnArgs& p, int i, int pass, int& longest) {
+  if (TT > kUnplanned || p.items) {
     const i32x4 v = scalar_load(reinterpret_cast<const i32x4*>(p.items) + i);
     return {v[0], v[1], v[2]};
   }
-  const int e = scalar_load(p.active + i);
-  return {e, scalar_load(p.offset + e), scalar_load(p.count + e)};
+  const int e = scalar_load(p.active + i), count = scalar_load(p.count + e), from = pass * TT;
+  longest = max(longest, count);
+  const int rest = min(count - from, TT);
+  return {e, scalar_load(p.offset + e) + (rest > 0 ? from : 0), max(rest, 0)};
+}
+
+// Without a plan a chosen expert is an item, of up to T routes, unless a token
+// names an expert twice: what is past TT routes of an expert then takes the
+// workgroup another pass over its tiles.  Between two: the loads of the last,
+// out of range, have been written, and nobody reads its stages any more.
+__device__ __forceinline__ void next_pass() {
+  wait_loads<0>();
+  wait_lds();
+  barrier();
 }
 
 // A workgroup's tiles: a run of those of all items, an item's row tiles one
@@ -149,15 +162,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
   const int kb = blocks_of(p.H), ib = blocks_of(p.I);
   T tl;
   tl.rx = make_rsrc(p.x, (uint32_t)p.T * (uint32_t)p.H);
+  int pass = 0, longest = 0;                                 // an expert's routes, of those that were items
   int loaded = -1;                                           // the item that the loads' addresses are of
   Item item_in;
   auto begin = [&](int i) MOE_INLINE {
     const int at = run.first + i, number = at / row_tiles, tile = at - number * row_tiles;
     if (number != loaded) {
       loaded = number;
-      item_in = item_at(p, number);
-      auto token = [&](int r) MOE_INLINE { return (uint32_t)(p.src[item_in.first + min(r, item_in.toks - 1)] / p.k); };
-      tl.tokens(wave, lane, [&](int r) MOE_INLINE {
+      item_in = item_at<TT>(p, number, pass, longest);
+      auto token = [&](int r) MOE_INLINE { return (uint32_t)(p.src[item_in.first + max(min(r, item_in.toks - 1), 0)] / p.k); };
+      tl.gathered_tokens(wave, lane, [&](int r) MOE_INLINE {
         const uint32_t at = token(r) * (uint32_t)p.H;
         return r < item_in.toks ? at : kOutside;
       });
@@ -173,17 +187,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
     tl.weights(p.gate.q + row * p.H, p.up.q + row * p.H, min(kBlock, p.I - n0), p.H, wave, lane);
     tl.weight_scales(p.gate.s + scale, p.up.s + scale, kb, wave);
   };
-  begin(0);
   // The item whose sums are made.  When a tile's last step is done, the next one's
   // first kLead are issued: with more steps than that a tile, the loads are still at
   // it, and its item is theirs.
-  Item item = item_in;
-  int done = loaded;
+  Item item;
+  int done;
   auto live = [&](int i) MOE_INLINE {
     const int number = (run.first + i) / row_tiles;
     if (number != done) {
       done = number;
-      item = kb > T::kLead ? item_in : item_at(p, number);
+      item = kb > T::kLead ? item_in : item_at<TT>(p, number, pass, longest);
     }
     return item.toks > wt * T::JT * 16;
   };
@@ -192,7 +205,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
     constexpr int HT = T::HT, Q = T::Q;
     int l = lane;
     asm volatile("" : "+v"(l));                              // (addresses are made here, and not kept through the loop)
-    const int g = l >> 4;
+    const int g = l >> 4, n = n0 + T::group_of(wr, 0) + g * (4 * Q);
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {
       float h[4 * HT];
@@ -202,7 +215,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
         h[i] = a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)) * tl.acc[i / 4 + HT][j][i % 4];
         tl.acc[i / 4][j][i % 4] = h[i];
       }
-      uint32_t top = largest(h);
+      uint32_t top = n < p.I ? largest(h) : 0u;              // (rows past I are not its)
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
       if (g == 0) s_max[wr * TT + (wt * T::JT + j) * 16 + l] = top;
@@ -212,7 +225,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
     // every lane stores, those past the item's routes or I out of range
     const __amdgpu_buffer_rsrc_t to_q = make_rsrc(p.hq + (size_t)first * p.I, (uint32_t)toks * (uint32_t)p.I);
     const __amdgpu_buffer_rsrc_t to_s = make_rsrc(p.hs + (size_t)tile * p.T * p.k + first, (uint32_t)toks * 4u);
-    const int n = n0 + T::group_of(wr, 0) + g * (4 * Q);
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {
       const int r = (wt * T::JT + j) * 16 + (l & 15);
@@ -232,7 +244,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
       else __builtin_amdgcn_raw_buffer_store_b32(c[0], to_q, at, 0, 0);
     }
   };
-  tl.template run<false, false, 2 * T::JT>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.H, begin, end, live);
+  for (;; ++pass, next_pass()) {
+    loaded = -1;
+    begin(0);
+    item = item_in, done = loaded;
+    tl.template run<false, false, 2 * T::JT>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.H, begin, end, live);
+    if (TT > kUnplanned || longest <= (pass + 1) * TT) break;
+  }
 }
 
 // o of 256 rows of an item's routes
@@ -247,15 +265,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
   if (run.tiles == 0) return;
   const int kb = blocks_of(p.I), hb = blocks_of(p.H);
   T tl;
+  int pass = 0, longest = 0;                                 // an expert's routes, of those that were items
   int loaded = -1;                                           // the item that the loads' addresses are of
   Item item_in;
   auto begin = [&](int i) MOE_INLINE {
     const int at = run.first + i, number = at / row_tiles, n0 = (at - number * row_tiles) * kTileRows;
     if (number != loaded) {
       loaded = number;
-      item_in = item_at(p, number);
+      item_in = item_at<TT>(p, number, pass, longest);
       tl.rx = make_rsrc(p.hq + (size_t)item_in.first * p.I, (uint32_t)item_in.toks * (uint32_t)p.I);
-      tl.tokens(wave, lane, [&](int r) { return r < item_in.toks ? (uint32_t)r * (uint32_t)p.I : kOutside; });
+      tl.tokens(p.I, wave, lane);
       tl.token_scales(p.hs + item_in.first, (uint32_t)item_in.toks * 4u, (size_t)p.T * p.k * 4, wave, lane,
                       [](int r) { return (uint32_t)r * 4u; });
     }
@@ -265,17 +284,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
     const float* const sw = p.down.s + ((size_t)item_in.expert * hb + n0 / kBlock) * (size_t)kb;
     tl.weight_scales(sw, rows > kBlock ? sw + kb : sw, kb, wave);
   };
-  begin(0);
   // The item whose sums are made.  When a tile's last step is done, the next one's
   // first kLead are issued: with more steps than that a tile, the loads are still at
   // it, and its item is theirs.
-  Item item = item_in;
-  int done = loaded;
+  Item item;
+  int done;
   auto live = [&](int i) MOE_INLINE {
     const int number = (run.first + i) / row_tiles;
     if (number != done) {
       done = number;
-      item = kb > T::kLead ? item_in : item_at(p, number);
+      item = kb > T::kLead ? item_in : item_at<TT>(p, number, pass, longest);
     }
     return item.toks > wt * T::JT * 16;
   };
@@ -283,8 +301,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
     const int n0 = (run.first + i) % row_tiles * kTileRows, first = item.first, toks = item.toks;
     // Each route's 128 outputs over the power of two that puts the largest
     // between 2^14 and 2^15: fp16 then keeps 11 bits of every output down to 2^-28
-    // of it.  o in fp32 would be twice the bytes (T = 4096 2048x512 of 512 experts,
-    // 335 MB written and read again:  us in place of ).
+    // of it, and loses it below 2^-40.  o in fp32 would be twice the bytes: of T =
+    // 4096 2048x512 of 512 experts 168 MB more, written and read again.
     int l = lane;
     asm volatile("" : "+v"(l));                              // (addresses are made here, and not kept through the loop)
     const int g = l >> 4;
@@ -293,6 +311,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
       float v[4 * T::MT];
 #pragma unroll
       for (int i = 0; i < 4 * T::MT; ++i) v[i] = tl.acc[i / 4][j][i % 4];
+#pragma unroll
+      for (int m = 0; m < T::MT; m += T::Q) {                // (rows past H are not its)
+        if (n0 + T::group_of(wr, m) + g * (4 * T::Q) < p.H) continue;
+#pragma unroll
+        for (int i = 0; i < 4 * T::Q; ++i) v[4 * m + i] = 0.0f;
+      }
       uint32_t top = largest(v);
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
@@ -332,7 +356,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
       }
     }
   };
-  tl.template run<false, false, (1 + T::MT / 2) * T::JT>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.I, begin, end, live);
+  for (;; ++pass, next_pass()) {
+    loaded = -1;
+    begin(0);
+    item = item_in, done = loaded;
+    tl.template run<false, false, (1 + T::MT / 2) * T::JT>(stage_at, wave, wr, wt, lane, 0, kb, run.tiles, p.I, begin, end, live);
+    if (TT > kUnplanned || longest <= (pass + 1) * TT) break;
+  }
 }
 
 // A thread to eight outputs of a token
@@ -371,9 +401,64 @@ __global__ __launch_bounds__(kFfnThreads) void combine_kernel(FfnArgs p) {
                  to_bf16(v[4]) | to_bf16(v[5]) << 16, to_bf16(v[6]) | to_bf16(v[7]) << 16);
 }
 
-// Tokens of a tile; up to that many the experts themselves are the items
+// Few routes: 16 outputs of every token.  A wave takes the chosen experts in
+// turn, all of an expert's reduction at once; the routes' sums meet in LDS, where
+// a token's are added in slot order.
+constexpr int kDownWaves = 16;
+constexpr int kDownThreads = kDownWaves * kWave;
+constexpr int kDownRoutes = 512;             // most, of up to 16 tokens
+
+__global__ __launch_bounds__(kDownThreads, 4) void down_combine_kernel(FfnArgs p) {
+  __shared__ float s_o[kDownRoutes][17];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4, n0 = (int)blockIdx.x * 16;
+  const int R = p.T * p.k, kb = blocks_of(p.I), hb = blocks_of(p.H), active = scalar_load(p.n_active);
+  for (int a = wave; a < active; a += kDownWaves) {
+    const int e = scalar_load(p.active + a), first = scalar_load(p.offset + e), count = scalar_load(p.count + e);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.down.q + ((size_t)e * p.H + n0) * (size_t)p.I, 16u * (uint32_t)p.I);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.hq, (uint32_t)R * (uint32_t)p.I);
+    const float* const sw = p.down.s + ((size_t)e * hb + n0 / kBlock) * (size_t)kb;
+    for (int c0 = 0; c0 < count; c0 += 16) {                 // (more than 16 where a token names an expert twice)
+      const int r = first + min(c0 + l16, count - 1);
+      f32x4 sum{};
+      constexpr int kAhead = 4;                              // blocks whose loads are in flight together
+      for (int b0 = 0; b0 < kb; b0 += kAhead) {
+        i32x8 w[kAhead], x[kAhead];
+        float s[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          w[i] = load_block(rw, (uint32_t)(l16 * p.I), b0 + i, p.I, g);
+          x[i] = load_block(rx, (uint32_t)(r * p.I), b0 + i, p.I, g);
+          const int b = min(b0 + i, kb - 1);
+          s[i] = p.hs[(size_t)b * R + r] * scalar_load(sw + b);
+        }
+        __builtin_amdgcn_sched_barrier(0);                   // (all loads first)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (b0 + i >= kb) break;
+          const f32x4 d = block_product(w[i], x[i]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sum[c] = fmaf(d[c], s[i], sum[c]);
+        }
+      }
+      if (c0 + l16 < count) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s_o[r][g * 4 + c] = sum[c];
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < p.T * 16; i += kDownThreads) {
+    const int t = i / 16, n = i % 16;
+    float v = 0.0f;
+    for (int j = 0; j < p.k; ++j) v = fmaf(p.topk_w[t * p.k + j], s_o[p.pos[t * p.k + j]][n], v);
+    p.y[(size_t)t * p.H + n0 + n] = (uint16_t)to_bf16(v);
+  }
+}
+
+// Tokens of a tile
 int tile_tokens(int T, int E, int k) {
-  if (T <= 128) return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  if (T <= kUnplanned) return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   return (long long)T * k >= 128ll * E ? 256 : 128;
 }
 // Most items that R routes can make, in pieces of half a tile or more
@@ -391,7 +476,12 @@ void launch_products(const FfnArgs& p, int items, hipStream_t s) {
     return (unsigned)(tiles < most ? tiles : most);
   };
   gate_up_kernel<TT><<<grid(up), kTileThreads, 0, s>>>(p, up);
-  down_kernel<TT><<<grid(down), kTileThreads, 0, s>>>(p, down);
+  if constexpr (TT == 16) {
+    down_combine_kernel<<<(unsigned)p.H / 16, kDownThreads, 0, s>>>(p);
+  } else {
+    down_kernel<TT><<<grid(down), kTileThreads, 0, s>>>(p, down);
+    combine_kernel<<<(unsigned)(((size_t)p.T * (p.H / 8) + kFfnThreads - 1) / kFfnThreads), kFfnThreads, 0, s>>>(p);
+  }
 }
 
 inline bool ffn_dims_ok(int T, int H, int I, int E, int k) {
@@ -410,7 +500,7 @@ extern "C" size_t moe_block_expert_ffn_workspace_size(int T, int H, int I, int E
   if (T <= 0 || !ffn_dims_ok(T, H, I, E, k) || !ffn_dims_fit(T, H, I, E, k)) return 0;
   const size_t R = (size_t)T * (size_t)k;
   return align256(R * I) + align256(R * blocks_of(I) * 4) + align256(R * H * 2) + align256(R * blocks_of(H) * 4) +
-         (T > 128 ? align256((size_t)most_items(R, E, 128) * sizeof(int4)) + 256 + align256(R * blocks_of(H) * 4) : 0);
+         (T > kUnplanned ? align256((size_t)most_items(R, E, 128) * sizeof(int4)) + 256 + align256(R * blocks_of(H) * 4) : 0);
 }
 
 extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scale, const uint8_t* w_gate,
@@ -444,7 +534,7 @@ extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scal
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int tt = tile_tokens(T, E, k);
   int items = (int)(R < (size_t)E ? R : (size_t)E);
-  if (T > tt) {
+  if (T > kUnplanned) {
     items = most_items(R, E, tt);
     p.items = reinterpret_cast<int4*>(take((size_t)items * sizeof(int4)));
     p.n_items = reinterpret_cast<int*>(take(4));
@@ -460,6 +550,5 @@ extern "C" moe_status moe_block_expert_ffn(const uint8_t* x, const float* x_scal
     case 128: launch_products<128>(p, items, s); break;
     default: launch_products<256>(p, items, s);
   }
-  combine_kernel<<<(unsigned)(((size_t)T * (H / 8) + kFfnThreads - 1) / kFfnThreads), kFfnThreads, 0, s>>>(p);
   return launch_status();
 }

@@ -1,7 +1,7 @@
-// The products of a tile: 256 weight rows (of a gate/up pair 128 of each) by TT
+// The products of a tile: ROWS weight rows (of a gate/up pair 128 of each) by TT
 // tokens, by a workgroup of eight waves.
 //
-// Tokens, weights and scales go straight to LDS (buffer_load ... lds), a block
+// Tokens, weights and scales go straight to LDS (buffer_load ... lds), U blocks
 // of 128 of the reduction a step, in a ring of NS stages.  A row's step is 128
 // bytes, its 16-byte chunks permuted so that the reads of 16 lanes, one chunk of
 // the 16 rows of a product, hit all banks.  The rows of Q products are
@@ -63,25 +63,31 @@ struct Stage {
   uint8_t* x;
 };
 
-template <int TT, bool PAIR>
+// ROWS: weight rows of the tile (256 of a pair, 128 of each matrix); U: blocks of
+// the reduction a step
+template <int TT, bool PAIR, int ROWS = kTileRows, int U = 1>
 struct Tile {
-  static constexpr int WR = TT == 256 ? 2 : TT == 16 ? 8 : 4, WT = 8 / WR;
-  static constexpr int MT = kTileRows / WR / 16, JT = TT / WT / 16;        // row tiles, token tiles a wave
+  static constexpr int WR = TT == ROWS ? 2 : TT == 16 ? 8 : 4, WT = 8 / WR;
+  static constexpr int MT = ROWS / WR / 16, JT = TT / WT / 16;        // row tiles, token tiles a wave
   static constexpr int HT = PAIR ? MT / 2 : MT, Q = HT < 4 ? HT : 4;       // row tiles of one matrix, interleaved ones
-  static constexpr int kWeightBytes = kTileRows * kBlock, kTokenBytes = TT * kBlock;
+  static constexpr int kWeightBytes = U * ROWS * kBlock, kTokenBytes = U * TT * kBlock;
   static constexpr int kScaleGroups = (TT + 63) / 64 + 2;                  // 64 of the tokens' scales each, and the weights'
-  static constexpr int kScaledBytes = kWeightBytes + kScaleGroups * 256;   // the weights and all scales
+  static constexpr int kScaledBytes = kWeightBytes + U * kScaleGroups * 256;         // the weights and all scales
   static constexpr int kFit = 160 * 1024 / (kScaledBytes + kTokenBytes), NS = kFit < 4 ? kFit : 4, kLead = NS - 1;
-  static constexpr int XL = TT < 64 ? 1 : TT / 64;                         // a wave's token loads a step
-  static constexpr int kLoads = 4 + 1 + XL;
-  static_assert(NS >= 2 && (kLead - 1) * kLoads < 64, "two stages or more");
+  static constexpr int WL = U * ROWS / 64, XL = U * TT < 64 ? 1 : U * TT / 64;       // a wave's loads of 1 KB a step
+  static constexpr int kLoads = WL + 1 + XL;
+  static constexpr uint32_t kStep = U * kBlock, kNoStep = kOutside / kStep;          // a step's bytes of a row; one past all
+  static_assert(NS >= 2 && (kLead - 1) * kLoads < 48, "two stages or more, and stores behind the loads");
+  static_assert(U * kScaleGroups <= 8 && (ROWS == kTileRows || !PAIR), "one load of scales a wave");
 
   __amdgpu_buffer_rsrc_t rw, rx;             // the wave's weight rows, the tokens
   const float* s_from;                       // the wave's scales
   uint32_t s_bytes;
   size_t s_stride;
-  uint32_t w_off[4], x_off[XL], s_off;
+  uint32_t w_off[WL], s_off;
+  uint32_t x_off[PAIR ? XL : 1], x_row;      // of a pair's tokens, gathered; else of the first piece's, 64 rows apart
   uint32_t token_at, scale_at;               // where a wave's first token piece and its scales go
+  int scale_block;                           // the block of the step that its scales are of
   f32x4 acc[MT][JT];
 
   // Row of the tile (of a pair: in the 128 of either matrix, the second's from
@@ -100,29 +106,38 @@ struct Tile {
   static __device__ __forceinline__ int mix(int r) { return ((r >> 1) & 1) | (r / (4 * Q) & 3) << 1; }
   static __device__ __forceinline__ int token_mix(int r) { return (r >> 1) & 7; }
 
-  // The wave's loads.  Weight piece i: 8 rows from (wave * 4 + i) * 8 on.
+  // The wave's pieces, of 8 rows of a block each: the step's blocks one after another
+  static __device__ __forceinline__ int weight_piece(int i, int wave) { return wave * WL + i; }
+  static __device__ __forceinline__ int token_piece(int i, int wave) { return U * TT < 64 ? wave % (U * TT / 8) : i * 8 + wave; }
+
   // `first`, `second`: a pair's matrices from the tile's first row on, of which
-  // there are `rows` (those past them repeat the last); else the first alone.
+  // there are `rows` (those past them are out of range); else the first alone.
   __device__ __forceinline__ void weights(const uint8_t* first, const uint8_t* second, int rows, int K, int wave, int lane) {
     const bool other = PAIR && wave >= 4;
     rw = make_rsrc(other ? second : first, (uint32_t)rows * (uint32_t)K);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = (wave * 4 + i) * 8 + (lane >> 3), c = (lane & 7) ^ mix(r);
-      const int in = PAIR ? r & 127 : r;
-      w_off[i] = (uint32_t)min(in, rows - 1) * (uint32_t)K + (uint32_t)c * 16u;
+    for (int i = 0; i < WL; ++i) {
+      const int q = weight_piece(i, wave), r = q % (ROWS / 8) * 8 + (lane >> 3), c = (lane & 7) ^ mix(r);
+      w_off[i] = (uint32_t)(PAIR ? r & 127 : r) * (uint32_t)K + (uint32_t)(q / (ROWS / 8) * kBlock + c * 16);
     }
   }
-  // Token row r's place in the tile's token loads: f(r) is its offset
+  // A pair's token row r: f(r) is its offset
   template <class F>
-  __device__ __forceinline__ void tokens(int wave, int lane, F&& f) {
+  __device__ __forceinline__ void gathered_tokens(int wave, int lane, F&& f) {
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
-      const int piece = TT < 64 ? wave % (TT / 8) : i * 8 + wave;          // 8 rows each
-      const int r = piece * 8 + (lane >> 3), c = (lane & 7) ^ token_mix(r);
-      x_off[i] = f(r) + (uint32_t)c * 16u;
+      const int q = token_piece(i, wave), r = q % (TT / 8) * 8 + (lane >> 3), c = (lane & 7) ^ token_mix(r);
+      x_off[i] = f(r) + (uint32_t)(c * 16);
     }
-    token_at = (TT < 64 ? wave % (TT / 8) : wave) * 1024u;
+    token_at = token_piece(0, wave) * 1024u;
+  }
+  // Else rows of K bytes, from the start of rx on, which ends behind the last
+  __device__ __forceinline__ void tokens(int K, int wave, int lane) {
+    const int q = token_piece(0, wave), r = q % (TT / 8) * 8 + (lane >> 3), c = (lane & 7) ^ token_mix(r);
+    x_off[0] = (uint32_t)r * (uint32_t)K + (uint32_t)(q / (TT / 8) * kBlock + c * 16);
+    x_row = U > 1 ? kBlock : 64u * (uint32_t)K;              // (U > 1: a wave's pieces are of the same rows)
+    static_assert(U == 1 || XL == 1 || (U == 2 && TT == 64), "");
+    token_at = q * 1024u;
   }
 
   // A wave's 64 scales of a step: of tokens, at `first` + step * stride bytes, f(r)
@@ -130,8 +145,9 @@ struct Tile {
   // or of the second.
   template <class F>
   __device__ __forceinline__ void token_scales(const float* first, uint32_t bytes, size_t stride, int wave, int lane, F&& f) {
-    const int group = wave % kScaleGroups;
-    scale_at = kWeightBytes + group * 256u;
+    const int id = wave % (U * kScaleGroups), group = id % kScaleGroups;
+    scale_block = id / kScaleGroups;
+    scale_at = kWeightBytes + id * 256u;
     s_off = 0;
     if (group < kScaleGroups - 2) {
       s_from = first, s_bytes = bytes, s_stride = stride;
@@ -139,45 +155,43 @@ struct Tile {
     }
   }
   __device__ __forceinline__ void weight_scales(const float* first, const float* second, int kb, int wave) {
-    const int group = wave % kScaleGroups;
+    const int group = wave % (U * kScaleGroups) % kScaleGroups;
     if (group >= kScaleGroups - 2)
       s_from = group == kScaleGroups - 2 ? first : second, s_bytes = (uint32_t)kb * 4u, s_stride = 4;
   }
 
-  // Load i (a constant) of a step: its weights, scales, then tokens
-  __device__ __forceinline__ void issue_scaled(int i, uint8_t* w, int wave, uint32_t step) {
-    if (i < 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, w + (wave * 4 + i) * 1024, 16, w_off[i] + step * kBlock, 0, 0, 0);
-    else {
-      const bool none = step >= kOutside / kBlock;
-      const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<const uint8_t*>(s_from) + (none ? 0 : step * s_stride), s_bytes);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, w + scale_at, 4, none ? kOutside : s_off, 0, 0, 0);
-    }
-  }
-  __device__ __forceinline__ void issue_token(int i, uint8_t* x, uint32_t step) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, x + token_at + i * 8192, 16, x_off[i] + step * kBlock, 0, 0, 0);
-  }
-  __device__ __forceinline__ void issue_weights(uint8_t* w, int wave, uint32_t step) {
+  __device__ __forceinline__ void issue(const Stage& stage, int wave, uint32_t step) {
 #pragma unroll
-    for (int i = 0; i < 5; ++i) issue_scaled(i, w, wave, step);
+    for (int i = 0; i < XL; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, stage.x + token_at + i * 8192, 16,
+                                               (PAIR ? x_off[PAIR ? i : 0] : x_off[0] + (uint32_t)i * x_row) + step * kStep, 0, 0, 0);
     fence();
-  }
-  __device__ __forceinline__ void issue_tokens(uint8_t* x, uint32_t step) {
 #pragma unroll
-    for (int i = 0; i < XL; ++i) issue_token(i, x, step);
+    for (int i = 0; i < WL; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, stage.w + weight_piece(i, wave) * 1024, 16, w_off[i] + step * kStep, 0, 0, 0);
+    const bool none = step >= kNoStep;
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(reinterpret_cast<const uint8_t*>(s_from) + (none ? 0 : (step * U + scale_block) * s_stride), s_bytes);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, stage.w + scale_at, 4, none ? kOutside : s_off, 0, 0, 0);
     fence();
   }
 
-  // What follows a row's last value in its last step is not its: zero, in the
-  // pieces that this wave loaded (chunks from `from` on)
-  __device__ __forceinline__ void clear_tail(const Stage& stage, int wave, int lane, int from) {
-    auto clear = [&](uint8_t* piece, int by) {
-      if (((lane & 7) ^ by) >= from) *reinterpret_cast<uint4*>(piece + lane * 16) = make_uint4(0, 0, 0, 0);
+  // What follows a row's last value, `rest` from the step's first, is not its:
+  // zero, in the pieces that this wave loaded
+  __device__ __forceinline__ void clear_tail(const Stage& stage, int wave, int lane, int rest) {
+    auto clear = [&](uint8_t* piece, int block, int by) {
+      if (((lane & 7) ^ by) * 16 >= rest - block * kBlock) *reinterpret_cast<uint4*>(piece + lane * 16) = make_uint4(0, 0, 0, 0);
     };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) clear(stage.w + (wave * 4 + i) * 1024, mix((wave * 4 + i) * 8 + (lane >> 3)));
+    for (int i = 0; i < WL; ++i) {
+      const int q = weight_piece(i, wave);
+      clear(stage.w + q * 1024, q / (ROWS / 8), mix(q % (ROWS / 8) * 8 + (lane >> 3)));
+    }
 #pragma unroll
-    for (int i = 0; i < XL; ++i)
-      clear(stage.x + token_at + i * 8192, token_mix((TT < 64 ? wave % (TT / 8) : i * 8 + wave) * 8 + (lane >> 3)));
+    for (int i = 0; i < XL; ++i) {
+      const int q = token_piece(i, wave);
+      clear(stage.x + token_at + i * 8192, q / (TT / 8), token_mix(q % (TT / 8) * 8 + (lane >> 3)));
+    }
   }
 
   static __device__ __forceinline__ i32x8 read(const uint8_t* rows, int r, int x, int g) {
@@ -186,20 +200,22 @@ struct Tile {
                     *reinterpret_cast<const i32x4*>(row + (((g + 4) ^ x) << 4)));
   }
 
-  // One step's products
-  __device__ __forceinline__ void products(const Stage& stage, int wr, int wt, int lane) {
+  // The products of block u of a step
+  __device__ __forceinline__ void products(const Stage& stage, int u, int wr, int wt, int lane) {
     const int l16 = lane & 15, g = lane >> 4;
-    const float* const scales = reinterpret_cast<const float*>(stage.w + kWeightBytes);
+    const uint8_t* const weights = stage.w + u * (ROWS * kBlock);
+    const uint8_t* const tokens = stage.x + u * (TT * kBlock);
+    const float* const scales = reinterpret_cast<const float*>(stage.w + kWeightBytes + u * kScaleGroups * 256);
     const float* const sw = scales + (kScaleGroups - 2) * 64;
     const float s0 = PAIR || wr * MT < 8 ? sw[0] : sw[64], s1 = PAIR ? sw[64] : s0;
     i32x8 b[JT], a[2];
     float s[2][JT];
     const int by = (l16 >> 1 & 1) | (l16 >> 2) << 1;         // mix(row_of(...))
-    a[0] = read(stage.w, row_of(wr, 0, l16), by, g);
+    a[0] = read(weights, row_of(wr, 0, l16), by, g);
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
       const int r = (wt * JT + j) * 16 + l16;
-      b[j] = read(stage.x, r, token_mix(r), g);
+      b[j] = read(tokens, r, token_mix(r), g);
       s[0][j] = scales[r];
     }
 #pragma unroll
@@ -207,12 +223,13 @@ struct Tile {
       if constexpr (PAIR) s[1][j] = s[0][j] * s1;
       s[0][j] *= s0;
     }
+    // (4096^3: 69.6 us with 3, 72.1 with 2, 75.4 with 1)
     constexpr int kDelay = 3, kAll = MT * JT;
     f32x4 d[kDelay + 1];
     for_each<kAll + kDelay>([&](auto n_c) MOE_INLINE {
       constexpr int n = decltype(n_c)::value, q = n - kDelay;
       if constexpr (n < kAll) {
-        if constexpr (n % JT == 0 && n / JT + 1 < MT) a[(n / JT + 1) % 2] = read(stage.w, row_of(wr, n / JT + 1, l16), by, g);
+        if constexpr (n % JT == 0 && n / JT + 1 < MT) a[(n / JT + 1) % 2] = read(weights, row_of(wr, n / JT + 1, l16), by, g);
         d[n % (kDelay + 1)] = block_product(a[n / JT % 2], b[n % JT]);
       }
       if constexpr (q >= 0) {
@@ -232,7 +249,7 @@ struct Tile {
       for (int j = 0; j < JT; ++j) acc[m][j] = f32x4{};
   }
 
-  // `tiles` tiles of `steps` steps each, from block `first` of the reduction on,
+  // `tiles` tiles of `steps` steps each, from step `first` of the reduction on,
   // as one stream: while a tile's last steps are multiplied the next one's first
   // are on their way.  begin(i) sets the loads to tile i (0 is set before);
   // end(i) finishes tile i's sums; live(i): whether this wave has any of its tokens
@@ -243,10 +260,8 @@ struct Tile {
                                       Begin&& begin, End&& end, Live&& live) {
     int in = 0, tile_in = 0;                                 // the next loads' step and tile
     // past the last tile they are issued out of range: they read nothing
-    auto issue = [&](const Stage& stage) MOE_INLINE {
-      const uint32_t at = tile_in < tiles ? (uint32_t)(first + in) : kOutside / kBlock;
-      issue_tokens(stage.x, at);
-      issue_weights(stage.w, wave, at);
+    auto load = [&](const Stage& stage) MOE_INLINE {
+      issue(stage, wave, tile_in < tiles ? (uint32_t)(first + in) : kNoStep);
       ++in;
       if (ONE) {
         if (in == steps) tile_in = 1;
@@ -255,7 +270,7 @@ struct Tile {
         if (++tile_in < tiles) begin(tile_in);
       }
     };
-    for_each<kLead>([&](auto s) MOE_INLINE { issue(stage_at(s)); });
+    for_each<kLead>([&](auto s) MOE_INLINE { load(stage_at(s)); });
     clear_sums();
     int out = 0, tile_out = 0;
     bool here = ALL || live(0);
@@ -265,13 +280,17 @@ struct Tile {
       // this wave's loads of the step have landed (loads and stores end in order)
       if (!ONE && out == 0 && tile_out > 0) wait_loads<(kLead - 1) * kLoads + STORES>();
       else wait_loads<(kLead - 1) * kLoads>();
-      const int rest = K - (first + out) * kBlock;
-      if (rest < kBlock) clear_tail(stage, wave, lane, rest / 16);
+      const int rest = K - (first + out) * (int)kStep;
+      if (rest < (int)kStep) clear_tail(stage, wave, lane, rest);
       wait_lds();                                            // and its reads of the step before returned
       barrier();
       // (spread between the products instead, they end later: 4096^3 65.0 us, and 66.5)
-      issue(stage_at(std::integral_constant<int, (S + kLead) % NS>{}));
-      if (ALL || here) products(stage, wr, wt, lane);
+      load(stage_at(std::integral_constant<int, (S + kLead) % NS>{}));
+      if (ALL || here) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (u == 0 || rest > u * kBlock) products(stage, u, wr, wt, lane);
+      }
       ++out;
       if (!ONE && out == steps) {
         out = 0;

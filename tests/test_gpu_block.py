@@ -144,6 +144,9 @@ LINEAR = [
     (4, 40, 12288), (4, 30, 32768), (600, 6500, 80), (513, 8200, 144), (300, 16390, 64), (20, 33, 16384), (17, 1000, 4128),
     (60, 700, 8192), (130, 2600, 4160), (24, 130, 32752), (512, 640, 640), (16, 30, 32768), (700, 11000, 96),
     (1025, 4100, 160), (33000, 260, 32), (650, 5000, 640), (1300, 4090, 1152), (256, 4096, 384), (2050, 2049, 272),
+    # each kind of tile with odd sizes and a long reduction, whole and in parts
+    (1, 9999, 4096), (12, 8200, 656), (16, 16385, 2064), (821, 9429, 1680), (2212, 1982, 1584), (69, 9536, 5600),
+    (93, 9870, 1520), (451, 2055, 1504), (1725, 74, 7552), (40, 8235, 1632), (2872, 681, 1680), (419, 527, 7808), (2132, 8, 7008),
 ]
 
 
@@ -276,6 +279,24 @@ def test_ffn_nonfinite(T, H, I, E, k):  # noqa: E741
     assert torch.isnan(y[bad].float()).any(dim=1).all()
 
 
+@pytest.mark.parametrize("T,H,I,E,k,top", [(3, 256, 144, 8, 8, 1), (16, 144, 272, 32, 32, 2), (16, 512, 128, 5, 4, 3), (20, 256, 256, 4, 4, 1),
+                                           (60, 272, 144, 16, 9, 2), (128, 128, 640, 8, 5, 1), (128, 640, 128, 70, 32, 64),
+                                           (129, 256, 144, 3, 3, 1), (300, 272, 256, 6, 5, 2)])
+def test_ffn_expert_twice(T, H, I, E, k, top):  # noqa: E741
+    """Tokens that name an expert more than once: up to T * k routes of one expert."""
+    rng = np.random.default_rng(T + top)
+    x, gate, up, down, _, w, _ = ffn_case(rng, T, H, I, E, k, 0)
+    idx = (rng.integers(0, top, (T, k)) * (E // top)).astype(np.int32)
+    out = torch.full((T + 2, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = sme.make_block_ffn_workspace(T, H, I, E, k, DEV)
+    ws.fill_(0xFF)
+    y = sme.moe_block_expert_ffn(dev_tokens(x), dev_experts(gate, up, down), dev(w), sme.moe_bucket_routes(dev(idx), E), ws, out[:T])
+    deq = oracle.block.weight
+    ref, tol = ffn_reference(oracle.block.tokens(*x), deq(*gate), deq(*up), deq(*down), idx, w)
+    assert_near(as_f64(y), ref, tol, (T, H, I, E, k, top))
+    assert torch.all(out[T:] == 7.0)
+
+
 def test_ffn_zero_weights():
     """Routes of weight zero and tokens of zeros: exactly zero."""
     rng = np.random.default_rng(3)
@@ -384,6 +405,48 @@ def test_graph_replays():
         assert same_bits(r2, res_out) and same_bits(p2, p) and same_bits(y2, y)
 
 
+def test_graphs_share_workspaces():
+    """Graphs of different sizes with one pair of workspaces, of the largest's size, replayed in turn."""
+    rng = np.random.default_rng(10)
+    H, I, E, k, sizes = 2048, 144, 12, 3, (300, 4, 40, 130)  # noqa: E741
+    gate, up, down = random_weight(rng, E, I, H), random_weight(rng, E, I, H), random_weight(rng, E, H, I)
+    experts, lin = dev_experts(gate, up, down), dev_weight(random_weight(rng, 70, H))
+    ws, lws = sme.make_block_ffn_workspace(max(sizes), H, I, E, k, DEV), sme.make_block_linear_workspace(DEV)
+    ws.fill_(0xFF)
+    lws.fill_(0xFF)
+    held = []
+    for T in sizes:
+        _, w, b = routes(rng, T, E, k)
+        held.append([torch.zeros((T, H), dtype=torch.bfloat16, device=DEV), sme.empty_fp8_tokens(T, H, DEV), dev(w), b,
+                     torch.empty((T, 70), dtype=torch.bfloat16, device=DEV), torch.empty((T, H), dtype=torch.bfloat16, device=DEV)])
+
+    def run(x, tokens, w, b, p, y):
+        sme.moe_block_quantize(x, tokens)
+        sme.moe_block_linear(tokens, lin, None, p, lws)
+        sme.moe_block_expert_ffn(tokens, experts, w, b, ws, y)
+
+    graphs = []
+    for h in held:
+        run(*h)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            run(*h)
+    for _ in range(3):
+        want = []
+        for h in held:
+            h[0].copy_(torch.from_numpy(rng.standard_normal(tuple(h[0].shape))).to(DEV, torch.bfloat16))
+            tokens = sme.moe_block_quantize(h[0])
+            want.append((sme.moe_block_linear(tokens, lin), sme.moe_block_expert_ffn(tokens, experts, h[2], h[3])))
+            h[4].fill_(0.0)
+            h[5].fill_(0.0)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for h, (p, y) in zip(held, want):
+            assert same_bits(h[4], p) and same_bits(h[5], y)
+
+
 @pytest.mark.parametrize("T", [4, 300])
 def test_two_streams(T):
     """Calls at once on streams of their own, behind work queued there, with workspaces of their own."""
@@ -459,3 +522,73 @@ def test_step(T, grouped, stream):
         layers(a, b)
         torch.cuda.synchronize()
         assert same_bits(b.y, y) and torch.equal(b.residual, r)
+
+
+# ------------------------------------------------------------------ beyond 2^31
+
+def random_codes(*shape):
+    """Random finite e4m3 codes of [0.0625, 448), either sign, made on the device."""
+    q = torch.empty(shape, dtype=torch.uint8, device=DEV)
+    for part in q.view(-1).split(1 << 30):
+        part.random_(0x20 << 1, 0x7E << 1)
+    return torch.bitwise_or(q >> 1, q << 7, out=q).view(E4M3)
+
+
+def random_scales(*shape, of):
+    return (torch.rand(shape, device=DEV) + 0.5) * of
+
+
+@pytest.mark.parametrize("T,N,K", [(2, 1 << 18, 16384), (70, 1 << 18, 16384), (300, 1 << 18, 16384), (70000, 65600, 16),
+                                   (1 << 17, 200, 32768)])
+def test_linear_beyond_32_bits(T, N, K):
+    """Weights, outputs, or tokens of more than 2^31 values (their first and last rows and some between are compared)."""
+    rng = np.random.default_rng(T)
+    torch.manual_seed(T)
+    x = sme.Fp8Tokens(random_codes(T, K), random_scales(T, blocks(K), of=1 / 256))
+    w = sme.Fp8Weight(random_codes(N, K), random_scales(blocks(N), blocks(K), of=1 / (128 * K ** 0.5)))
+    y = sme.moe_block_linear(x, w)
+    t, n = (np.unique(np.concatenate([[0, m - 1], rng.integers(0, m, 30), rng.integers(m * 7 // 8, m, 30)])) for m in (T, N))
+    dt, dn = dev(t), dev(n)
+    bytes_at = lambda q, at: q.view(torch.uint8)[at].view(E4M3)  # noqa: E731
+    hx = oracle.block.tokens(as_f64(bytes_at(x.q, dt)), x.scale[dt].cpu().numpy())
+    s = np.repeat(w.scale[dn // 128].cpu().numpy().astype(np.float64), 128, axis=1)[:, :K]
+    ref, tol = linear_reference(hx, as_f64(bytes_at(w.q, dn)) * s)
+    assert_near(as_f64(y[dt][:, dn]), ref, tol, (T, N, K))
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(3, 4096, 1040, 1024, 2), (150, 4096, 1040, 1024, 2), (1 << 18, 4096, 144, 4, 4),
+                                       (1 << 17, 144, 4224, 4, 4)])
+def test_ffn_beyond_32_bits(T, H, I, E, k):  # noqa: E741
+    """A matrix of all experts, or the routes' sums or hidden values, of more than 2^31 values."""
+    rng = np.random.default_rng(T)
+    torch.manual_seed(T)
+    x = sme.Fp8Tokens(random_codes(T, H), random_scales(T, blocks(H), of=1 / 256))
+    mats = []
+    for n, kk in ((I, H), (I, H), (H, I)):
+        mats += [random_codes(E, n, kk), random_scales(E, blocks(n), blocks(kk), of=1 / (128 * kk ** 0.5))]
+    chosen = np.array([0, E - 1])
+    idx = np.argsort(rng.standard_normal((T, E)), axis=1).astype(np.int32)[:, :k] if E == k else chosen[
+        np.argsort(rng.standard_normal((T, 2)), axis=1)].astype(np.int32)
+    w = rng.uniform(0.05, 1.0, (T, k)).astype(np.float32)
+    y = sme.moe_block_expert_ffn(x, sme.Fp8Experts(*mats), dev(w), sme.moe_bucket_routes(dev(idx), E))
+    t = np.unique(np.concatenate([[0, T - 1], rng.integers(0, T, 20), rng.integers(T * 7 // 8, T, 20)]))
+    hx = oracle.block.tokens(as_f64(x.q.view(torch.uint8)[dev(t)].view(E4M3)), x.scale[dev(t)].cpu().numpy())
+    used = np.unique(idx[t])
+    gate, up, down = ([oracle.block.weight(as_f64(mats[m].view(torch.uint8)[int(e)].view(E4M3)), mats[m + 1][int(e)].cpu().numpy())
+                       for e in used] for m in (0, 2, 4))
+    ref, tol = ffn_reference(hx, *(np.stack(m) for m in (gate, up, down)), np.searchsorted(used, idx[t]), w[t])
+    assert_near(as_f64(y[dev(t)]), ref, tol, (T, H, I, E, k))
+
+
+def test_norm_beyond_32_bits():
+    torch.manual_seed(5)
+    T, H = 140000, 16384
+    x = torch.randn((1000, H), dtype=torch.bfloat16, device=DEV).repeat(T // 1000, 1)
+    w = torch.rand(H, dtype=torch.bfloat16, device=DEV)
+    tokens, r = sme.moe_norm_quantize(x, w, x)
+    t, r1 = sme.moe_norm_quantize(x[:1000], w, x[:1000])
+    q = sme.moe_block_quantize(x)
+    q1 = sme.moe_block_quantize(x[:1000])
+    for i in (0, 65000, T - 1000):                                     # (the 131072nd row is the 2^31st value's)
+        for a, b in ((tokens.q, t.q), (tokens.scale, t.scale), (r, r1), (q.q, q1.q), (q.scale, q1.scale)):
+            assert same_bits(a[i:i + 1000], b)
