@@ -401,21 +401,39 @@ __global__ __launch_bounds__(kFfnThreads) void combine_kernel(FfnArgs p) {
                  to_bf16(v[4]) | to_bf16(v[5]) << 16, to_bf16(v[6]) | to_bf16(v[7]) << 16);
 }
 
-// Few routes: 16 outputs of every token.  A wave takes the chosen experts in
+// Few routes: ROWS outputs of every token.  A wave takes the chosen experts in
 // turn, all of an expert's reduction at once; the routes' sums meet in LDS, where
-// a token's are added in slot order.
+// a token's are added in slot order.  Bound by the weight bytes, and at one
+// workgroup a compute unit by how many of those read: 8 rows, half a product's,
+// where that many workgroups all run at once (T = 4 2048x512 of 512 experts, 40
+// chosen: 13.0 us, 15.6 with 16 rows; 2048x1024 of 64: 10.2 and 12.6; but 2304x512
+// of 256: 18.7 and 13.4).  In a launch of its own the sum took 5 us more.
 constexpr int kDownWaves = 16;
+constexpr int kDownGroups = 256;             // workgroups that run at once, one on a compute unit
 constexpr int kDownThreads = kDownWaves * kWave;
 constexpr int kDownRoutes = 512;             // most, of up to 16 tokens
 
+template <int ROWS>
 __global__ __launch_bounds__(kDownThreads, 4) void down_combine_kernel(FfnArgs p) {
-  __shared__ float s_o[kDownRoutes][17];
+  __shared__ float s_o[kDownRoutes][ROWS + 1], s_weight[kDownRoutes];
+  __shared__ int s_expert[kDownRoutes][3], s_pos[kDownRoutes];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, g = lane >> 4, n0 = (int)blockIdx.x * 16;
-  const int R = p.T * p.k, kb = blocks_of(p.I), hb = blocks_of(p.H), active = scalar_load(p.n_active);
+  const int l16 = lane & 15, g = lane >> 4, n0 = (int)blockIdx.x * ROWS;
+  const int R = p.T * p.k, kb = blocks_of(p.I), hb = blocks_of(p.H);
+  // all that the weights' addresses and the sums go by, once
+  for (int i = tid; i < R; i += kDownThreads) {
+    const int a = min(i, p.E - 1), active = *p.n_active, e = p.active[a];
+    const float weight = p.topk_w[i];
+    const int pos = p.pos[i];
+    if (a < active) s_expert[a][0] = e, s_expert[a][1] = p.offset[e], s_expert[a][2] = p.count[e];
+    s_weight[i] = weight, s_pos[i] = pos;
+  }
+  __syncthreads();
+  const int active = scalar_load(p.n_active);
   for (int a = wave; a < active; a += kDownWaves) {
-    const int e = scalar_load(p.active + a), first = scalar_load(p.offset + e), count = scalar_load(p.count + e);
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.down.q + ((size_t)e * p.H + n0) * (size_t)p.I, 16u * (uint32_t)p.I);
+    const int e = __builtin_amdgcn_readfirstlane(s_expert[a][0]), first = __builtin_amdgcn_readfirstlane(s_expert[a][1]);
+    const int count = __builtin_amdgcn_readfirstlane(s_expert[a][2]);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.down.q + ((size_t)e * p.H + n0) * (size_t)p.I, (uint32_t)(ROWS * p.I));
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.hq, (uint32_t)R * (uint32_t)p.I);
     const float* const sw = p.down.s + ((size_t)e * hb + n0 / kBlock) * (size_t)kb;
     for (int c0 = 0; c0 < count; c0 += 16) {                 // (more than 16 where a token names an expert twice)
@@ -441,17 +459,17 @@ __global__ __launch_bounds__(kDownThreads, 4) void down_combine_kernel(FfnArgs p
           for (int c = 0; c < 4; ++c) sum[c] = fmaf(d[c], s[i], sum[c]);
         }
       }
-      if (c0 + l16 < count) {
+      if (c0 + l16 < count && g * 4 < ROWS) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) s_o[r][g * 4 + c] = sum[c];
       }
     }
   }
   __syncthreads();
-  for (int i = tid; i < p.T * 16; i += kDownThreads) {
-    const int t = i / 16, n = i % 16;
+  for (int i = tid; i < p.T * ROWS; i += kDownThreads) {
+    const int t = i / ROWS, n = i % ROWS;
     float v = 0.0f;
-    for (int j = 0; j < p.k; ++j) v = fmaf(p.topk_w[t * p.k + j], s_o[p.pos[t * p.k + j]][n], v);
+    for (int j = 0; j < p.k; ++j) v = fmaf(s_weight[t * p.k + j], s_o[s_pos[t * p.k + j]][n], v);
     p.y[(size_t)t * p.H + n0 + n] = (uint16_t)to_bf16(v);
   }
 }
@@ -477,7 +495,8 @@ void launch_products(const FfnArgs& p, int items, hipStream_t s) {
   };
   gate_up_kernel<TT><<<grid(up), kTileThreads, 0, s>>>(p, up);
   if constexpr (TT == 16) {
-    down_combine_kernel<<<(unsigned)p.H / 16, kDownThreads, 0, s>>>(p);
+    if (p.H / 8 <= kDownGroups) down_combine_kernel<8><<<(unsigned)p.H / 8, kDownThreads, 0, s>>>(p);
+    else down_combine_kernel<16><<<(unsigned)p.H / 16, kDownThreads, 0, s>>>(p);
   } else {
     down_kernel<TT><<<grid(down), kTileThreads, 0, s>>>(p, down);
     combine_kernel<<<(unsigned)(((size_t)p.T * (p.H / 8) + kFfnThreads - 1) / kFfnThreads), kFfnThreads, 0, s>>>(p);
