@@ -474,10 +474,13 @@ __global__ __launch_bounds__(kDownThreads, 4) void down_combine_kernel(FfnArgs p
   }
 }
 
-// Tokens of a tile
+// Tokens of a tile.  Beyond 128 by an expert's routes on average: wide tiles need
+// fewer weight loads, narrow ones waste less (2048x512: 125 routes 72.8 us with 256,
+// 91.9 with 128, 80 routes 458 and 429; 4096x2048: 125 routes 126 and 140, 75
+// routes 121 and 116).
 int tile_tokens(int T, int E, int k) {
   if (T <= kUnplanned) return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-  return (long long)T * k >= 128ll * E ? 256 : 128;
+  return (long long)T * k >= 100ll * E ? 256 : 128;
 }
 // Most items that R routes can make, in pieces of half a tile or more
 int most_items(size_t R, int E, int tt) {
