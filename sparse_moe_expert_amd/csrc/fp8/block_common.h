@@ -37,7 +37,6 @@ struct BlockMat {
   const float* s;          // [blocks of N, blocks of K]
 };
 
-inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 namespace {

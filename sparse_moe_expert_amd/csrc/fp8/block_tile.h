@@ -11,6 +11,11 @@
 // each product followed, three products later, by the four multiply-adds that
 // scale it onto the sums: the matrix pipe and the vector pipe then work side by
 // side.
+//
+// What bounds it: of 4096^3 a step of 256 x 256 takes 1.2 us with its loads left
+// out, 1.0 with its products left out, and 1.7 whole.  The 72 loads of a step and
+// the waves' reads of the products' operands share the path into LDS, and one
+// workgroup fills a compute unit's LDS, so that nothing else runs meanwhile.
 #pragma once
 
 #include "block_common.h"
@@ -223,7 +228,7 @@ struct Tile {
       if constexpr (PAIR) s[1][j] = s[0][j] * s1;
       s[0][j] *= s0;
     }
-    // (4096^3: 69.6 us with 3, 72.1 with 2, 75.4 with 1)
+    // (4096^3: 67.8 us with 3, 72.1 with 2, 75.4 with 1)
     constexpr int kDelay = 3, kAll = MT * JT;
     f32x4 d[kDelay + 1];
     for_each<kAll + kDelay>([&](auto n_c) MOE_INLINE {
@@ -284,7 +289,7 @@ struct Tile {
       if (rest < (int)kStep) clear_tail(stage, wave, lane, rest);
       wait_lds();                                            // and its reads of the step before returned
       barrier();
-      // (spread between the products instead, they end later: 4096^3 65.0 us, and 66.5)
+      // (before the products: spread between them, 4096^3 takes 66.5 us and not 65.0)
       load(stage_at(std::integral_constant<int, (S + kLead) % NS>{}));
       if (ALL || here) {
 #pragma unroll

@@ -2,7 +2,10 @@
 binding's."""
 
 import ctypes
+import glob
+import hashlib
 import os
+import re
 
 import pytest
 import torch
@@ -145,3 +148,18 @@ def test_step_refusals():
         sme.Fp8MoeStep(2, 64, 64, 8, 2, "cpu", rule=sme.RouteRule(4))
     with pytest.raises(ValueError, match="residual_dtype"):
         sme.Fp8MoeStep(2, 64, 64, 8, 2, "cpu", residual_dtype=torch.float16)
+
+
+def test_profile_names_the_current_sources():
+    """The summary of these operators' kernels names the digest of csrc/fp8/*.hip and *.h (contents concatenated in sorted
+    path order), which that of csrc/*.hip and *.h does not cover."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    fp8 = os.path.join(root, "sparse_moe_expert_amd", "csrc", "fp8")
+    h = hashlib.sha256()
+    for name in sorted(glob.glob(os.path.join(fp8, "*.hip")) + glob.glob(os.path.join(fp8, "*.h"))):
+        with open(name, "rb") as f:
+            h.update(f.read())
+    with open(os.path.join(root, "profiles", "block_operators_kernel_stats.md")) as f:
+        m = re.search(r"csrc/fp8/[^`]*sha256 prefix: `([0-9a-f]{16})`", f.read())
+    assert m, "the summary names no digest of csrc/fp8"
+    assert m.group(1) == h.hexdigest()[:16], "the summary was taken on other sources"
