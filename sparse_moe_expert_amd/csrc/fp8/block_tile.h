@@ -87,12 +87,12 @@ struct Tile {
 
   __amdgpu_buffer_rsrc_t rw, rx;             // the wave's weight rows, the tokens
   const float* s_from;                       // the wave's scales
-  uint32_t s_bytes;
+  uint32_t s_bytes, s_blocks;                // s_blocks: a row's
   size_t s_stride;
   uint32_t w_off[WL], s_off;
   uint32_t x_off[PAIR ? XL : 1], x_row;      // of a pair's tokens, gathered; else of the first piece's, 64 rows apart
   uint32_t token_at, scale_at;               // where a wave's first token piece and its scales go
-  int scale_block;                           // the block of the step that its scales are of
+  uint32_t scale_block;                           // the block of the step that its scales are of
   f32x4 acc[MT][JT];
 
   // Row of the tile (of a pair: in the 128 of either matrix, the second's from
@@ -151,7 +151,7 @@ struct Tile {
   template <class F>
   __device__ __forceinline__ void token_scales(const float* first, uint32_t bytes, size_t stride, int wave, int lane, F&& f) {
     const int id = wave % (U * kScaleGroups), group = id % kScaleGroups;
-    scale_block = id / kScaleGroups;
+    scale_block = (uint32_t)(id / kScaleGroups);
     scale_at = kWeightBytes + id * 256u;
     s_off = 0;
     if (group < kScaleGroups - 2) {
@@ -161,6 +161,7 @@ struct Tile {
   }
   __device__ __forceinline__ void weight_scales(const float* first, const float* second, int kb, int wave) {
     const int group = wave % (U * kScaleGroups) % kScaleGroups;
+    s_blocks = (uint32_t)kb;
     if (group >= kScaleGroups - 2)
       s_from = group == kScaleGroups - 2 ? first : second, s_bytes = (uint32_t)kb * 4u, s_stride = 4;
   }
@@ -174,9 +175,10 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < WL; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, stage.w + weight_piece(i, wave) * 1024, 16, w_off[i] + step * kStep, 0, 0, 0);
-    const bool none = step >= kNoStep;
-    const __amdgpu_buffer_rsrc_t rs =
-        make_rsrc(reinterpret_cast<const uint8_t*>(s_from) + (none ? 0 : (step * U + scale_block) * s_stride), s_bytes);
+    // (U > 1: a row's last step may have no second block)
+    const uint32_t block = step * U + scale_block;
+    const bool none = U > 1 ? block >= s_blocks : step >= kNoStep;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<const uint8_t*>(s_from) + (none ? 0 : block * s_stride), s_bytes);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, stage.w + scale_at, 4, none ? kOutside : s_off, 0, 0, 0);
     fence();
   }
