@@ -13,7 +13,8 @@
 // in fp32.  It is taken all the same: the operands are e4m3, off by up to 2^-4 of
 // themselves, and on activations as layers have them the cuts move an output by
 // 1e-4 of its size, a seventeenth of its own rounding to bf16.  Products in bf16
-// would keep every bit, at half the rate and with a conversion of each operand.
+// keep every bit, at half the rate and with a conversion of each operand: the
+// experts' first products of small batches, whose result is encoded once more.
 //
 // The instruction's lanes: weights as A, lane l holds row l%16; tokens as B,
 // lane l holds column l%16; lane l's 32 bytes are the same reduction indices in
@@ -64,6 +65,30 @@ __device__ __forceinline__ i32x8 fragment(const i32x4 lo, const i32x4 hi) {
 // One block's products (scale operands of 0: the instruction without scales)
 __device__ __forceinline__ f32x4 block_product(i32x8 a, i32x8 b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{}, 0, 0, 0, 0, 0, 0);
+}
+
+// The same in bf16, which holds every e4m3 code: four instructions of 32 bytes of
+// the block each, and no product loses a bit
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+struct Wide {
+  bf16x8v part[4];
+};
+__device__ __forceinline__ Wide widen(const i32x8 f) {
+  Wide w;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[i], 1.0f, false);
+    const auto hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[i], 1.0f, true);
+    w.part[i / 2][i % 2 * 4] = lo[0], w.part[i / 2][i % 2 * 4 + 1] = lo[1];
+    w.part[i / 2][i % 2 * 4 + 2] = hi[0], w.part[i / 2][i % 2 * 4 + 3] = hi[1];
+  }
+  return w;
+}
+__device__ __forceinline__ f32x4 block_product(const Wide& a, const Wide& b) {
+  f32x4 d{};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.part[i], b.part[i], d, 0, 0, 0);
+  return d;
 }
 
 // max over the 16 lanes of a row of lanes, in each of them

@@ -43,7 +43,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs
   tl.template run<true, true, 0>(stage_at, wave, wr, wt, lane, first, steps, 1, p.K, [](int) {}, [&](int) MOE_INLINE {
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {
-      const int r = (wt * T::JT + j) * 16 + (lane & 15);
+      const int r = T::token_tile(wt, j) * 16 + (lane & 15);
       if (r >= toks) continue;
 #pragma unroll
       for (int m = 0; m < T::MT; m += T::Q) {
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void linear_tile_kernel(LinearArgs
         }
       }
     }
-  }, [](int) { return true; });
+  }, [](int) { return T::JT; });
 }
 
 // The parts' sums, in order, to outputs: a thread to four of a token

@@ -6,15 +6,16 @@
 //
 // Routes are grouped by expert, so that an expert's weights are read once for all
 // of its routes in a tile: bound by the weight bytes while an expert has few
-// routes (T = 100 2560x640 of 512 experts: 2.2 GB in 406 to 425 us, 5.2 to 5.4
-// TB/s; T = 4096 2048x512 of 512: 429, of which the sums written and read are 70),
+// routes (T = 100 2560x640 of 512 experts: 2.2 GB in 407 to 414 us, 5.2 to 5.3
+// TB/s; T = 4096 2048x512 of 512: 432, of which the sums written and read are 70),
 // by the products and by how evenly whole tiles fill the chip else (T = 2000
 // 4096x2048 of 16: 191, 1050 TFLOP/s).
 //
 // h in 8 bits is what makes the second product one of 8 bits.  Where h lies next
-// to the middle between two codes, what the first products' instruction cuts
-// (block_common.h) can turn its code over: a token's y is off by 1.7e-3 of its
-// size in the median (its rounding to bf16), 4.4e-3 to 6.4e-3 in the worst of 100.
+// to the middle between two codes, what an 8-bit product cuts (block_common.h) can
+// turn its code over: a token's y is off by 1.7e-3 of its size in the median (its
+// rounding to bf16), 4.4e-3 to 6.4e-3 in the worst of 100.  Up to 128 tokens the
+// first products are made in bf16 and cut nothing: 1.7e-3 for every token.
 #include "block_few.h"
 #include "block_tile.h"
 
@@ -161,10 +162,13 @@ __device__ __forceinline__ Run run_of(const FfnArgs& p, int row_tiles) {
 }
 
 // h of 128 rows of an item's routes, in 8 bits: the rows are one block, whose
-// largest value goes from wave to wave through LDS
-template <int TT>
+// largest value goes from wave to wave through LDS.  WIDE: products in bf16, which
+// lose no bit; without a plan, where the weights' bytes take longer (T = 4 2048x512
+// of 512 experts 37.9 us, 37.3 in 8 bits, T = 100 2560x640 414 and 411; but T = 4096
+// 2048x512 474 and 433).
+template <int TT, bool WIDE>
 __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int row_tiles) {
-  using T = Tile<TT, true>;
+  using T = Tile<TT, true, kTileRows, 1, WIDE>;
   MOE_TILE_STAGES(T)
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave % T::WR, wt = wave / T::WR;
@@ -210,7 +214,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
       done = number;
       item = kb > T::kLead ? item_in : item_at<TT>(p, number, pass, longest);
     }
-    return item.toks > wt * T::JT * 16;
+    return T::tiles_of(wt, item.toks);
   };
   auto end = [&](int i) MOE_INLINE {
     const int tile = (run.first + i) % row_tiles, n0 = tile * kBlock, first = item.first, toks = item.toks;
@@ -230,7 +234,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
       uint32_t top = n < p.I ? largest(h) : 0u;              // (rows past I are not its)
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
-      if (g == 0) s_max[wr * TT + (wt * T::JT + j) * 16 + l] = top;
+      if (g == 0) s_max[wr * TT + T::token_tile(wt, j) * 16 + l] = top;
     }
     wait_lds();
     barrier();
@@ -239,7 +243,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
     const __amdgpu_buffer_rsrc_t to_s = make_rsrc(p.hs + (size_t)tile * p.T * p.k + first, (uint32_t)toks * 4u);
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {
-      const int r = (wt * T::JT + j) * 16 + (l & 15);
+      const int r = T::token_tile(wt, j) * 16 + (l & 15);
       uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < T::WR; ++w) top = max(top, s_max[w * TT + r]);
@@ -307,7 +311,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
       done = number;
       item = kb > T::kLead ? item_in : item_at<TT>(p, number, pass, longest);
     }
-    return item.toks > wt * T::JT * 16;
+    return T::tiles_of(wt, item.toks);
   };
   auto end = [&](int i) MOE_INLINE {
     const int n0 = (run.first + i) % row_tiles * kTileRows, first = item.first, toks = item.toks;
@@ -332,7 +336,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
       uint32_t top = largest(v);
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
-      if (g == 0) s_max[wr * TT + (wt * T::JT + j) * 16 + l] = top;
+      if (g == 0) s_max[wr * TT + T::token_tile(wt, j) * 16 + l] = top;
     }
     wait_lds();
     barrier();
@@ -343,7 +347,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void down_kernel(FfnArgs p, int ro
     const __amdgpu_buffer_rsrc_t to_s = make_rsrc(p.os + (size_t)first * hb, (uint32_t)toks * (uint32_t)hb * 4u);
 #pragma unroll
     for (int j = 0; j < T::JT; ++j) {
-      const int r = (wt * T::JT + j) * 16 + (l & 15);
+      const int r = T::token_tile(wt, j) * 16 + (l & 15);
       uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < kShare; ++w) top = max(top, s_max[(wr / kShare * kShare + w) * TT + r]);
@@ -418,7 +422,7 @@ __global__ __launch_bounds__(kFfnThreads) void combine_kernel(FfnArgs p) {
 // a token's are added in slot order.  Bound by the weight bytes, and at one
 // workgroup a compute unit by how many of those read: 8 rows, half a product's,
 // where that many workgroups all run at once (T = 4 2048x512 of 512 experts, 40
-// chosen: 13.0 us, 15.6 with 16 rows; 2048x1024 of 64: 10.2 and 12.6; but 2304x512
+// chosen: 11.9 us, 15.6 with 16 rows; 2048x1024 of 64: 10.2 and 12.6; but 2304x512
 // of 256: 18.7 and 13.4).  In a launch of its own the sum took 5 us more.
 constexpr int kDownWaves = 16;
 constexpr int kDownGroups = 256;             // workgroups that run at once, one on a compute unit
@@ -508,7 +512,10 @@ void launch_products(const FfnArgs& p, int items, hipStream_t s) {
     const long long tiles = ((long long)items * row_tiles + kXcds - 1) / kXcds * kXcds;
     return (unsigned)(tiles < most ? tiles : most);
   };
-  gate_up_kernel<TT><<<grid(up), kTileThreads, 0, s>>>(p, up);
+  if constexpr (TT <= kUnplanned)
+    if (!p.items) gate_up_kernel<TT, true><<<grid(up), kTileThreads, 0, s>>>(p, up);
+  if constexpr (TT >= kUnplanned)
+    if (p.items) gate_up_kernel<TT, false><<<grid(up), kTileThreads, 0, s>>>(p, up);
   if constexpr (TT == 16) {
     if (p.H / 8 <= kDownGroups) down_combine_kernel<8><<<(unsigned)p.H / 8, kDownThreads, 0, s>>>(p);
     else down_combine_kernel<16><<<(unsigned)p.H / 16, kDownThreads, 0, s>>>(p);

@@ -69,8 +69,8 @@ struct Stage {
 };
 
 // ROWS: weight rows of the tile (256 of a pair, 128 of each matrix); U: blocks of
-// the reduction a step
-template <int TT, bool PAIR, int ROWS = kTileRows, int U = 1>
+// the reduction a step; WIDE: products in bf16
+template <int TT, bool PAIR, int ROWS = kTileRows, int U = 1, bool WIDE = false>
 struct Tile {
   static constexpr int WR = TT == ROWS ? 2 : TT == 16 ? 8 : 4, WT = 8 / WR;
   static constexpr int MT = ROWS / WR / 16, JT = TT / WT / 16;        // row tiles, token tiles a wave
@@ -207,7 +207,21 @@ struct Tile {
                     *reinterpret_cast<const i32x4*>(row + (((g + 4) ^ x) << 4)));
   }
 
-  // The products of block u of a step
+  // A wave's token tile j, of the tile's 16-token tiles: two runs of kHalf, the
+  // second from the tile's middle on, so that in a tile that is not full some waves
+  // of each SIMD make half the products (T = 4096 2048x512 of 512 experts: down 161
+  // us, 174 with one run each; not for 256 tokens, whose products in both forms leave
+  // too few registers: 8192 tokens of the same 617 us, 602 with one run).
+  static constexpr int kHalf = TT <= 128 && JT > 1 ? JT / 2 : JT;
+  static __device__ __forceinline__ int token_tile(int wt, int j) { return j / kHalf * (kHalf * WT) + wt * kHalf + j % kHalf; }
+  // Of a wave's, those up to the end of the last run with any of `toks` tokens
+  static __device__ __forceinline__ int tiles_of(int wt, int toks) {
+    const int at = wt * kHalf * 16;
+    return kHalf < JT && toks > at + kHalf * WT * 16 ? JT : toks > at ? kHalf : 0;
+  }
+
+  // The products of block u of a step and the wave's first J token tiles
+  template <int J>
   __device__ __forceinline__ void products(const Stage& stage, int u, int wr, int wt, int lane) {
     const int l16 = lane & 15, g = lane >> 4;
     const uint8_t* const weights = stage.w + u * (ROWS * kBlock);
@@ -215,35 +229,42 @@ struct Tile {
     const float* const scales = reinterpret_cast<const float*>(stage.w + kWeightBytes + u * kScaleGroups * 256);
     const float* const sw = scales + (kScaleGroups - 2) * 64;
     const float s0 = PAIR || wr * MT < 8 ? sw[0] : sw[64], s1 = PAIR ? sw[64] : s0;
-    i32x8 b[JT], a[2];
-    float s[2][JT];
+    i32x8 b[J], a[2];
+    float s[2][J];
     const int by = (l16 >> 1 & 1) | (l16 >> 2) << 1;         // mix(row_of(...))
     a[0] = read(weights, row_of(wr, 0, l16), by, g);
 #pragma unroll
-    for (int j = 0; j < JT; ++j) {
-      const int r = (wt * JT + j) * 16 + l16;
+    for (int j = 0; j < J; ++j) {
+      const int r = token_tile(wt, j) * 16 + l16;
       b[j] = read(tokens, r, token_mix(r), g);
       s[0][j] = scales[r];
     }
 #pragma unroll
-    for (int j = 0; j < JT; ++j) {
+    for (int j = 0; j < J; ++j) {
       if constexpr (PAIR) s[1][j] = s[0][j] * s1;
       s[0][j] *= s0;
     }
     // (4096^3: 67.8 us with 3, 72.1 with 2, 75.4 with 1)
-    constexpr int kDelay = 3, kAll = MT * JT;
+    constexpr int kDelay = 3, kAll = MT * J;
+    Wide wide_a, wide_b[WIDE ? J : 1];
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) wide_b[j] = widen(b[j]);
+    }
     f32x4 d[kDelay + 1];
     for_each<kAll + kDelay>([&](auto n_c) MOE_INLINE {
       constexpr int n = decltype(n_c)::value, q = n - kDelay;
       if constexpr (n < kAll) {
-        if constexpr (n % JT == 0 && n / JT + 1 < MT) a[(n / JT + 1) % 2] = read(weights, row_of(wr, n / JT + 1, l16), by, g);
-        d[n % (kDelay + 1)] = block_product(a[n / JT % 2], b[n % JT]);
+        if constexpr (n % J == 0 && n / J + 1 < MT) a[(n / J + 1) % 2] = read(weights, row_of(wr, n / J + 1, l16), by, g);
+        if constexpr (WIDE && n % J == 0) wide_a = widen(a[n / J % 2]);
+        if constexpr (WIDE) d[n % (kDelay + 1)] = block_product(wide_a, wide_b[n % J]);
+        else d[n % (kDelay + 1)] = block_product(a[n / J % 2], b[n % J]);
       }
       if constexpr (q >= 0) {
-        const float scale = s[PAIR && q / JT >= HT][q % JT];
+        const float scale = s[PAIR && q / J >= HT][q % J];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[q / JT][q % JT][i] = fmaf(d[q % (kDelay + 1)][i], scale, acc[q / JT][q % JT][i]);
-        asm volatile("" : "+v"(acc[q / JT][q % JT]));         // here, and not where the sums are used next
+        for (int i = 0; i < 4; ++i) acc[q / J][q % J][i] = fmaf(d[q % (kDelay + 1)][i], scale, acc[q / J][q % J][i]);
+        asm volatile("" : "+v"(acc[q / J][q % J]));         // here, and not where the sums are used next
       }
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -259,9 +280,9 @@ struct Tile {
   // `tiles` tiles of `steps` steps each, from step `first` of the reduction on,
   // as one stream: while a tile's last steps are multiplied the next one's first
   // are on their way.  begin(i) sets the loads to tile i (0 is set before);
-  // end(i) finishes tile i's sums; live(i): whether this wave has any of its tokens
-  // (ALL: not asked).  ONE: one tile only; else end(i) stores STORES times, whatever
-  // the tile, and the next step need not wait for that.
+  // end(i) finishes tile i's sums; live(i): this wave's tiles_of its tokens (ALL: not
+  // asked).  ONE: one tile only; else end(i) stores STORES times, whatever the tile,
+  // and the next step need not wait for that.
   template <bool ALL, bool ONE, int STORES, class At, class Begin, class End, class Live>
   __device__ __forceinline__ void run(At&& stage_at, int wave, int wr, int wt, int lane, int first, int steps, int tiles, int K,
                                       Begin&& begin, End&& end, Live&& live) {
@@ -280,7 +301,7 @@ struct Tile {
     for_each<kLead>([&](auto s) MOE_INLINE { load(stage_at(s)); });
     clear_sums();
     int out = 0, tile_out = 0;
-    bool here = ALL || live(0);
+    int here = ALL ? JT : live(0);
     auto body = [&](auto stage_c) MOE_INLINE {
       constexpr int S = decltype(stage_c)::value;
       const Stage stage = stage_at(stage_c);
@@ -293,11 +314,13 @@ struct Tile {
       barrier();
       // (before the products: spread between them, 4096^3 takes 66.5 us and not 65.0)
       load(stage_at(std::integral_constant<int, (S + kLead) % NS>{}));
-      if (ALL || here) {
+      for_each<ALL || kHalf == JT ? 1 : 2>([&](auto half) MOE_INLINE {
+        constexpr int J = decltype(half)::value ? kHalf : JT;
+        if (!ALL && (here == 0 || (kHalf < JT && (here <= kHalf) != (J < JT)))) return;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (u == 0 || rest > u * kBlock) products(stage, u, wr, wt, lane);
-      }
+          if (u == 0 || rest > u * kBlock) products<J>(stage, u, wr, wt, lane);
+      });
       ++out;
       if (!ONE && out == steps) {
         out = 0;
