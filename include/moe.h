@@ -800,8 +800,10 @@ size_t moe_block_expert_ffn_workspace_size(int T, int H, int I, int E, int k);
  *   h_p = SiLU(Wg_e x_t) * (Wu_e x_t) in fp32, then encoded as above,
  *   o_p = Wd_e h_p,
  *   y_t = sum_j topk_w[t,j] * o_(t,j), in slot order, rounded once to bf16,
- * products and sums as in moe_block_linear.  Each chosen expert's weights are
- * read once for all of its routes.
+ * products and sums as in moe_block_linear, but that up to 128 tokens Wg_e x_t and
+ * Wu_e x_t drop no bits, and that beyond 16 tokens o_p keeps 11 bits of each value
+ * (down to 2^-28 of the largest of its 128).  Each chosen expert's weights are read
+ * once for all of its routes; a token may name an expert more than once.
  *   x, x_scale           tokens [T, H]             in
  *   w_gate/w_up, s_*     E weights [I, H]: codes [E, I, H], scales
  *                        [E, ceil(I/128), ceil(H/128)]    in
