@@ -719,9 +719,9 @@ moe_status moe_quant_shared_expert(int format, const uint16_t* x,
  * K (and H and I) are multiples of 16.
  *
  * Encoding of values v: per block s = max(amax |v| / 448, 2^-126), codes
- * e4m3(v / s), to nearest even.  An infinite or NaN v has no part in amax and
- * its code is NaN (e4m3 has no infinities); a product with it is NaN, in the
- * outputs of its own token only.
+ * e4m3(v / s), to nearest even, both divisions rounded to fp32.  An infinite or
+ * NaN v has no part in amax and its code is NaN (e4m3 has no infinities); a
+ * product with it is NaN, in the outputs of its own token only.
  *
  * moe_norm_quantize — residual addition, RMS norm and encoding in one pass.
  *

@@ -122,11 +122,32 @@ __device__ __forceinline__ uint32_t largest(const float (&v)[N]) {
 // it within e4m3, and normal, so that its reciprocal is finite
 __device__ __forceinline__ float block_scale(float amax) { return fmaxf(amax / 448.0f, 0x1p-126f); }
 
+// The quotient by a block's scale as fp32 division rounds it, so that a code is the
+// one of any quantiser that divides: v * (1 / s) takes another one on ties, of bf16
+// rows 6e-4 of the codes.  One reciprocal for the block, and a correction of each
+// product by its remainder, which leaves it within 2^-22 of a unit of the exact
+// quotient before the last rounding.  So it is the division's unless the exact one
+// lies that near the middle between two fp32 values; next to a tie between codes,
+// where alone that counts, s would have to lie within 8 units of an eighth of its
+// power of two, and not on it: no s = a / 448 of a bf16 a does.  (The remainder's
+// sign is such that -0 stays -0.)
+// T = 8192 4096 encoded: 18.6 us, 18.0 to 18.4 with v * (1 / s), 20.9 with the
+// compiler's division; the experts' gate/up kernels 0.4 to 0.8% and 2 to 3%.
+struct Divisor {
+  float s, inv;
+};
+__device__ __forceinline__ float over(float v, const Divisor& d) {
+  const float q = v * d.inv;
+  return fmaf(-fmaf(q, d.s, -v), d.inv, q);
+}
+// What v and s are both taken times: 2^90 where remainders would be subnormal
+__device__ __forceinline__ float lift_of(float s) { return s < 0x1p-90f ? 0x1p90f : 1.0f; }
+
 // Four values over the scale -> four codes, to nearest even; beyond 464, and so
 // of an infinity, the conversion's code is NaN
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
-  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, const Divisor& s) {
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(over(a, s), over(b, s), 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(over(c, s), over(d, s), w, true);
 }
 
 }  // namespace

@@ -247,12 +247,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int
       uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < T::WR; ++w) top = max(top, s_max[w * TT + r]);
-      const float s = block_scale(__uint_as_float(top)), inv = 1.0f / s;
+      const float s = block_scale(__uint_as_float(top));
+      const float lift = lift_of(s);
+      const Divisor d{s * lift, 1.0f / (s * lift)};
       __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), to_s,
                                             wr == 0 && g == 0 ? (uint32_t)r * 4u : kOutside, 0, 0);
       uint32_t c[Q];
 #pragma unroll
-      for (int q = 0; q < Q; ++q) c[q] = encode4(tl.acc[q][j][0], tl.acc[q][j][1], tl.acc[q][j][2], tl.acc[q][j][3], inv);
+      for (int q = 0; q < Q; ++q) {
+        const f32x4 v = tl.acc[q][j] * lift;
+        c[q] = encode4(v[0], v[1], v[2], v[3], d);
+      }
       static_assert(HT == Q, "a lane's values of a token are neighbours");
       const uint32_t at = n < p.I && r < toks ? (uint32_t)r * (uint32_t)p.I + (uint32_t)n : kOutside;      // (I is a multiple of 16)
       if constexpr (Q == 4) __builtin_amdgcn_raw_buffer_store_b128(u32x4{c[0], c[1], c[2], c[3]}, to_q, at, 0, 0);

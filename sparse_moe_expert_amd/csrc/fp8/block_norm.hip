@@ -9,7 +9,7 @@
 // row of the cross-lane network, hold a block of 128.  The sum of squares is
 // fp64: squares of large values leave fp32, and with the row in registers it
 // costs less than the loads it runs beside.  (T = 4096 2560, an fp32 residual:
-// 25.5 us, 5.4 TB/s; T = 8192 4096 encoded: 18.3 us, 5.6 TB/s.  A large copy
+// 25.5 us, 5.4 TB/s; T = 8192 4096 encoded: 18.6 us, 5.5 TB/s.  A large copy
 // reaches 5.2.)
 #include "block_common.h"
 
@@ -45,11 +45,18 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 
 // Eight values of a block that 16 lanes hold (those past the row: zero) to
 // codes at q and, from its first lane, the scale
-__device__ __forceinline__ void encode8(const float (&v)[8], bool here, uint8_t* q, float* scale) {
+__device__ __forceinline__ void encode8(float (&v)[8], bool here, uint8_t* q, float* scale) {
   const float s = block_scale(__uint_as_float(max16(largest(v))));
-  const float inv = 1.0f / s;
   if (!here) return;
-  *reinterpret_cast<uint2*>(q) = make_uint2(encode4(v[0], v[1], v[2], v[3], inv), encode4(v[4], v[5], v[6], v[7], inv));
+  float lifted = s;
+  if (__builtin_expect(__any(s < 0x1p-90f), 0)) {
+    const float lift = lift_of(s);
+    lifted = s * lift;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= lift;
+  }
+  const Divisor d{lifted, 1.0f / lifted};
+  *reinterpret_cast<uint2*>(q) = make_uint2(encode4(v[0], v[1], v[2], v[3], d), encode4(v[4], v[5], v[6], v[7], d));
   if ((threadIdx.x & 15) == 0) *scale = s;
 }
 

@@ -1,0 +1,130 @@
+"""Codes of the block-scaled 8-bit operators, bit for bit where the arithmetic in front of them is exact: the fp32 quotient
+v / s to the nearest e4m3, ties to the even code, on values chosen to lie on ties and next to them."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sparse_moe_expert_amd as sme
+from block_testlib import as_f64, dev, dev_experts, dev_tokens
+from gpu_harness import DEV
+from layer_testlib import bits, dev_bf16
+
+pytestmark = pytest.mark.gpu
+
+F = np.float32
+
+
+def encoded(v):
+    """(code bytes, fp32 scales) of fp32 values [T, K], with fp32 divisions."""
+    T, K = v.shape
+    s = np.stack([np.maximum(np.abs(v[:, b:b + 128]).max(axis=1) / F(448.0), F(2.0 ** -126)) for b in range(0, K, 128)], axis=1)
+    ratio = v / np.repeat(s, 128, axis=1)[:, :K]
+    assert s.dtype == ratio.dtype == np.float32
+    return torch.from_numpy(ratio).to(torch.float8_e4m3fn).view(torch.uint8).numpy(), s
+
+
+def check_tokens(tokens, v, what):
+    q, s = encoded(v)
+    assert np.array_equal(tokens.scale.cpu().numpy(), s), f"{what}: scales"
+    got = tokens.q.view(torch.uint8).cpu().numpy()
+    wrong = np.argwhere(got != q)
+    assert wrong.size == 0, f"{what}: {len(wrong)} codes of {q.size}, first at {wrong[0]}: {got[tuple(wrong[0])]}, not {q[tuple(wrong[0])]}"
+
+
+def bf16(v):
+    return oracle.bf16_bits_to_f64(bits(v)).astype(np.float32)
+
+
+def near_ties(rng, T, K):
+    """Values with eight bits whose quotient by their block's scale lies on the middle between two codes or within a few
+    roundings of it: every such pair of a largest value and another, at many powers of two."""
+    m = np.arange(128, 256)
+    ratio = 448.0 * m[None, :] / m[:, None]                            # of value m over scale top / 448, top the row
+    _, e = np.frexp(ratio)
+    steps = ratio / np.ldexp(1.0, e - 4)                               # in steps of the codes there
+    top, low = np.nonzero(np.abs(steps - np.floor(steps) - 0.5) < 2.0 ** -18)
+    x = np.zeros((T, K))
+    for b in range(0, K, 128):
+        block = x[:, b:b + 128]
+        for row in block:
+            t = rng.choice(top)
+            row[:] = m[rng.choice(low[top == t], row.size)] * 2.0 ** -rng.integers(1, 6, row.size)
+            row[rng.integers(0, row.size)] = m[t]
+    x *= np.where(rng.integers(0, 2, (T, K)), 1.0, -1.0) * 2.0 ** rng.integers(-30, 30, (T, 1))
+    assert np.array_equal(bf16(x), x.astype(F))
+    return x.astype(F)
+
+
+@pytest.mark.parametrize("T,K", [(1, 16), (300, 144), (70, 2048), (9, 8208)])
+def test_quantize_bits(T, K):
+    rng = np.random.default_rng(K)
+    for x in (bf16(rng.standard_normal((T, K))), near_ties(rng, T, K)):
+        x[rng.random((T, K)) < 0.02] = 0.0
+        x[rng.random((T, K)) < 0.02] = -0.0
+        check_tokens(sme.moe_block_quantize(dev_bf16(bits(x))), x, (T, K))
+
+
+def test_quantize_bits_of_tiny_values():
+    """Blocks whose scale is the smallest or close above it, their values down to the subnormal ones."""
+    rng = np.random.default_rng(1)
+    x = bf16(rng.standard_normal((200, 256)) * 2.0 ** rng.integers(-132, -90, (200, 1)))
+    check_tokens(sme.moe_block_quantize(dev_bf16(bits(x))), x, "tiny")
+
+
+@pytest.mark.parametrize("stream", [None, torch.bfloat16, torch.float32])
+def test_norm_bits(stream):
+    """Rows of +-1 with an eps that 1 + eps leaves out: y is +-weight exactly."""
+    rng = np.random.default_rng(2)
+    T, H = 40, 2064
+    sign = np.where(rng.integers(0, 2, (T, H)), F(1.0), F(-1.0))
+    for w in (bf16(rng.standard_normal(H)), near_ties(rng, 1, H)[0]):
+        res = None if stream is None else dev(sign * F(2.0)).to(stream)
+        x = sign if stream is None else -sign
+        tokens, _ = sme.moe_norm_quantize(dev_bf16(bits(x)), dev_bf16(bits(w)), res, eps=1e-30)
+        check_tokens(tokens, sign * w, stream)
+
+
+@pytest.mark.parametrize("T", [3, 16, 30, 60, 120, 200, 600])
+def test_expert_codes(T):
+    """h = g u with SiLU(g) = g (e^-g is below half a step of 1) and each of g and u one code by the two scales' product, so
+    that its codes are known; `down` hands them through."""
+    rng = np.random.default_rng(T)
+    H = I = 128  # noqa: E741
+    E = 1 if T < 600 else 2                                  # (200 and 600: tiles of 256 and 128 routes)
+    x = np.zeros((T, H))
+    x[:, 0] = 1.0
+    sx = rng.uniform(0.5, 2.0, (T, 1)).astype(F)
+    gate, up, down = np.zeros((E, I, H)), np.zeros((E, I, H)), np.zeros((E, H, I))
+    gate[:, :, 0] = 448.0
+    up[:, :, 0] = np.resize([12.0, 9.0, 10.0, 11.0, 4.5, 8.0, 5.5, 2.25, 3.25, 7.0, 1.125, 0.5625], I)
+    down[:, np.arange(H), np.arange(I)] = 1.0
+    one = np.ones((E, 1, 1), F)
+    sg, su = F(0.9), F(0.7)
+    g = F(448.0) * (sx * sg)
+    h = g * (up[0, :, 0].astype(F) * (sx * su))
+    assert g.dtype == h.dtype == np.float32 and g.min() > 110.0
+    q, s = encoded(h)
+    idx = rng.integers(0, E, (T, 1)).astype(np.int32)
+    w = np.ones((T, 1), F)
+    y = sme.moe_block_expert_ffn(dev_tokens((x, sx)), dev_experts((gate, one * sg), (up, one * su), (down, one)), dev(w),
+                                 sme.moe_bucket_routes(dev(idx), E))
+    # y is code * s but for roundings of 2^-8 and 2^-11 at most; neighbouring codes are 2^-4 apart
+    got = oracle.block.round_e4m3(as_f64(y) / s.astype(np.float64))
+    want = torch.from_numpy(q).view(torch.float8_e4m3fn).double().numpy()
+    wrong = got != want
+    assert not wrong.any(), f"{wrong.sum()} codes of {wrong.size}: {h[wrong][:3]}, scales {s[np.where(wrong)[0][:3], 0]}"
+
+
+def test_reciprocals_would_differ():
+    """What these inputs are for: with v * (1 / s) in place of the quotient some of each test's codes are other ones."""
+    rng = np.random.default_rng(3)
+
+    def other(v):
+        q, s = encoded(v)
+        per = np.repeat(F(1.0) / s, 128, axis=1)[:, :v.shape[1]]
+        return (torch.from_numpy(v * per).to(torch.float8_e4m3fn).view(torch.uint8).numpy() != q).mean()
+
+    assert other(bf16(rng.standard_normal((300, 144)))) > 1e-4
+    assert other(near_ties(rng, 300, 144)) > 1e-4
