@@ -122,10 +122,13 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs p) {
   }
 }
 
-// A thread to 8 values, 16 neighbouring threads to a block
+// A thread to 8 values, 16 neighbouring threads to a block.  The largest batch has
+// 2^32 threads, which no row of workgroups can have: two rows of them then.
+constexpr size_t kGroupsRow = 1 << 23;
+
 __global__ __launch_bounds__(kNormThreads) void quantize_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ q,
                                                                 float* __restrict__ scale, int K, int kb, size_t blocks) {
-  const size_t block = (size_t)blockIdx.x * (kNormThreads / 16) + (threadIdx.x >> 4);
+  const size_t block = (blockIdx.y * kGroupsRow + blockIdx.x) * (kNormThreads / 16) + (threadIdx.x >> 4);
   if (block >= blocks) return;               // all 16 lanes of a block alike
   const size_t t = block / (size_t)kb;
   const int at = (int)(block - t * (size_t)kb) * kBlock + (threadIdx.x & 15) * 8;
@@ -178,7 +181,8 @@ extern "C" moe_status moe_block_quantize(const uint16_t* x, int T, int K, uint8_
   if (!aligned16(x) || !aligned16(q) || !aligned16(scale)) return MOE_ERR_MISALIGNED;
   const int kb = blocks_of(K);
   const size_t blocks = (size_t)T * (size_t)kb;              // at most 2^28
-  const unsigned grid = (unsigned)((blocks + kNormThreads / 16 - 1) / (kNormThreads / 16));
+  const size_t groups = (blocks + kNormThreads / 16 - 1) / (kNormThreads / 16);
+  const dim3 grid((unsigned)(groups < kGroupsRow ? groups : kGroupsRow), (unsigned)((groups + kGroupsRow - 1) / kGroupsRow));
   quantize_kernel<<<grid, kNormThreads, 0, static_cast<hipStream_t>(stream)>>>(x, q, scale, K, kb, blocks);
   return launch_status();
 }

@@ -128,3 +128,22 @@ def test_reciprocals_would_differ():
 
     assert other(bf16(rng.standard_normal((300, 144)))) > 1e-4
     assert other(near_ties(rng, 300, 144)) > 1e-4
+
+
+def test_quantize_largest_batch():
+    """The most tokens of the longest rows: 2^28 blocks."""
+    torch.cuda.empty_cache()
+    T, K, part = 1 << 20, 1 << 15, 1 << 10
+    rows = torch.randn((part, K), dtype=torch.bfloat16, device=DEV)
+    x = torch.empty((T // part, part, K), dtype=torch.bfloat16, device=DEV)
+    x[:] = rows
+    out = sme.empty_fp8_tokens(T, K, DEV)
+    out.scale.fill_(-1.0)
+    sme.moe_block_quantize(x.view(T, K), out)
+    del x
+    want = sme.moe_block_quantize(rows)
+    q, s = out.q.view(torch.uint8).view(-1, part, K), out.scale.view(-1, part, K // 128)
+    for i in range(0, T // part, 32):
+        assert (q[i:i + 32] == want.q.view(torch.uint8)).all() and (s[i:i + 32] == want.scale).all(), i
+    del q, s, out
+    torch.cuda.empty_cache()
