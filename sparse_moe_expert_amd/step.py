@@ -15,7 +15,9 @@ import torch
 
 from ._lib import (
     ExpertWeights,
+    _check,
     empty_buckets,
+    load_library,
     make_workspace,
     moe_bucket_routes,
     moe_expert_ffn,
@@ -25,7 +27,9 @@ from ._lib import (
     moe_step,
 )
 from .block import Fp8Experts, empty_fp8_tokens, make_block_ffn_workspace, moe_block_expert_ffn, moe_norm_quantize
-from .layer import RouteRule, moe_route_grouped, moe_route_grouped_bucket
+from .layer import RouteRule, _int, moe_route_grouped, moe_route_grouped_bucket
+
+_NULL_POINTER = 1        # MOE_ERR_NULL_POINTER
 
 
 def expert_weights_from_numpy(bank, device) -> ExpertWeights:
@@ -120,7 +124,8 @@ class Fp8MoeStep:
     weight_offset), routes n (moe_router_logits on n in bf16; top-k, or by
     `rule`) and returns y, the experts' output for n in 8 bits.  `residual`
     (bf16, or fp32 with residual_dtype) holds r afterwards; the next layer's x
-    is y."""
+    is y.  Sizes that one of the calls does not take (the router: H up to 4096)
+    are refused here, with its MoeError."""
 
     def __init__(self, T: int, H: int, I: int, E: int, k: int, device, rule: Optional[RouteRule] = None,
                  residual_dtype: torch.dtype = torch.bfloat16, eps: float = 1e-6, weight_offset: float = 0.0):
@@ -128,6 +133,7 @@ class Fp8MoeStep:
             raise ValueError(f"residual_dtype must be bfloat16 or float32, got {residual_dtype}")
         if rule is not None and rule.k != k:
             raise ValueError(f"rule.k must be k={k}, got {rule.k}")
+        self._check_sizes(T, H, I, E, k)
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         self.rule, self.eps, self.weight_offset = rule, eps, weight_offset
         self.device = torch.device(device)
@@ -141,9 +147,24 @@ class Fp8MoeStep:
         self.workspace = make_block_ffn_workspace(T, H, I, E, k, self.device)
         self.y = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
 
+    @staticmethod
+    def _check_sizes(T: int, H: int, I: int, E: int, k: int):  # noqa: E741
+        """The calls' own checks of sizes, which stand before those of pointers: all NULL here."""
+        T, H, I, E, k = (_int(v, n) for v, n in zip((T, H, I, E, k), "THIEk"))  # noqa: E741
+        lib = load_library()
+        for name, args in (("moe_norm_quantize", [None, None, 0, None, 0.0, 1.0, T, H] + [None] * 5),
+                           ("moe_router_logits", [None, None, T, H, E, None, None]),
+                           ("moe_block_expert_ffn", [None] * 15 + [T, H, I, E, k, None, 0, None, None])):
+            status = getattr(lib, name)(*args)
+            if status != _NULL_POINTER:
+                _check(name, status)
+
     def run(self, x: torch.Tensor, residual: torch.Tensor, norm_weight: torch.Tensor, w_router: torch.Tensor,
             bias: Optional[torch.Tensor], experts: Fp8Experts) -> torch.Tensor:
-        """The step of bf16 x [T,H]; `residual` [T,H] may be self.residual, of the step before."""
+        """The step of bf16 x [T,H]; `residual` [T,H] may be self.residual, of the step before, and is
+        zeros where there is none."""
+        if residual is None:
+            raise TypeError("residual must be a tensor: zeros where there is no residual stream yet")
         moe_norm_quantize(x, norm_weight, residual, self.eps, self.weight_offset, self.tokens, self.residual, self.hidden)
         moe_router_logits(self.hidden, w_router, self.logits)
         if self.rule is not None:

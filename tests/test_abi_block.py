@@ -150,6 +150,27 @@ def test_step_refusals():
         sme.Fp8MoeStep(2, 64, 64, 8, 2, "cpu", residual_dtype=torch.float16)
 
 
+@pytest.mark.parametrize("sizes,status", [
+    ((2, 4112, 64, 8, 2), UNSUPPORTED),        # the router ends at 4096, the operators in 8 bits at 2^15
+    ((2, 8192, 64, 8, 2), UNSUPPORTED), ((2, 64, (1 << 15) + 16, 8, 2), UNSUPPORTED), ((2, 64, 64, 1025, 2), UNSUPPORTED),
+    (((1 << 20) + 1, 64, 64, 8, 2), UNSUPPORTED), ((2, 64, 64, 64, 33), UNSUPPORTED), ((-1, 64, 64, 8, 2), SHAPE),
+    ((2, 72, 64, 8, 2), SHAPE), ((2, 64, 40, 8, 2), SHAPE), ((2, 64, 64, 8, 9), SHAPE), ((2, 64, 64, 8, 0), SHAPE)])
+def test_step_sizes_refused_when_made(lib, sizes, status):
+    with pytest.raises(sme.MoeError) as e:
+        sme.Fp8MoeStep(*sizes, "cpu")
+    assert e.value.status == status
+
+
+@pytest.mark.parametrize("sizes", [(0, 64, 64, 8, 2), (1, 16, 16, 1, 1), (3, 4096, 64, 4, 4), (2, 16, 8192, 1, 1)])
+def test_step_sizes_taken(lib, sizes):
+    step = sme.Fp8MoeStep(*sizes, "cpu")
+    assert step.y.shape == sizes[:2]
+    with pytest.raises(TypeError, match="zeros"):
+        step.run(step.y, None, None, None, None, None)
+    with pytest.raises(ValueError, match="at most"):
+        sme.Fp8MoeStep(1 << 32, *sizes[1:], "cpu")
+
+
 def test_profile_names_the_current_sources():
     """The summary of these operators' kernels names the digest of csrc/fp8/*.hip and *.h (contents concatenated in sorted
     path order), which that of csrc/*.hip and *.h does not cover."""
