@@ -167,9 +167,11 @@ struct Tile {
   }
 
   __device__ __forceinline__ void issue(const Stage& stage, int wave, uint32_t step) {
+    // (kNoStep added to a missing row's kOutside would be an offset in range again)
+    const __amdgpu_buffer_rsrc_t tokens = PAIR && step >= kNoStep ? make_rsrc(nullptr, 0) : rx;
 #pragma unroll
     for (int i = 0; i < XL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, stage.x + token_at + i * 8192, 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(tokens, stage.x + token_at + i * 8192, 16,
                                                (PAIR ? x_off[PAIR ? i : 0] : x_off[0] + (uint32_t)i * x_row) + step * kStep, 0, 0, 0);
     fence();
 #pragma unroll
