@@ -716,6 +716,8 @@ moe_status moe_quant_shared_expert(int format, const uint16_t* x,
  *           block of 128 x 128 (shorter at the edges)
  * A value is its code times its scale.  Weight scales are finite; a token's
  * are what moe_norm_quantize and moe_block_quantize write, or any finite ones.
+ * Products multiply by the two scales' product, rounded to fp32: it has to be
+ * finite, and below 2^-126 it is subnormal or zero.
  * K (and H and I) are multiples of 16.
  *
  * Encoding of values v: per block s = max(amax |v| / 448, 2^-126), codes
@@ -802,8 +804,10 @@ size_t moe_block_expert_ffn_workspace_size(int T, int H, int I, int E, int k);
  *   y_t = sum_j topk_w[t,j] * o_(t,j), in slot order, rounded once to bf16,
  * products and sums as in moe_block_linear, but that up to 128 tokens Wg_e x_t and
  * Wu_e x_t drop no bits, and that beyond 16 tokens o_p keeps 11 bits of each value
- * (down to 2^-28 of the largest of its 128).  Each chosen expert's weights are read
- * once for all of its routes; a token may name an expert more than once.
+ * (down to 2^-28 of the largest of its 128).  So a token's y can differ in its
+ * last bits with the number of tokens beside it, between 16 and 17, and by codes
+ * of h between 128 and 129.  Each chosen expert's weights are read once for a
+ * tile of its routes (up to 128 or 256); a token may name an expert more than once.
  *   x, x_scale           tokens [T, H]             in
  *   w_gate/w_up, s_*     E weights [I, H]: codes [E, I, H], scales
  *                        [E, ceil(I/128), ceil(H/128)]    in

@@ -3,8 +3,9 @@
 // Few tokens are bound by the weight bytes (block_few.hip), more of them by the
 // products, of which each is worth its loads only in tiles of many rows and
 // tokens; where such tiles are too few for the chip, smaller ones take more loads
-// in less time.  (T = 32 9999x4096 10.0 us, 4.2 TB/s; T = 333 2560x5200 18.3;
-// 4096^3 63 to 65, 2100 to 2200 TFLOP/s.)
+// in less time.  (T = 32 9999x4096 13.5 us, 3.1 TB/s, with the weights from HBM, 9.8
+// with one weight read again and again, from the Infinity Cache; T = 333 2560x5200
+// 18.8 and 17.9; 4096^3 66.4 and 63.6, 2070 and 2160 TFLOP/s.)
 #include "block_linear.h"
 #include "block_tile.h"
 
@@ -83,11 +84,13 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs p, int np, 
 constexpr int kComputeUnits = 256;
 
 // A kernel of tiles: its tokens, rows, blocks a step; about what a workgroup's
-// start and end take and a block of its reduction, in ns.  (Measured with up to
-// 256 tiles: T = 333 2560x5200 18.7 us with 64x64 tiles, 21.8 with 128x64 in two
-// parts, 27.4 with 256x128 in six; T = 500 2048x2048 8.7, 10.1 with 128x64, 13.1
-// with 128x128; T = 1000 4096x4096 25.6 with 128x128, 31.1 with 128x64, 36.2 with
-// 256x128; T = 2000 2560x2560 25.7 with 256x128, 30.6 with 128x128.)
+// start and end take and a block of its reduction, in ns, measured with up to 256
+// tiles on one weight.  A block's bytes over its time are 39 to 57 KB a us for every
+// kind: it goes by what a compute unit brings into its LDS.  (Weights from HBM, rows
+// x tokens: T = 333 2560x5200 18.6 us with 64x64 tiles, 22.2 with 128x64 in two parts;
+// T = 500 2048x2048 8.7, 10.7 with 128x64, 15.3 with 128x128; T = 1000 4096x4096
+// 30.5 with 128x128, 37.1 with 128x64, 41.7 with 256x128; T = 2000 2560x2560 27.8
+// with 256x128, 36.9 with 128x128.)
 struct Kind {
   int tt, rows, unit;
   float start_ns, block_ns;

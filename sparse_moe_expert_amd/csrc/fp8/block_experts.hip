@@ -6,16 +6,17 @@
 //
 // Routes are grouped by expert, so that an expert's weights are read once for all
 // of its routes in a tile: bound by the weight bytes while an expert has few
-// routes (T = 100 2560x640 of 512 experts: 2.2 GB in 407 to 414 us, 5.2 to 5.3
-// TB/s; T = 4096 2048x512 of 512: 432, of which the sums written and read are 70),
-// by the products and by how evenly whole tiles fill the chip else (T = 2000
-// 4096x2048 of 16: 191, 1050 TFLOP/s).
+// routes (T = 100 2560x640 of 512 experts: 2.2 GB in 413 to 418 us, 5.2 to 5.3
+// TB/s; T = 4096 2048x512 of 512: 432 to 436, of which the sums written and read are
+// 70), by the products of tiles that are not full else (T = 2000 4096x2048 of 16: 184
+// to 189, 1070 to 1090 TFLOP/s).
 //
 // h in 8 bits is what makes the second product one of 8 bits.  Where h lies next
 // to the middle between two codes, what an 8-bit product cuts (block_common.h) can
-// turn its code over: a token's y is off by 1.7e-3 of its size in the median (its
-// rounding to bf16), 4.4e-3 to 6.4e-3 in the worst of 100.  Up to 128 tokens the
-// first products are made in bf16 and cut nothing: 1.7e-3 for every token.
+// turn its code over: a token's y is off by 1.8e-3 of its size in the median (1.7e-3
+// is its rounding to bf16), 4e-3 to 8e-3 in one of 100, 1.1e-2 to 1.4e-2 in the worst
+// of 4096.  Up to 128 tokens the first products are made in bf16 and cut nothing:
+// 1.7e-3, and 1.9e-3 in the worst, where the rounding of fp32 sums turned a code over.
 #include "block_few.h"
 #include "block_tile.h"
 
@@ -70,7 +71,9 @@ __device__ __forceinline__ int wave_scan(int v) {
 // to `size` routes, between half a tile and a whole one, chosen so that the
 // workgroups' longest run of gate/up tiles takes the least loads: `size` token
 // rows and 256 weight rows a step.  (T = 2000 4096x2048 of 16 experts: gate/up
-// 127 us with whole tiles, 123 so, down 76 and 71.)
+// 127 us with whole tiles, 123 so, down 76 and 71.  The products follow a piece's
+// size in steps only: of a tile of 256 tokens the waves of two of the SIMDs hold the
+// first and the third 64, so that from 129 tokens on they make all of theirs.)
 //
 // The other workgroups copy the tokens' scales to bucket positions, a block of H
 // together: of [T, blocks] the tiles would fetch a cache line for each four
@@ -163,9 +166,10 @@ __device__ __forceinline__ Run run_of(const FfnArgs& p, int row_tiles) {
 
 // h of 128 rows of an item's routes, in 8 bits: the rows are one block, whose
 // largest value goes from wave to wave through LDS.  WIDE: products in bf16, which
-// lose no bit; without a plan, where the weights' bytes take longer (T = 4 2048x512
-// of 512 experts 37.9 us, 37.3 in 8 bits, T = 100 2560x640 414 and 411; but T = 4096
-// 2048x512 474 and 433).
+// lose no bit; without a plan, where the weights' bytes mostly take longer (weights
+// from HBM: T = 4 2048x512 of 512 experts 38.2 us, 37.8 in 8 bits, T = 1 23.6 and
+// 21.4, T = 100 2560x640 418 and 414; of 3 experts T = 120 4096x2048 80.6 and 60.8; but
+// T = 4096 2048x512 of 512 477 and 432).
 template <int TT, bool WIDE>
 __global__ __launch_bounds__(kTileThreads, 2) void gate_up_kernel(FfnArgs p, int row_tiles) {
   using T = Tile<TT, true, kTileRows, 1, WIDE>;
@@ -426,9 +430,10 @@ __global__ __launch_bounds__(kFfnThreads) void combine_kernel(FfnArgs p) {
 // turn, all of an expert's reduction at once; the routes' sums meet in LDS, where
 // a token's are added in slot order.  Bound by the weight bytes, and at one
 // workgroup a compute unit by how many of those read: 8 rows, half a product's,
-// where that many workgroups all run at once (T = 4 2048x512 of 512 experts, 40
-// chosen: 11.9 us, 15.6 with 16 rows; 2048x1024 of 64: 10.2 and 12.6; but 2304x512
-// of 256: 18.7 and 13.4).  In a launch of its own the sum took 5 us more.
+// where that many workgroups all run at once (weights in the Infinity Cache: T = 4
+// 2048x512 of 512 experts, 40 chosen, 11.9 us, 15.6 with 16 rows; 2048x1024 of 64
+// 10.2 and 12.6; but 2304x512 of 256 18.7 and 13.4).  In a launch of its own the sum
+// took 5 us more.
 constexpr int kDownWaves = 16;
 constexpr int kDownGroups = 256;             // workgroups that run at once, one on a compute unit
 constexpr int kDownThreads = kDownWaves * kWave;

@@ -66,9 +66,10 @@ __global__ __launch_bounds__(kFewThreads, 2) void linear_few_kernel(LinearArgs p
 }
 
 // Many rows: 64 a workgroup, whose tokens are then read by a quarter as many
-// (T = 16 9999x4096 14.1 us, 17.6 with 16 rows; T = 1 11.9 and 12.7); else as many
-// workgroups as there are (T = 32 4096x4096 10.6 us, 15.9 with 64 rows), the
-// reduction's blocks spread over the waves.
+// (T = 16 9999x4096 14.0 us, 17.4 with 16 rows; T = 1 12.0 and 14.3); else as many
+// workgroups as there are (T = 32 4096x4096 10.8 us, 16.0 with 64 rows), the
+// reduction's blocks spread over the waves.  (Weights from HBM, as in a decode loop
+// over layers; so are the figures below.)
 template <int JT>
 void launch(const LinearArgs& p, hipStream_t s) {
   const int kb = blocks_of(p.K);
@@ -81,8 +82,10 @@ void launch(const LinearArgs& p, hipStream_t s) {
 
 }  // namespace
 
-// Beyond 16 tokens, small weights only: T = 32 2048x2048 5.9 us, 8.2 in tiles of 64 rows;
-// 4096x4096 10.6 and 10.1; 9999x4096 17.4 and 14.9.
+// Beyond 16 tokens, small weights only: T = 32 2048x2048 6.3 us, 7.4 in tiles of 64
+// rows; 4096x4096 10.8 and 10.6; 9999x4096 16.7 and 13.5.  (Up to 16 tokens tiles have
+// not been fitted: 9999x4096 takes 12.0 us here and 11.1 in tiles for one token, 14.0
+// and 11.9 for 16.)
 bool linear_few_ok(int T, int N, int K) { return T <= 16 || (T <= 32 && (long long)N * K <= 1 << 23); }
 
 moe_status linear_few(const LinearArgs& p, hipStream_t s) {
