@@ -92,7 +92,7 @@ def test_expert_codes(T):
     that its codes are known; `down` hands them through."""
     rng = np.random.default_rng(T)
     H = I = 128  # noqa: E741
-    E = 1 if T < 600 else 2                                  # (200 and 600: tiles of 256 and 128 routes)
+    E = 1 if T < 600 else 8                                  # (200 and 600 tokens: tiles of 256 and 128 routes)
     x = np.zeros((T, H))
     x[:, 0] = 1.0
     sx = rng.uniform(0.5, 2.0, (T, 1)).astype(F)
